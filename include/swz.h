@@ -17,7 +17,9 @@
  * into matrix-instruction fragments (swz_stage_operand, and both operands of
  * one GEMM at once: swz_stage_operands) and their consumer
  * (swz_gemm_frag); the GEMM that stages its own operands through swizzled
- * tiles (swz_gemm, swz_gemm_ex for a bf16 result); host-only planning, bank-conflict prediction and layout
+ * tiles (swz_gemm, swz_gemm_ex for a bf16 result); 8-bit floating-point
+ * operands with a scale per block of 128 (swz_quant_f8) and their product
+ * (swz_gemm_f8); host-only planning, bank-conflict prediction and layout
  * algebra (swz_choose, swz_plan, swz_predict_conflicts, swz_kernel_accesses,
  * swz_bank_model_get, swz_fold); and two diagnostics (swz_copy,
  * swz_lds_probe).
@@ -435,6 +437,67 @@ enum swz_c_type { SWZ_C_F32 = 0, SWZ_C_BF16 = 1 };
  * Errors: those of swz_gemm; SWZ_EINVAL for another c_type. */
 int swz_gemm_ex(const void* d_a, const void* d_bt, void* d_c, int64_t m, int64_t n, int64_t k, int32_t layout,
                 const swz_params* p_or_null, int32_t c_type, void* stream);
+
+/* Element types of the operators below. */
+enum swz_x_type { SWZ_X_BF16 = 0, SWZ_X_F16 = 1, SWZ_X_F32 = 2 };
+/* 8-bit floating point: e4m3 (largest value 448, no infinities) and e5m2
+ * (57344, with infinities). */
+enum swz_f8_type { SWZ_F8_E4M3 = 0, SWZ_F8_E5M2 = 1 };
+/* What shares a scale: 128 consecutive elements of a row (the last block of
+ * a row may be shorter), or a square of 128 x 128. */
+enum swz_f8_block { SWZ_BLOCK_1X128 = 0, SWZ_BLOCK_128X128 = 1 };
+/* How scales are stored: fp32, or one byte e + 127 for 2^e (byte 255: NaN). */
+enum swz_scale_type { SWZ_SCALE_F32 = 0, SWZ_SCALE_E8M0 = 1 };
+
+/* A matrix to 8-bit floating point with a power-of-two scale per block, and
+ * on request its transpose, which the gradient products contract over.
+ *   d_x       : x_type [rows][ld_x], ld_x >= cols elements.
+ *   d_q       : 8-bit [rows][ld_q]; columns cols .. ld_q - 1 stay as they were.
+ *   d_scale   : SWZ_BLOCK_1X128   [rows][ceil(cols / 128)],
+ *               SWZ_BLOCK_128X128 [ceil(rows / 128)][ceil(cols / 128)].
+ *   d_qt, d_scale_t : the same of the transposed matrix, [cols][ld_qt] and
+ *               [cols or ceil(cols / 128)][ceil(rows / 128)].  With row blocks
+ *               the transpose is rounded from x with scales of its own.
+ *   Either output pair may be NULL (not both).  ld_q, ld_qt: bytes, multiples
+ *   of 16, as swz_gemm_f8 takes them; d_q and d_qt 16-byte aligned, d_x
+ *   aligned to its element.  Rows of x whose pitch and start are multiples of
+ *   16 bytes, with cols a multiple of 8, move in 16-byte pieces.
+ * With a the largest finite magnitude of a block and F the format's largest
+ * value, the scale is 2^e, e >= -127 the smallest integer with a <= F 2^e
+ * (e = 0 for a block without a finite nonzero element); each element is
+ * x 2^-e rounded to nearest, ties to even.  NaN becomes NaN; infinities stay
+ * infinities in e5m2 and become NaN in e4m3.
+ * Errors: SWZ_EINVAL (sizes, pitches, alignment, NULL, overlap, enum values),
+ * SWZ_EUNSUPPORTED (more than 2^23 tiles of 128 x 128 with a transpose or
+ * square blocks). */
+int swz_quant_f8(const void* d_x, int32_t x_type, int64_t rows, int64_t cols, int64_t ld_x, int32_t f8_type,
+                 int32_t block, int32_t scale_type, void* d_q, void* d_scale, int64_t ld_q, void* d_qt,
+                 void* d_scale_t, int64_t ld_qt, void* stream);
+
+/* C = A B^T of 8-bit operands with a scale per block of 128 along k:
+ *   C[i][j] = sum over blocks b of sA[i][b] sB[j][b] sum over k in b of A[i][k] B[j][k].
+ *   d_a       : a_type [m][lda]; d_b : b_type [n][ldb]; lda, ldb >= k bytes,
+ *               multiples of 16 and below 2^23; bytes behind column k are not
+ *               used, whatever they hold.
+ *   d_scale_a : scale_type, laid out as swz_quant_f8 writes it for a_block;
+ *   d_scale_b : the same for b_block.
+ *   d_c       : float or bf16 (c_type, enum swz_c_type) [m][n], written
+ *               whatever it held (k = 0 writes zeros); must not overlap the
+ *               inputs.
+ * A forward product takes activations in rows (1x128) and weights in squares
+ * (128x128); the data gradient the weight's transpose; the weight gradient
+ * both transposes in rows.  Any m, n, k >= 0: calls with few rows of A (up to
+ * 64) go to kernels that stream B once.  d_a, d_b 16-byte aligned, fp32 scales
+ * 4-byte, d_c aligned to its element; rows of C whose pitch and start are
+ * multiples of 16 bytes are written in 16-byte pieces.
+ * The products are exact in fp32; sums over k are fp32, a bf16 C is rounded
+ * once, to nearest even.  fp32 scales multiply the fp32 sum of their block.
+ * NaN and infinities in the used elements and scales propagate.
+ * Errors: SWZ_EINVAL (sizes, pitches, alignment, NULL, overlap, enum values),
+ * SWZ_EUNSUPPORTED (lda or ldb of 2^23 and more, or over 2^22 tiles of C). */
+int swz_gemm_f8(const void* d_a, const void* d_scale_a, const void* d_b, const void* d_scale_b, void* d_c, int64_t m,
+                int64_t n, int64_t k, int64_t lda, int64_t ldb, int32_t a_type, int32_t b_type, int32_t a_block,
+                int32_t b_block, int32_t scale_type, int32_t c_type, void* stream);
 
 /* Host only.  The swizzle the library uses for a tile of tile_rows x
  * tile_cols elements of elem_bytes, staged by vec_bytes-wide stores and read

@@ -1,0 +1,241 @@
+"""The 8-bit quantizer and product on the GPU against their 64-bit definitions.
+
+The quantizer's one rounding is to the 8-bit grid (its scales are powers of
+two), so its values and scales must be equal, not near.  Products of operands
+made of small whole numbers are exact in fp32 and must be equal too; random
+operands stay within the first-order bound of an fp32 sum
+(oracle.products.product_f8_bound) plus, for a bf16 result, half a step
+(2^-8 of the value).
+"""
+
+import numpy as np
+import pytest
+
+from oracle import products as P
+
+import torch
+
+import tiled_movement_amd as T
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+XT = {"bf16": (torch.bfloat16, T.X_BF16), "fp16": (torch.float16, T.X_F16), "fp32": (torch.float32, T.X_F32)}
+KIND = {"e4m3": T.F8_E4M3, "e5m2": T.F8_E5M2}
+SENTINEL = 0x5A
+
+
+def announce(*what):
+    print("case:", *what, flush=True)
+
+
+def up16(n):
+    return -(-n // 16) * 16
+
+
+def quant(x, kind, square, scale_type, rows=True, transposed=True, ld_x=None, x_type=None, **kw):
+    """Runs the call on x [R][ld_x] with sentinel-filled outputs; returns host bytes and scales."""
+    r = x.shape[0]
+    c = kw.pop("cols", x.shape[1])
+    sdt = torch.uint8 if scale_type == T.SCALE_E8M0 else torch.float32
+    br = 128 if square else 1
+
+    def out(rr, cc):
+        return (torch.full((rr, up16(cc) + 16), SENTINEL, dtype=torch.uint8, device=DEV),
+                torch.full((-(-rr // br), -(-cc // 128)), 7, dtype=sdt, device=DEV))
+
+    q, s = out(r, c) if rows else (None, None)
+    qt, st = out(c, r) if transposed else (None, None)
+    T.swz_quant_f8(x, q, s, r, c, x_type=x_type, f8_type=KIND[kind], block=T.BLOCK_128X128 if square else T.BLOCK_1X128,
+                   scale_type=scale_type, ld_x=ld_x, ld_q=up16(c) + 16, qt=qt, scale_t=st, ld_qt=up16(r) + 16, **kw)
+    torch.cuda.synchronize()
+    return [None if t is None else t.cpu().numpy() for t in (q, s, qt, st)]
+
+
+def check_quant(q, s, x, kind, square):
+    ref, ex = P.quantize(x, kind, 128 if square else 1)
+    got = P.f8_decode(q[:, :x.shape[1]], kind)
+    assert np.array_equal(got, ref, equal_nan=True)
+    if s.dtype == np.uint8:
+        assert np.array_equal(s, ex + 127)
+    else:
+        assert np.array_equal(s.astype(np.float64), 2.0 ** ex)
+    assert np.all(q[:, x.shape[1]:] == SENTINEL)  # the pitch's padding is left alone
+
+
+def values(r, c, seed, spread=1.5):
+    rng = np.random.default_rng(seed)
+    return rng.standard_normal((r, c)) * np.exp(spread * rng.standard_normal((r, 1))) * np.exp(spread * rng.standard_normal((1, c)))
+
+
+@pytest.mark.parametrize("xt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("square", [False, True])
+@pytest.mark.parametrize("r,c", [(1, 8), (1, 1), (3, 129), (130, 256), (128, 128), (257, 120), (65, 391)])
+def test_quant_equals_definition(xt, kind, square, r, c):
+    announce("quant", xt, kind, square, r, c)
+    dt, code = XT[xt]
+    x = torch.from_numpy(values(r, c, r * 1000 + c)).to(dt)
+    xf = x.double().numpy()
+    q, s, qt, st = quant(x.to(DEV), kind, square, T.SCALE_E8M0, x_type=code)
+    check_quant(q, s, xf, kind, square)
+    check_quant(qt, st, np.ascontiguousarray(xf.T), kind, square)
+    # one output at a time, fp32 scales
+    q, s, _, _ = quant(x.to(DEV), kind, square, T.SCALE_F32, transposed=False, x_type=code)
+    check_quant(q, s, xf, kind, square)
+    _, _, qt, st = quant(x.to(DEV), kind, square, T.SCALE_F32, rows=False, x_type=code)
+    check_quant(qt, st, np.ascontiguousarray(xf.T), kind, square)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+def test_every_rounding_and_tie(kind):
+    """Every bf16 significand at every distance from the block's largest value."""
+    announce("quant ties", kind)
+    m = np.arange(128, 256) / 128.0
+    rows = []
+    for d in range(0, 24):
+        rows.append(np.concatenate([[1.75], (m * 2.0 ** -d)[:127]]))
+        rows.append(np.concatenate([[-1.0], -(m * 2.0 ** -d)[1:]]) if d else np.concatenate([[-1.9921875], -m[:127]]))
+    x = np.stack(rows)
+    t = torch.from_numpy(x).to(torch.bfloat16)
+    assert np.array_equal(t.double().numpy(), x)
+    q, s, qt, st = quant(t.to(DEV), kind, False, T.SCALE_E8M0, x_type=T.X_BF16)
+    check_quant(q, s, x, kind, False)
+    check_quant(qt, st, np.ascontiguousarray(x.T), kind, False)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("square", [False, True])
+def test_special_values(kind, square):
+    announce("quant special", kind, square)
+    x = values(140, 260, 3).astype(np.float32)
+    x[0, :] = 0
+    x[1, 5], x[2, 7], x[3, 130] = np.inf, -np.inf, np.nan
+    x[4, :] = np.nan
+    x[5, :128] = np.inf
+    x[6, :] = 1e-42  # subnormal
+    x[7, 3] = 3.4e38
+    x[8, :] = -0.0
+    x[9, :128] = 448.0
+    x[9, 128:] = np.nextafter(np.float32(448.0), np.float32(1e9))
+    q, s, qt, st = quant(torch.from_numpy(x).to(DEV), kind, square, T.SCALE_E8M0, x_type=T.X_F32)
+    check_quant(q, s, x.astype(np.float64), kind, square)
+    check_quant(qt, st, np.ascontiguousarray(x.T.astype(np.float64)), kind, square)
+
+
+@pytest.mark.parametrize("off,ld", [(0, 264), (1, 264), (0, 261), (4, 300)])
+def test_quant_pitched_and_unaligned_input(off, ld):
+    announce("quant pitch", off, ld)
+    buf = torch.from_numpy(values(1, 70 * 300 + 8, 9)[0]).to(torch.bfloat16)
+    x = buf[off:off + 70 * ld].view(70, ld)
+    dev = buf.to(DEV)[off:off + 70 * ld]
+    q, s, qt, st = quant(dev.view(70, ld), "e4m3", False, T.SCALE_E8M0, ld_x=ld, x_type=T.X_BF16, cols=256)
+    xf = x[:, :256].double().numpy()
+    check_quant(q, s, xf, "e4m3", False)
+    check_quant(qt, st, np.ascontiguousarray(xf.T), "e4m3", False)
+
+
+# ------------------------------------------------------------------ product
+def operand(r, k, kind, square, scale_type, seed, exact=False):
+    """(device bytes [r][ld], device scales, float64 values); bytes behind k are NaN bytes."""
+    rng = np.random.default_rng(seed)
+    ld = up16(k) + 16
+    if exact:
+        v = rng.integers(-3, 4, size=(r, k)).astype(np.float64)
+        t = torch.from_numpy(v)
+    else:
+        t = torch.from_numpy(rng.standard_normal((r, k)) * 8)
+    f8 = torch.float8_e4m3fn if kind == "e4m3" else torch.float8_e5m2
+    bits = t.to(f8).view(torch.uint8).numpy()
+    data = np.full((r, ld), 0x7F, dtype=np.uint8)
+    data[:, :k] = bits
+    shape = (-(-r // 128) if square else r, -(-k // 128))
+    if scale_type == T.SCALE_E8M0:
+        s = rng.integers(124, 131, size=shape).astype(np.uint8)
+    elif exact:
+        s = 2.0 ** rng.integers(-3, 4, size=shape).astype(np.float32)
+    else:
+        s = np.exp(rng.standard_normal(shape)).astype(np.float32)
+    val = P.dequantize(bits, kind, s, square)
+    return torch.from_numpy(data).to(DEV), torch.from_numpy(s).to(DEV), val
+
+
+def gemm(a, b, m, n, k, ak, bk, sqa, sqb, scale_type, c_type, pad=0):
+    dt = torch.float32 if c_type == T.C_F32 else torch.bfloat16
+    c = torch.full((m * n + 2 * pad,), float("nan"), dtype=dt, device=DEV)
+    out = c[pad:pad + m * n]
+    T.swz_gemm_f8(a[0], a[1], b[0], b[1], out, m, n, k, lda=a[0].shape[1], ldb=b[0].shape[1], a_type=KIND[ak],
+                  b_type=KIND[bk], a_block=int(sqa), b_block=int(sqb), scale_type=scale_type, c_type=c_type)
+    torch.cuda.synchronize()
+    full = c.double().cpu().numpy()
+    assert np.all(np.isnan(full[:pad])) and np.all(np.isnan(full[pad + m * n:]))
+    return full[pad:pad + m * n].reshape(m, n)
+
+
+SHAPES = [(1, 1, 1), (1, 300, 128), (3, 17, 1000), (16, 256, 256), (17, 130, 384), (33, 640, 520), (64, 100, 640),
+          (65, 257, 129), (130, 48, 4111), (256, 256, 128), (300, 521, 272), (513, 260, 1024)]
+
+
+@pytest.mark.parametrize("scale_type,sqa,sqb", [(T.SCALE_E8M0, False, True), (T.SCALE_E8M0, False, False),
+                                                (T.SCALE_E8M0, True, True), (T.SCALE_F32, False, True),
+                                                (T.SCALE_F32, False, False), (T.SCALE_F32, True, False)])
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_gemm_whole_numbers_equal(m, n, k, scale_type, sqa, sqb):
+    announce("gemm exact", m, n, k, scale_type, sqa, sqb)
+    a = operand(m, k, "e4m3", sqa, scale_type, m + k, exact=True)
+    b = operand(n, k, "e4m3", sqb, scale_type, n + 2 * k, exact=True)
+    got = gemm(a, b, m, n, k, "e4m3", "e4m3", sqa, sqb, scale_type, T.C_F32, pad=4)
+    # sums of multiples of 2^-6 below 2^17: exact in fp32
+    assert np.array_equal(got, P.product_f8(a[2], b[2]))
+
+
+@pytest.mark.parametrize("ak,bk", [("e4m3", "e4m3"), ("e5m2", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("scale_type,sqb", [(T.SCALE_E8M0, True), (T.SCALE_E8M0, False), (T.SCALE_F32, True),
+                                            (T.SCALE_F32, False)])
+@pytest.mark.parametrize("m,n,k", [(5, 260, 1000), (40, 200, 700), (300, 264, 1032)])
+@pytest.mark.parametrize("c_type", [T.C_F32, T.C_BF16])
+def test_gemm_random_within_bound(ak, bk, scale_type, sqb, m, n, k, c_type):
+    announce("gemm random", ak, bk, scale_type, sqb, m, n, k, c_type)
+    a = operand(m, k, ak, False, scale_type, 1)
+    b = operand(n, k, bk, sqb, scale_type, 2)
+    got = gemm(a, b, m, n, k, ak, bk, False, sqb, scale_type, c_type)
+    ref, bound = P.product_f8(a[2], b[2]), P.product_f8_bound(a[2], b[2])
+    if c_type == T.C_BF16:
+        bound = bound + 2.0 ** -8 * (np.abs(ref) + bound)
+    assert np.all(np.abs(got - ref) <= bound)
+
+
+@pytest.mark.parametrize("pad,n", [(1, 256), (0, 257), (3, 129), (2, 320)])
+@pytest.mark.parametrize("m", [2, 70])
+def test_gemm_unaligned_result(pad, n, m):
+    announce("gemm unaligned", pad, n, m)
+    a = operand(m, 256, "e4m3", False, T.SCALE_E8M0, 5, exact=True)
+    b = operand(n, 256, "e4m3", True, T.SCALE_E8M0, 6, exact=True)
+    ref = P.product_f8(a[2], b[2])
+    got = gemm(a, b, m, n, 256, "e4m3", "e4m3", False, True, T.SCALE_E8M0, T.C_F32, pad)
+    assert np.array_equal(got, ref)
+    got = gemm(a, b, m, n, 256, "e4m3", "e4m3", False, True, T.SCALE_E8M0, T.C_BF16, pad)
+    assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref))
+
+
+@pytest.mark.parametrize("m", [1, 20, 100])
+def test_gemm_empty_k_writes_zeros(m):
+    announce("gemm k=0", m)
+    z = torch.zeros(1, dtype=torch.uint8, device=DEV)
+    c = torch.full((m, 33), float("nan"), dtype=torch.float32, device=DEV)
+    T.swz_gemm_f8(z, z, z, z, c, m, 33, 0, lda=0, ldb=0, c_type=T.C_F32)
+    torch.cuda.synchronize()
+    assert torch.all(c == 0)
+
+
+@pytest.mark.parametrize("m", [4, 90])
+def test_gemm_nan_stays_in_its_row_and_column(m):
+    announce("gemm nan", m)
+    a = operand(m, 200, "e4m3", False, T.SCALE_E8M0, 8, exact=True)
+    b = operand(140, 200, "e4m3", True, T.SCALE_E8M0, 9, exact=True)
+    a[0][2, 150] = 0x7F
+    b[0][7, 3] = 0xFF
+    ref = P.product_f8(a[2], b[2])
+    ref[2, :] = np.nan
+    ref[:, 7] = np.nan
+    got = gemm(a, b, m, 140, 200, "e4m3", "e4m3", False, True, T.SCALE_E8M0, T.C_F32)
+    assert np.array_equal(got, ref, equal_nan=True)

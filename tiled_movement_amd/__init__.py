@@ -33,6 +33,10 @@ ORDER_DIAGONAL, ORDER_HALF_DIAGONAL, ORDER_COLUMNS, ORDER_STEEP_DIAGONAL = 0, 1,
 ORDER_SLOPE_8, ORDER_SLOPE_16, ORDER_SLOPE_32 = 4, 5, 6
 ORDERS = tuple(range(7))
 C_F32, C_BF16 = 0, 1
+X_BF16, X_F16, X_F32 = 0, 1, 2
+F8_E4M3, F8_E5M2 = 0, 1
+BLOCK_1X128, BLOCK_128X128 = 0, 1
+SCALE_F32, SCALE_E8M0 = 0, 1
 LAYOUTS = {"swizzle": LAYOUT_SWIZZLE, "pad": LAYOUT_PAD, "plain": LAYOUT_PLAIN, "direct": LAYOUT_SWIZZLE_DIRECT}
 
 EXPORTS = (
@@ -48,6 +52,8 @@ EXPORTS = (
     "swz_gemm_frag",
     "swz_gemm",
     "swz_gemm_ex",
+    "swz_quant_f8",
+    "swz_gemm_f8",
     "swz_fold",
     "swz_choose",
     "swz_predict_conflicts",
@@ -147,6 +153,8 @@ def _load() -> ctypes.CDLL:
     lib.swz_strerror.restype = ctypes.c_char_p
     lib.swz_copy.argtypes = [vp, vp, i64, vp]
     lib.swz_lds_probe.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp]
+    lib.swz_quant_f8.argtypes = [vp, i32, i64, i64, i64, i32, i32, i32, vp, vp, i64, vp, vp, i64, vp]
+    lib.swz_gemm_f8.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i32, i32, i32, i32, i32, i32, vp]
     for name in EXPORTS:
         if name != "swz_strerror":
             getattr(lib, name).restype = ctypes.c_int
@@ -318,6 +326,38 @@ def swz_gemm_ex(a, bt, c, m: int, n: int, k: int, layout: str = "swizzle", param
     _buf("swz_gemm_ex", a=(a, 2 * m * k), bt=(bt, 2 * n * k), c=(c, (2 if c_type == C_BF16 else 4) * m * n))
     _check(lib.swz_gemm_ex(_ptr(a), _ptr(bt), _ptr(c), m, n, k, _layout(layout), _params(params), c_type,
                            _stream(stream, a, bt, c)), "swz_gemm_ex")
+
+
+def _f8_scale_bytes(rows: int, cols: int, block: int, scale_type: int) -> int:
+    return (-(-rows // 128) if block == BLOCK_128X128 else rows) * -(-cols // 128) * (1 if scale_type == SCALE_E8M0 else 4)
+
+
+def swz_quant_f8(x, q, scale, rows: int, cols: int, x_type: int = X_BF16, f8_type: int = F8_E4M3,
+                 block: int = BLOCK_1X128, scale_type: int = SCALE_E8M0, ld_x: Optional[int] = None,
+                 ld_q: Optional[int] = None, qt=None, scale_t=None, ld_qt: Optional[int] = None, stream=None) -> None:
+    """x [rows][cols] to 8-bit values q with power-of-two scales, and its transpose qt [cols][rows].
+
+    Pitches default to tight rows (ld_x) and to tight rows rounded up to 16 bytes (ld_q, ld_qt)."""
+    ld_x = cols if ld_x is None else ld_x
+    ld_q = -(-cols // 16) * 16 if ld_q is None else ld_q
+    ld_qt = -(-rows // 16) * 16 if ld_qt is None else ld_qt
+    _buf("swz_quant_f8", x=(x, rows * ld_x * (4 if x_type == X_F32 else 2)), q=(q, rows * ld_q),
+         scale=(scale, _f8_scale_bytes(rows, cols, block, scale_type)), qt=(qt, cols * ld_qt),
+         scale_t=(scale_t, _f8_scale_bytes(cols, rows, block, scale_type)))
+    _check(lib.swz_quant_f8(_ptr(x), x_type, rows, cols, ld_x, f8_type, block, scale_type, _ptr(q), _ptr(scale), ld_q,
+                            _ptr(qt), _ptr(scale_t), ld_qt, _stream(stream, x, q, qt)), "swz_quant_f8")
+
+
+def swz_gemm_f8(a, scale_a, b, scale_b, c, m: int, n: int, k: int, lda: Optional[int] = None,
+                ldb: Optional[int] = None, a_type: int = F8_E4M3, b_type: int = F8_E4M3, a_block: int = BLOCK_1X128,
+                b_block: int = BLOCK_128X128, scale_type: int = SCALE_E8M0, c_type: int = C_BF16, stream=None) -> None:
+    """C [m][n] = A B^T of 8-bit operands with scales (pitches default to k rounded up to 16 bytes)."""
+    lda = -(-k // 16) * 16 if lda is None else lda
+    ldb = -(-k // 16) * 16 if ldb is None else ldb
+    _buf("swz_gemm_f8", a=(a, m * lda), scale_a=(scale_a, _f8_scale_bytes(m, k, a_block, scale_type)), b=(b, n * ldb),
+         scale_b=(scale_b, _f8_scale_bytes(n, k, b_block, scale_type)), c=(c, (2 if c_type == C_BF16 else 4) * m * n))
+    _check(lib.swz_gemm_f8(_ptr(a), _ptr(scale_a), _ptr(b), _ptr(scale_b), _ptr(c), m, n, k, lda, ldb, a_type, b_type,
+                           a_block, b_block, scale_type, c_type, _stream(stream, a, b, c)), "swz_gemm_f8")
 
 
 def swz_fold(params, base: int, active: int):

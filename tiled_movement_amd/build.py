@@ -27,6 +27,8 @@ SOURCES = [
     "kernels_tile.hip",
     "kernels_gemm.hip",
     "kernels_gemm_tiles.hip",
+    "kernels_gemm_f8.hip",
+    "kernels_quant.hip",
     "kernels_map.hip",
     "kernels_rows.hip",
     "kernels_copy.hip",
@@ -52,8 +54,8 @@ def flags():
         "-fvisibility=hidden",
         "-Wall",
         "-Wno-unused-function",
-        # Packed fp32 VALU ops stay off: the path has no float arithmetic,
-        # and the compiler must not introduce them.
+        # Packed fp32 VALU ops stay off: the compiler must not form them from
+        # the float arithmetic of the quantizer and the products.
         "-Xclang",
         "-target-feature",
         "-Xclang",

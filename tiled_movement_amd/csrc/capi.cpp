@@ -32,6 +32,18 @@ bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
 // unsigned, so that a huge n wraps instead of overflowing (16 divides 2^64).
 bool pitch16(int64_t n, int32_t esz) { return (static_cast<uint64_t>(n) * static_cast<uint64_t>(esz)) % 16 == 0; }
 
+// Row pitches of the products' operands stay below this many bytes, so that
+// the rows of a tile lie within 31-bit offsets (mma_core.h).
+constexpr int64_t kMaxPitch = int64_t(1) << 23;
+
+// Bytes of an 8-bit operand [rows][ld] and of its scales.
+bool f8_operand_bytes(int64_t rows, int64_t cols, int64_t ld, bool square, int32_t scale_type, int64_t* data,
+                      int64_t* scales) {
+    int64_t n;
+    const int64_t srows = square ? rows / 128 + (rows % 128 != 0) : rows, scols = cols / 128 + (cols % 128 != 0);
+    return mul_ok(rows, ld, data) && mul_ok(srows, scols, &n) && mul_ok(n, scale_type == SWZ_SCALE_F32 ? 4 : 1, scales);
+}
+
 int ilog2(int64_t v) {
     int r = -1;
     while (v > 0) {
@@ -537,6 +549,84 @@ SWZ_API int swz_gemm_ex(const void* d_a, const void* d_bt, void* d_c, int64_t m,
 SWZ_API int swz_gemm(const void* d_a, const void* d_bt, float* d_c, int64_t m, int64_t n, int64_t k, int32_t layout,
                      const swz_params* p_or_null, void* stream) {
     return swz_gemm_ex(d_a, d_bt, d_c, m, n, k, layout, p_or_null, SWZ_C_F32, stream);
+}
+
+SWZ_API int swz_quant_f8(const void* d_x, int32_t x_type, int64_t rows, int64_t cols, int64_t ld_x, int32_t f8_type,
+                         int32_t block, int32_t scale_type, void* d_q, void* d_scale, int64_t ld_q, void* d_qt,
+                         void* d_scale_t, int64_t ld_qt, void* stream) {
+    if (x_type != SWZ_X_BF16 && x_type != SWZ_X_F16 && x_type != SWZ_X_F32) return SWZ_EINVAL;
+    if (f8_type != SWZ_F8_E4M3 && f8_type != SWZ_F8_E5M2) return SWZ_EINVAL;
+    if (block != SWZ_BLOCK_1X128 && block != SWZ_BLOCK_128X128) return SWZ_EINVAL;
+    if (scale_type != SWZ_SCALE_F32 && scale_type != SWZ_SCALE_E8M0) return SWZ_EINVAL;
+    if (rows < 0 || cols < 0 || ld_x < cols) return SWZ_EINVAL;
+    if (!d_q && !d_qt) return SWZ_EINVAL;
+    const int64_t esz = x_type == SWZ_X_F32 ? 4 : 2;
+    const bool square = block == SWZ_BLOCK_128X128;
+    int64_t n, x_bytes, q_bytes = 0, s_bytes = 0, qt_bytes = 0, st_bytes = 0;
+    if (!mul_ok(rows, ld_x, &n) || !mul_ok(n, esz, &x_bytes)) return SWZ_EINVAL;
+    if (d_q) {
+        if (!d_scale || ld_q < cols || ld_q % 16 || !f8_operand_bytes(rows, cols, ld_q, square, scale_type, &q_bytes, &s_bytes))
+            return SWZ_EINVAL;
+        if (reinterpret_cast<uintptr_t>(d_q) % 16) return SWZ_EINVAL;
+    }
+    if (d_qt) {
+        if (!d_scale_t || ld_qt < rows || ld_qt % 16 ||
+            !f8_operand_bytes(cols, rows, ld_qt, square, scale_type, &qt_bytes, &st_bytes))
+            return SWZ_EINVAL;
+        if (reinterpret_cast<uintptr_t>(d_qt) % 16) return SWZ_EINVAL;
+    }
+    if (rows == 0 || cols == 0) return SWZ_OK;
+    if (!d_x || reinterpret_cast<uintptr_t>(d_x) % static_cast<uintptr_t>(esz)) return SWZ_EINVAL;
+    const uintptr_t sal = scale_type == SWZ_SCALE_F32 ? 4 : 1;
+    const void* buf[5] = {d_x, d_q, d_q ? d_scale : nullptr, d_qt, d_qt ? d_scale_t : nullptr};
+    const int64_t bytes[5] = {x_bytes, q_bytes, s_bytes, qt_bytes, st_bytes};
+    for (int i = 0; i < 5; ++i) {
+        if (!buf[i]) continue;
+        if ((i == 2 || i == 4) && reinterpret_cast<uintptr_t>(buf[i]) % sal) return SWZ_EINVAL;
+        for (int j = 0; j < i; ++j)
+            if (buf[j] && overlaps(buf[i], bytes[i], buf[j], bytes[j])) return SWZ_EINVAL;
+    }
+    const int64_t tr = (rows - 1) / 128 + 1, tc = (cols - 1) / 128 + 1;
+    if ((d_qt || square) && tr > (int64_t(1) << 23) / tc) return SWZ_EUNSUPPORTED;
+    const swz::QuantJob job{d_x,   x_type,  rows, cols,      ld_x, f8_type == SWZ_F8_E5M2, square, scale_type == SWZ_SCALE_F32,
+                            d_q,   d_scale, ld_q, d_qt, d_scale_t, ld_qt};
+    return hip_status(swz::launch_quant(job, static_cast<hipStream_t>(stream)));
+}
+
+SWZ_API int swz_gemm_f8(const void* d_a, const void* d_scale_a, const void* d_b, const void* d_scale_b, void* d_c,
+                        int64_t m, int64_t n, int64_t k, int64_t lda, int64_t ldb, int32_t a_type, int32_t b_type,
+                        int32_t a_block, int32_t b_block, int32_t scale_type, int32_t c_type, void* stream) {
+    for (const int32_t t : {a_type, b_type})
+        if (t != SWZ_F8_E4M3 && t != SWZ_F8_E5M2) return SWZ_EINVAL;
+    for (const int32_t b : {a_block, b_block})
+        if (b != SWZ_BLOCK_1X128 && b != SWZ_BLOCK_128X128) return SWZ_EINVAL;
+    if (scale_type != SWZ_SCALE_F32 && scale_type != SWZ_SCALE_E8M0) return SWZ_EINVAL;
+    if (c_type != SWZ_C_F32 && c_type != SWZ_C_BF16) return SWZ_EINVAL;
+    if (m < 0 || n < 0 || k < 0 || lda < k || ldb < k || lda % 16 || ldb % 16) return SWZ_EINVAL;
+    const bool sqa = a_block == SWZ_BLOCK_128X128, sqb = b_block == SWZ_BLOCK_128X128;
+    const int64_t esz = c_type == SWZ_C_BF16 ? 2 : 4;
+    int64_t a_bytes, sa_bytes, b_bytes, sb_bytes, c_elems, c_bytes;
+    if (!f8_operand_bytes(m, k, lda, sqa, scale_type, &a_bytes, &sa_bytes) ||
+        !f8_operand_bytes(n, k, ldb, sqb, scale_type, &b_bytes, &sb_bytes) || !mul_ok(m, n, &c_elems) ||
+        !mul_ok(c_elems, esz, &c_bytes))
+        return SWZ_EINVAL;
+    if (m == 0 || n == 0) return SWZ_OK;
+    if (!d_c || reinterpret_cast<uintptr_t>(d_c) % static_cast<uintptr_t>(esz)) return SWZ_EINVAL;
+    if (k > 0) {
+        if (!d_a || !d_b || !d_scale_a || !d_scale_b) return SWZ_EINVAL;
+        if (reinterpret_cast<uintptr_t>(d_a) % 16 || reinterpret_cast<uintptr_t>(d_b) % 16) return SWZ_EINVAL;
+        if (scale_type == SWZ_SCALE_F32 &&
+            (reinterpret_cast<uintptr_t>(d_scale_a) % 4 || reinterpret_cast<uintptr_t>(d_scale_b) % 4))
+            return SWZ_EINVAL;
+        if (overlaps(d_c, c_bytes, d_a, a_bytes) || overlaps(d_c, c_bytes, d_b, b_bytes) ||
+            overlaps(d_c, c_bytes, d_scale_a, sa_bytes) || overlaps(d_c, c_bytes, d_scale_b, sb_bytes))
+            return SWZ_EINVAL;
+    }
+    if (lda >= kMaxPitch || ldb >= kMaxPitch) return SWZ_EUNSUPPORTED;
+    if ((m - 1) / 16 + 1 > (int64_t(1) << 30) / ((n - 1) / 16 + 1)) return SWZ_EUNSUPPORTED;
+    const swz::GemmF8Job job{d_a, d_scale_a, d_b, d_scale_b, d_c, m, n, k, lda, ldb, a_type == SWZ_F8_E5M2,
+                             b_type == SWZ_F8_E5M2, sqa, sqb, scale_type == SWZ_SCALE_E8M0, c_type == SWZ_C_BF16};
+    return hip_status(swz::launch_gemm_f8(job, static_cast<hipStream_t>(stream)));
 }
 
 SWZ_API int swz_fold(const swz_params* p, uint32_t base, uint32_t active, uint32_t* collision,

@@ -1,0 +1,61 @@
+// C = A B^T of 8-bit floating-point operands with a scale per block of 128
+// along k, K-contiguous on both sides:
+//   C[i][j] = sum_b sA[i][b] sB[j][b] sum_{k in block b} A[i][k] B[j][k].
+// A stage of the core (mma_core.h) is one block of 128, so the scales change
+// exactly from stage to stage.
+#include "launch.h"
+#include "mma_core.h"
+
+namespace swz {
+namespace {
+
+using namespace mma;
+
+template <class C>
+__global__ __launch_bounds__(C::NT) void k_gemm_f8(Operand A, Operand B, void* __restrict__ c, int64_t ldc, int64_t k,
+                                                   uint32_t tiles_m, int bf16c, int vec) {
+    __shared__ i32x4 lds_v[C::kLds / 16];
+    lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x % tiles_m) * C::TL;
+    const int64_t j0 = static_cast<int64_t>(blockIdx.x / tiles_m) * C::TR;
+    f32x4 acc[C::BL][C::BR];
+    tile_product<C>(acc, A, B, i0, j0, k, lds);
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    lds_f32* slice = (lds_f32*)(lds + wave * C::kSlice);
+    const int64_t wi = i0 + wave / C::WR * C::BL * 16, wj = j0 + wave % C::WR * C::BR * 16;
+    auto same = [](float v) { return v; };
+    if (bf16c)
+        store_tile<C>(acc, slice, static_cast<__bf16*>(c), ldc, wi, wj, A.rows, B.rows, vec, lane, same);
+    else
+        store_tile<C>(acc, slice, static_cast<float*>(c), ldc, wi, wj, A.rows, B.rows, vec, lane, same);
+}
+
+template <int LT, int RT, int SC>
+hipError_t launch_typed(const GemmF8Job& j, hipStream_t stream) {
+    using C = Config<kF8, LT, RT, SC, 4, 2, 4, 8>;
+    const Operand A{static_cast<const uint8_t*>(j.a), j.lda, j.m, j.scale_a, (j.k + 127) / 128, j.a_square ? 7 : 0};
+    const Operand B{static_cast<const uint8_t*>(j.b), j.ldb, j.n, j.scale_b, (j.k + 127) / 128, j.b_square ? 7 : 0};
+    const int64_t tm = (j.m + C::TL - 1) / C::TL, tn = (j.n + C::TR - 1) / C::TR;
+    if (tm > 0x7fffffff / C::NT / tn) return hipErrorInvalidValue;
+    const int esz = j.bf16c ? 2 : 4;
+    const int vec = j.n * esz % 16 == 0 && reinterpret_cast<uintptr_t>(j.c) % 16 == 0;
+    hipLaunchKernelGGL(k_gemm_f8<C>, dim3(static_cast<unsigned>(tm * tn)), dim3(C::NT), 0, stream, A, B, j.c, j.n, j.k,
+                       static_cast<uint32_t>(tm), j.bf16c ? 1 : 0, vec);
+    return hipGetLastError();
+}
+
+template <int SC>
+hipError_t launch_scaled(const GemmF8Job& j, hipStream_t stream) {
+    if (j.a_e5m2) return j.b_e5m2 ? launch_typed<1, 1, SC>(j, stream) : launch_typed<1, 0, SC>(j, stream);
+    return j.b_e5m2 ? launch_typed<0, 1, SC>(j, stream) : launch_typed<0, 0, SC>(j, stream);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_f8(const GemmF8Job& j, hipStream_t stream) {
+    if (j.m == 0 || j.n == 0) return hipSuccess;
+    if (j.e8m0) return launch_scaled<kE8M0>(j, stream);
+    return j.b_square ? launch_scaled<kF32Square>(j, stream) : launch_scaled<kF32Rows>(j, stream);
+}
+
+}  // namespace swz

@@ -55,6 +55,30 @@ hipError_t launch_gemm_frag(const void* fa, const void* fb, float* c, int64_t m,
                             hipStream_t stream);
 hipError_t launch_gemm_tiles(const void* a, const void* bt, void* c, int64_t m, int64_t n, int64_t k,
                              const LdsLayout& layout, bool bf16c, hipStream_t stream);
+
+// swz_quant_f8: x to 8-bit values with power-of-two scales, and its transpose.
+struct QuantJob {
+    const void* x;
+    int32_t x_type;  // enum swz_x_type
+    int64_t rows, cols, ldx;
+    bool e5m2, square, f32_scale;
+    void* q;
+    void* scale;
+    int64_t ldq;
+    void* qt;
+    void* scale_t;
+    int64_t ldqt;
+};
+hipError_t launch_quant(const QuantJob& job, hipStream_t stream);
+
+// swz_gemm_f8: C [m][n] = A B^T of 8-bit operands with scales.
+struct GemmF8Job {
+    const void *a, *scale_a, *b, *scale_b;
+    void* c;
+    int64_t m, n, k, lda, ldb;
+    bool a_e5m2, b_e5m2, a_square, b_square, e8m0, bf16c;
+};
+hipError_t launch_gemm_f8(const GemmF8Job& job, hipStream_t stream);
 hipError_t launch_map(const int32_t* in, int32_t* out, int64_t n, swz_params p, hipStream_t stream);
 
 // Up to kMapBatch triples of one batched-map launch, passed by value.

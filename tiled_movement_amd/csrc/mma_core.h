@@ -1,0 +1,406 @@
+// Core of the products of K-contiguous operands: C[i][j] = sum_k L[i][k] R[j][k]
+// with both operands staged through swizzled LDS tiles of 128-byte rows, 64
+// two-byte or 128 one-byte values of k per stage.
+//
+// A workgroup of WL x WR waves owns a TL x TR tile of C.  Per stage it brings
+// TL rows of L and TR rows of R, 128 bytes each, into LDS with direct
+// HBM -> LDS loads of 16 bytes per lane.  16-byte slot p = 8 row + chunk of a
+// tile holds the tile element of slot swizzle(p), Swizzle<3,0,4> on slots
+// (Swizzle<3,3,4> on two-byte elements): the row's bits 1..3 are XORed into
+// its chunk, so the 16 rows that one fragment read touches in the same chunk
+// fall on 16 different 16-byte groups of the 64 banks (0 predicted and
+// measured conflict cycles; plain rows: 96 per 256 x 64 tile read).  Bits 4 and
+// up of the row stay out of the swizzle, so a lane's fragment addresses
+// differ by constants only and fold into the read instructions' offsets.
+//
+// Fragments: lane l reads row l%16 of a 16-row block, chunks l/16 and
+// l/16 + 4.  For the 16x16x32 two-byte instructions these are the two k steps
+// of the stage; for the 16x16x128 one-byte instruction they are the lane's 32
+// values of k.  That is not the instruction's own k order, but a sum over k
+// only asks that both operands use the same one, and the block of 128 shares
+// its scale.
+//
+// The R operand feeds the instruction's rows and L its columns, so lane l of
+// the wave holds four consecutive j (4*(l/16) .. +3 of a block) of one i
+// (l%16): results leave in runs along j, sums over j are sums within a lane
+// before they are sums over lanes, and an L row's scale is one number a lane.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace swz {
+namespace mma {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) float lds_f32;
+typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+typedef __attribute__((address_space(3))) uint32_t lds_u32;
+typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
+
+enum Elem { kBf16, kF16, kF8 };
+// Scales of one-byte operands, one per row (or 128 rows) and stage: none;
+// powers of two as exponent bytes, applied by the matrix instruction; fp32,
+// applied to the stage's product (kF32Square: R's scale is the same for all
+// rows of a wave, so only L's varies within a register block).
+enum Scale { kNoScale, kE8M0, kF32Rows, kF32Square };
+
+struct Operand {
+    const uint8_t* data;  // [rows][ld] bytes
+    int64_t ld;           // row pitch in bytes, a multiple of 16, below kMaxLd
+    int64_t rows;
+    const void* scale;    // [rows >> scale_shift][scale_ld]
+    int64_t scale_ld;
+    int scale_shift;      // 0: a scale per row, 7: per 128 rows
+};
+// 256 rows of this pitch stay within 31-bit offsets from a tile's first row.
+constexpr int64_t kMaxLd = int64_t(1) << 23;
+
+template <int ELEM_, int LT_, int RT_, int SC_, int WL_, int WR_, int BL_, int BR_>
+struct Config {
+    static constexpr int ELEM = ELEM_, LT = LT_, RT = RT_, SC = SC_;
+    static constexpr int WL = WL_, WR = WR_, BL = BL_, BR = BR_;  // waves; blocks of 16 rows per wave
+    static constexpr int NT = 64 * WL * WR;
+    static constexpr int TL = 16 * WL * BL, TR = 16 * WR * BR;
+    static constexpr int kBuf = (TL + TR) * 128;
+    static constexpr int kScaleBuf = SC == kNoScale ? 0 : SC == kE8M0 ? (TL + TR + 63) / 64 * 64 : (TL + TR) * 4;
+    static constexpr int kMain = 2 * (kBuf + kScaleBuf);
+    // a wave's slice of the epilogue: 16 rows of C, padded by 16 bytes
+    static constexpr int kPitch = 16 * BR + 4;
+    static constexpr int kSlice = 16 * kPitch * 4;
+    static constexpr int kLds = kMain > WL * WR * kSlice ? kMain : WL * WR * kSlice;
+    static constexpr int NS = (TL + TR + NT - 1) / NT;  // scales a thread stages
+    static_assert(TL * 8 % NT == 0 && TR * 8 % NT == 0 && NT % 128 == 0, "the fills split evenly");
+    static_assert(kLds <= 160 * 1024, "the stages fit in LDS");
+};
+
+__device__ __forceinline__ void wg_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// 16-byte slot of a tile that holds tile slot p, and the reverse.
+__device__ __forceinline__ uint32_t swz_slot(uint32_t p) { return p ^ ((p >> 4) & 7u); }
+
+// This thread's part of the fills of one operand's tile: slots t + NT q.
+// swizzle(t + NT q) = swizzle(t) + NT q (NT is a multiple of 128), so the
+// chunk is the same for all q and the row moves by NT / 8.  Rows behind the
+// operand's last are read as its last row; their results are not stored.
+template <int T, int NT>
+struct Fill {
+    static constexpr int Q = T * 8 / NT;
+    const uint8_t* base;
+    uint32_t off[Q];
+    uint32_t chunk16;
+    __device__ __forceinline__ void init(const Operand& o, int64_t row0, int t) {
+        base = o.data + row0 * o.ld;
+        const uint32_t e = swz_slot(static_cast<uint32_t>(t));
+        chunk16 = 16 * (e % 8);
+        const int64_t left = o.rows - row0 - 1;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int64_t r = static_cast<int64_t>(e / 8 + NT / 8 * q);
+            off[q] = static_cast<uint32_t>((r < left ? r : left) * o.ld) + chunk16;
+        }
+    }
+    // rem: bytes of k from this stage on; chunks behind them are read from
+    // the stage's first chunk (masked when used).
+    __device__ __forceinline__ void issue(int64_t stage, int64_t rem, lds_u8* dst, int wave) const {
+        const uint8_t* b = base + stage * 128;
+        const uint32_t back = static_cast<int64_t>(chunk16) < rem ? 0u : chunk16;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            __builtin_amdgcn_global_load_lds(b + (off[q] - back), dst + 16 * (64 * wave + NT * q), 16, 0, 0);
+    }
+};
+
+template <class C>
+struct Stager {
+    Fill<C::TL, C::NT> fl;
+    Fill<C::TR, C::NT> fr;
+    const uint8_t* sp[C::NS ? C::NS : 1];  // this thread's scales, advanced stage by stage
+    uint32_t sv[C::NS ? C::NS : 1];
+    int t, wave;
+    int64_t kbytes;
+
+    __device__ __forceinline__ void init(const Operand& L, const Operand& R, int64_t l0, int64_t r0, int64_t kb,
+                                         int tid) {
+        t = tid;
+        wave = __builtin_amdgcn_readfirstlane(tid / 64);
+        kbytes = kb;
+        fl.init(L, l0, tid);
+        fr.init(R, r0, tid);
+        if constexpr (C::SC != kNoScale) {
+            constexpr int ES = C::SC == kE8M0 ? 1 : 4;
+#pragma unroll
+            for (int i = 0; i < C::NS; ++i) {
+                int e = t + C::NT * i;
+                if (e >= C::TL + C::TR) e = C::TL + C::TR - 1;
+                const bool left = e < C::TL;
+                const Operand& o = left ? L : R;
+                int64_t row = left ? l0 + e : r0 + (e - C::TL);
+                row = row < o.rows ? row : o.rows - 1;
+                sp[i] = static_cast<const uint8_t*>(o.scale) + (row >> o.scale_shift) * o.scale_ld * ES;
+            }
+        }
+    }
+    __device__ __forceinline__ void issue(int64_t s, lds_u8* buf) {
+        fl.issue(s, kbytes - s * 128, buf, wave);
+        fr.issue(s, kbytes - s * 128, buf + C::TL * 128, wave);
+        if constexpr (C::SC == kE8M0) {
+#pragma unroll
+            for (int i = 0; i < C::NS; ++i) sv[i] = sp[i][s];
+        } else if constexpr (C::SC != kNoScale) {
+#pragma unroll
+            for (int i = 0; i < C::NS; ++i) sv[i] = reinterpret_cast<const uint32_t*>(sp[i])[s];
+        }
+    }
+    // Scales that issue() fetched into their LDS buffer: fp32 by row; bytes so
+    // that the four rows 16 apart of a 64-row group share a word.
+    __device__ __forceinline__ void put_scales(lds_u8* sbuf) const {
+        if constexpr (C::SC != kNoScale) {
+#pragma unroll
+            for (int i = 0; i < C::NS; ++i) {
+                const int e = t + C::NT * i;
+                if (C::NS * C::NT == C::TL + C::TR || e < C::TL + C::TR) {
+                    if constexpr (C::SC == kE8M0)
+                        sbuf[e / 64 * 64 + e % 16 * 4 + e / 16 % 4] = static_cast<uint8_t>(sv[i]);
+                    else
+                        reinterpret_cast<lds_u32*>(sbuf)[e] = sv[i];
+                }
+            }
+        }
+    }
+};
+
+// Bytes of k at or behind `valid` cleared in one 16-byte piece.
+__device__ __forceinline__ i32x4 keep_bytes(i32x4 v, int valid) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const int n = valid - 4 * d;  // bytes kept of this word
+        const uint32_t m = n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+        v[d] = static_cast<int>(static_cast<uint32_t>(v[d]) & m);
+    }
+    return v;
+}
+
+// One 16-row fragment at byte `at` of the tile (chunk l/16; the other half
+// is 64 bytes away by XOR).  rem: bytes of k left, for the last stage.
+template <bool TAIL>
+__device__ __forceinline__ i32x8 read_frag(const lds_u8* tile, uint32_t at, uint32_t off, int g, int rem) {
+    i32x4 lo = *reinterpret_cast<const lds_i32x4*>(tile + at + off);
+    i32x4 hi = *reinterpret_cast<const lds_i32x4*>(tile + (at ^ 64u) + off);
+    if constexpr (TAIL) {
+        lo = keep_bytes(lo, rem - 16 * g);
+        hi = keep_bytes(hi, rem - 16 * g - 64);
+    }
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+template <class C, int OL, int OR>
+__device__ __forceinline__ f32x4 mfma_e8m0(i32x8 r, i32x8 l, f32x4 c, int sr, int sl) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(r, l, c, C::RT, C::LT, OR, sr, OL, sl);
+}
+
+template <class C, int OL>
+__device__ __forceinline__ f32x4 mfma_e8m0_r(i32x8 r, i32x8 l, f32x4 c, int sr, int sl, int o) {
+    switch (o) {
+        case 0: return mfma_e8m0<C, OL, 0>(r, l, c, sr, sl);
+        case 1: return mfma_e8m0<C, OL, 1>(r, l, c, sr, sl);
+        case 2: return mfma_e8m0<C, OL, 2>(r, l, c, sr, sl);
+        default: return mfma_e8m0<C, OL, 3>(r, l, c, sr, sl);
+    }
+}
+
+// Adds one stage's product of block fragments: r rows (registers), l columns
+// (lanes).  ol, orr: bytes of the scale words (constants after unrolling).
+template <class C>
+__device__ __forceinline__ void mma_stage(f32x4& acc, i32x8 r, i32x8 l, int sr, int sl, int orr, int ol, f32x4 fr,
+                                          float fl) {
+    if constexpr (C::ELEM == kF8) {
+        if constexpr (C::SC == kE8M0) {
+            switch (ol) {
+                case 0: acc = mfma_e8m0_r<C, 0>(r, l, acc, sr, sl, orr); break;
+                case 1: acc = mfma_e8m0_r<C, 1>(r, l, acc, sr, sl, orr); break;
+                case 2: acc = mfma_e8m0_r<C, 2>(r, l, acc, sr, sl, orr); break;
+                default: acc = mfma_e8m0_r<C, 3>(r, l, acc, sr, sl, orr); break;
+            }
+        } else {
+            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+            const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(r, l, zero, C::RT, C::LT, 0, 0, 0, 0);
+            if constexpr (C::SC == kF32Square) {
+                const float s = fr[0] * fl;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(p[i], s, acc[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(p[i], fr[i] * fl, acc[i]);
+            }
+        }
+    } else {
+        const i32x4 r0 = __builtin_shufflevector(r, r, 0, 1, 2, 3), r1 = __builtin_shufflevector(r, r, 4, 5, 6, 7);
+        const i32x4 l0 = __builtin_shufflevector(l, l, 0, 1, 2, 3), l1 = __builtin_shufflevector(l, l, 4, 5, 6, 7);
+        if constexpr (C::ELEM == kBf16) {
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r0), __builtin_bit_cast(bf16x8, l0),
+                                                          acc, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r1), __builtin_bit_cast(bf16x8, l1),
+                                                          acc, 0, 0, 0);
+        } else {
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, r0), __builtin_bit_cast(f16x8, l0), acc,
+                                                         0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, r1), __builtin_bit_cast(f16x8, l1), acc,
+                                                         0, 0, 0);
+        }
+    }
+}
+
+// This lane's scales of a stage.
+template <class C>
+struct LaneScales {
+    int lw[(C::BL + 3) / 4], rw[(C::BR + 3) / 4];  // E8M0: words of four blocks
+    float lf[C::BL], rf;
+    __device__ __forceinline__ void read(const lds_u8* sbuf, int wl, int wr, int lane) {
+        const int l16 = lane % 16;
+        if constexpr (C::SC == kE8M0) {
+#pragma unroll
+            for (int i = 0; i < (C::BL + 3) / 4; ++i) {
+                const int blk = wl * C::BL + 4 * i;
+                lw[i] = static_cast<int>(*reinterpret_cast<const lds_u32*>(sbuf + blk / 4 * 64 + l16 * 4) >>
+                                         (C::BL % 4 ? 8 * (blk % 4) : 0));
+            }
+#pragma unroll
+            for (int i = 0; i < (C::BR + 3) / 4; ++i) {
+                const int blk = C::TL / 16 + wr * C::BR + 4 * i;
+                rw[i] = static_cast<int>(*reinterpret_cast<const lds_u32*>(sbuf + blk / 4 * 64 + l16 * 4) >>
+                                         (C::BR % 4 || C::TL % 64 ? 8 * (blk % 4) : 0));
+            }
+        } else if constexpr (C::SC != kNoScale) {
+            const lds_f32* f = reinterpret_cast<const lds_f32*>(sbuf);
+#pragma unroll
+            for (int x = 0; x < C::BL; ++x) lf[x] = f[(wl * C::BL + x) * 16 + l16];
+            if constexpr (C::SC == kF32Square) rf = f[C::TL + wr * C::BR * 16];
+        }
+    }
+    __device__ __forceinline__ f32x4 rvec(const lds_u8* sbuf, int wr, int y, int lane) const {
+        if constexpr (C::SC == kF32Rows)
+            return *reinterpret_cast<const lds_f32x4*>(sbuf + 4 * (C::TL + (wr * C::BR + y) * 16 + 4 * (lane / 16)));
+        else if constexpr (C::SC == kF32Square)
+            return f32x4{rf, rf, rf, rf};
+        else
+            return f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+};
+
+template <class C, bool TAIL>
+__device__ __forceinline__ void stage_products(f32x4 (&acc)[C::BL][C::BR], const lds_u8* buf, const lds_u8* sbuf,
+                                               uint32_t lat, uint32_t rat, int wl, int wr, int lane, int rem) {
+    const int g = lane / 16;
+    LaneScales<C> sc;
+    sc.read(sbuf, wl, wr, lane);
+    i32x8 lf[C::BL];
+#pragma unroll
+    for (int x = 0; x < C::BL; ++x) lf[x] = read_frag<TAIL>(buf, lat, 2048 * x, g, rem);
+#pragma unroll
+    for (int y = 0; y < C::BR; ++y) {
+        const i32x8 rf = read_frag<TAIL>(buf + C::TL * 128, rat, 2048 * y, g, rem);
+        const f32x4 rs = sc.rvec(sbuf, wr, y, lane);
+#pragma unroll
+        for (int x = 0; x < C::BL; ++x)
+            mma_stage<C>(acc[x][y], rf, lf[x], sc.rw[y / 4], sc.lw[x / 4], y % 4, x % 4, rs, sc.lf[x]);
+    }
+}
+
+// The whole product of one tile: rows l0 .. of L against rows r0 .. of R over
+// kbytes bytes of k.  Sums run over k in increasing order.
+template <class C>
+__device__ __forceinline__ void tile_product(f32x4 (&acc)[C::BL][C::BR], const Operand& L, const Operand& R, int64_t l0,
+                                             int64_t r0, int64_t kbytes, lds_u8* lds) {
+    const int t = threadIdx.x, lane = t % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(t / 64);
+    const int wl = wave / C::WR, wr = wave % C::WR;
+#pragma unroll
+    for (int x = 0; x < C::BL; ++x)
+#pragma unroll
+        for (int y = 0; y < C::BR; ++y) acc[x][y] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int64_t stages = (kbytes + 127) / 128, full = kbytes / 128;
+    if (stages == 0) return;
+    Stager<C> st;
+    st.init(L, R, l0, r0, kbytes, t);
+    lds_u8* sbufs = lds + 2 * C::kBuf;
+    const int l16 = lane % 16;
+    const uint32_t at = l16 * 128 + 16 * ((lane / 16) ^ ((l16 >> 1) & 7));
+    const uint32_t lat = wl * C::BL * 2048 + at, rat = wr * C::BR * 2048 + at;
+    st.issue(0, lds);
+    // Stage s: wait until this wave's loads of it have landed (the barrier
+    // covers the others') and every wave is done with stage s - 1, whose
+    // buffer the next loads reuse; then start stage s + 1's loads.
+    auto begin = [&](int64_t s) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        st.put_scales(sbufs + (s & 1) * C::kScaleBuf);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wg_barrier();
+        if (s + 1 < stages) st.issue(s + 1, lds + ((s + 1) & 1) * C::kBuf);
+    };
+    for (int64_t s = 0; s < full; ++s) {
+        begin(s);
+        stage_products<C, false>(acc, lds + (s & 1) * C::kBuf, sbufs + (s & 1) * C::kScaleBuf, lat, rat, wl, wr, lane, 128);
+    }
+    if (full < stages) {
+        begin(full);
+        stage_products<C, true>(acc, lds + (full & 1) * C::kBuf, sbufs + (full & 1) * C::kScaleBuf, lat, rat, wl, wr, lane,
+                                static_cast<int>(kbytes - full * 128));
+    }
+    // every wave is done reading before the epilogue reuses the buffers
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    wg_barrier();
+}
+
+// A wave's accumulators out to C [rows][ldc] of CT, rows i0 .., columns j0 ..
+// of the wave, through its LDS slice: 16 rows at a time, so that stores are
+// whole runs of C rows.  vec: ldc and the pointer allow 16-byte stores (the
+// columns then end on a whole piece too).  f(value) is applied first.
+template <class C, class CT, class F>
+__device__ __forceinline__ void store_tile(const f32x4 (&acc)[C::BL][C::BR], lds_f32* slice, CT* __restrict__ c,
+                                           int64_t ldc, int64_t i0, int64_t j0, int64_t rows, int64_t cols, bool vec,
+                                           int lane, F f) {
+    constexpr int W = 16 * C::BR, P = C::kPitch, V = 16 / sizeof(CT), PER = W / V;  // V elements a piece
+    typedef CT ctv __attribute__((ext_vector_type(V)));
+    const int g = lane / 16, l16 = lane % 16;
+#pragma unroll
+    for (int x = 0; x < C::BL; ++x) {
+#pragma unroll
+        for (int y = 0; y < C::BR; ++y) *reinterpret_cast<lds_f32x4*>(slice + l16 * P + 16 * y + 4 * g) = acc[x][y];
+        const int64_t ib = i0 + 16 * x;
+        if (ib >= rows) continue;
+        if (vec) {
+            static_assert(16 * PER % 64 == 0, "whole pieces per wave");
+#pragma unroll
+            for (int q = 0; q < 16 * PER / 64; ++q) {
+                const int u = 64 * q + lane, r = u / PER, cc = V * (u % PER);
+                ctv o;
+#pragma unroll
+                for (int h = 0; h < V / 4; ++h) {
+                    const f32x4 v = *reinterpret_cast<const lds_f32x4*>(slice + r * P + cc + 4 * h);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[4 * h + i] = static_cast<CT>(f(v[i]));
+                }
+                if (ib + r < rows && j0 + cc < cols)
+                    __builtin_nontemporal_store(o, reinterpret_cast<ctv*>(c + (ib + r) * ldc + j0 + cc));
+            }
+        } else {
+            for (int u = lane; u < 16 * W; u += 64) {
+                const int r = u / W, cc = u % W;
+                if (ib + r < rows && j0 + cc < cols) c[(ib + r) * ldc + j0 + cc] = static_cast<CT>(f(slice[r * P + cc]));
+            }
+        }
+    }
+}
+
+}  // namespace mma
+}  // namespace swz
