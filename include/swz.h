@@ -19,7 +19,8 @@
  * (swz_gemm_frag); the GEMM that stages its own operands through swizzled
  * tiles (swz_gemm, swz_gemm_ex for a bf16 result); 8-bit floating-point
  * operands with a scale per block of 128 (swz_quant_f8) and their product
- * (swz_gemm_f8); host-only planning, bank-conflict prediction and layout
+ * (swz_gemm_f8); the losses of an output layer whose logits are not kept, with
+ * their gradients (swz_linear_ce, swz_linear_distill); host-only planning, bank-conflict prediction and layout
  * algebra (swz_choose, swz_plan, swz_predict_conflicts, swz_kernel_accesses,
  * swz_bank_model_get, swz_fold); and two diagnostics (swz_copy,
  * swz_lds_probe).
@@ -490,14 +491,84 @@ int swz_quant_f8(const void* d_x, int32_t x_type, int64_t rows, int64_t cols, in
  * 64) go to kernels that stream B once.  d_a, d_b 16-byte aligned, fp32 scales
  * 4-byte, d_c aligned to its element; rows of C whose pitch and start are
  * multiples of 16 bytes are written in 16-byte pieces.
- * The products are exact in fp32; sums over k are fp32, a bf16 C is rounded
- * once, to nearest even.  fp32 scales multiply the fp32 sum of their block.
+ * A float C is summed in fp32 from exact products (the operands widened to
+ * bf16, at the bf16 rate); with SWZ_SCALE_E8M0 a value times its scale has to
+ * be a normal bf16 number for that.  A bf16 C takes the 8-bit matrix
+ * instruction, which adds the products of each eight consecutive k after
+ * dropping what lies more than 13 bits below the largest of them (1.5e-5 of
+ * the norm of a product of normal operands, a hundredth of the rounding to
+ * bf16), sums those in fp32 and is rounded once, to nearest even.  fp32 scales
+ * multiply fp32 sums within their block.
  * NaN and infinities in the used elements and scales propagate.
  * Errors: SWZ_EINVAL (sizes, pitches, alignment, NULL, overlap, enum values),
  * SWZ_EUNSUPPORTED (lda or ldb of 2^23 and more, or over 2^22 tiles of C). */
 int swz_gemm_f8(const void* d_a, const void* d_scale_a, const void* d_b, const void* d_scale_b, void* d_c, int64_t m,
                 int64_t n, int64_t k, int64_t lda, int64_t ldb, int32_t a_type, int32_t b_type, int32_t a_block,
                 int32_t b_block, int32_t scale_type, int32_t c_type, void* stream);
+
+/* Host only.  Bytes of workspace that the losses below need for n rows, v
+ * words, k features and `top` entries a row (1 for cross entropy): grad 0,
+ * the forward calls; 1, enough for the forward and the gradient calls.  A
+ * workspace is 256-byte aligned device memory that carries nothing from one
+ * call to the next; calls that may run at the same time (on two streams, in
+ * two graphs) need one each.
+ * Errors: SWZ_EINVAL, SWZ_EUNSUPPORTED (sizes, as the calls). */
+int swz_linear_loss_workspace(int64_t n, int64_t v, int64_t k, int32_t top, int32_t grad, int64_t* bytes);
+
+/* Softmax cross entropy of the logits z = H W^T, in pieces of the vocabulary
+ * and without keeping them:
+ *   lse[i] = log sum over v of exp(z[i][v]),  loss[i] = lse[i] - z[i][target[i]].
+ *   d_h      : x_type (SWZ_X_BF16 or SWZ_X_F16) [n][k]; d_w : the same type
+ *              [v][k]; k a multiple of 8, both 16-byte aligned.
+ *   d_target : int64 [n].  A target outside 0 .. v - 1 marks a row that does
+ *              not count: its loss is 0 and it adds nothing to the gradients.
+ *   d_loss, d_lse, d_zt : float [n]; zt is the logit at the target (0 for rows
+ *              that do not count).  lse and zt are what the gradient call takes.
+ * Products are exact in fp32 and summed in fp32.  A row with a logit that is
+ * NaN or +infinity has a NaN lse.
+ * Nothing written may overlap anything else.  n = 0 does nothing.
+ * Errors: SWZ_EINVAL (sizes, alignment, NULL, overlap, x_type, a workspace
+ * below swz_linear_loss_workspace), SWZ_EUNSUPPORTED (n or k of 2^22 and more,
+ * v of 2^31 and more, over 2^22 tiles of 256 x 256 logits). */
+int swz_linear_ce(const void* d_h, const void* d_w, int32_t x_type, const int64_t* d_target, float* d_loss,
+                  float* d_lse, float* d_zt, int64_t n, int64_t v, int64_t k, void* d_ws, int64_t ws_bytes,
+                  void* stream);
+
+/* Its gradients, for upstream[i] = d(total) / d(loss[i]) (float [n]):
+ *   dz[i][v] = upstream[i] (exp(z[i][v] - lse[i]) - [v = target[i]]),
+ *   dh = dz W ([n][k]), dw = dz^T H ([v][k]), both x_type, rounded once,
+ * overwritten; either may be NULL.  The logits are computed again, a piece of
+ * the vocabulary at a time.  dz is held in fp16 with the largest upstream
+ * taken out, H and W in fp16 with a power of two; sums are fp32.  n = 0
+ * writes a zero dw.  Results do not depend on the order of anything: the same
+ * call gives the same bits.
+ * Errors: as swz_linear_ce. */
+int swz_linear_ce_grad(const void* d_h, const void* d_w, int32_t x_type, const int64_t* d_target, const float* d_lse,
+                       const float* d_zt, const float* d_upstream, void* d_dh, void* d_dw, int64_t n, int64_t v,
+                       int64_t k, void* d_ws, int64_t ws_bytes, void* stream);
+
+/* Distillation from a teacher's top logits, without keeping the student's:
+ *   p[i] = softmax over the row's entries of teacher[i][j] / tau,
+ *   lse[i] = log sum over v of exp(z[i][v] / tau),
+ *   loss[i] = tau^2 sum over j of p[i][j] (log p[i][j] - (z[i][index[i][j]] / tau - lse[i])).
+ *   d_index   : int64 [n][top]; d_teacher : float [n][top]; 1 <= top <= 256.
+ *               Entries whose index is outside 0 .. v - 1 or whose logit is
+ *               -infinity are absent; a row without entries has loss 0 and adds
+ *               nothing to the gradients.  Equal indices add up.
+ *   d_zt      : float [n][top], the student's logits (before tau) at the entries.
+ *   tau       : > 0 and finite.
+ * The rest, and the errors, as swz_linear_ce (SWZ_EUNSUPPORTED also for top
+ * above 256). */
+int swz_linear_distill(const void* d_h, const void* d_w, int32_t x_type, const int64_t* d_index,
+                       const float* d_teacher, int32_t top, float tau, float* d_loss, float* d_lse, float* d_zt,
+                       int64_t n, int64_t v, int64_t k, void* d_ws, int64_t ws_bytes, void* stream);
+
+/* Its gradients with respect to H and W, as swz_linear_ce_grad:
+ *   dz[i][v] = upstream[i] tau (exp(z[i][v] / tau - lse[i]) - sum over j with index[i][j] = v of p[i][j]). */
+int swz_linear_distill_grad(const void* d_h, const void* d_w, int32_t x_type, const int64_t* d_index,
+                            const float* d_teacher, int32_t top, float tau, const float* d_lse, const float* d_zt,
+                            const float* d_upstream, void* d_dh, void* d_dw, int64_t n, int64_t v, int64_t k,
+                            void* d_ws, int64_t ws_bytes, void* stream);
 
 /* Host only.  The swizzle the library uses for a tile of tile_rows x
  * tile_cols elements of elem_bytes, staged by vec_bytes-wide stores and read

@@ -22,6 +22,8 @@ hipError_t launch_gemm_tiles(const void*, const void*, void*, int64_t, int64_t, 
 }
 hipError_t launch_quant(const QuantJob&, hipStream_t) { return hipSuccess; }
 hipError_t launch_gemm_f8(const GemmF8Job&, hipStream_t) { return hipSuccess; }
+hipError_t launch_loss(const LossJob&, hipStream_t) { return hipSuccess; }
+hipError_t launch_loss_grad(const LossJob&, const LossPlan&, hipStream_t) { return hipSuccess; }
 hipError_t launch_map(const int32_t*, int32_t*, int64_t, swz_params, hipStream_t) { return hipSuccess; }
 hipError_t launch_map_batch(const int32_t*, int32_t*, int64_t, const MapParamPack&, int, hipStream_t) {
     return hipSuccess;

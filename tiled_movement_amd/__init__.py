@@ -54,6 +54,11 @@ EXPORTS = (
     "swz_gemm_ex",
     "swz_quant_f8",
     "swz_gemm_f8",
+    "swz_linear_loss_workspace",
+    "swz_linear_ce",
+    "swz_linear_ce_grad",
+    "swz_linear_distill",
+    "swz_linear_distill_grad",
     "swz_fold",
     "swz_choose",
     "swz_predict_conflicts",
@@ -155,6 +160,12 @@ def _load() -> ctypes.CDLL:
     lib.swz_lds_probe.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp]
     lib.swz_quant_f8.argtypes = [vp, i32, i64, i64, i64, i32, i32, i32, vp, vp, i64, vp, vp, i64, vp]
     lib.swz_gemm_f8.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i32, i32, i32, i32, i32, i32, vp]
+    f32 = ctypes.c_float
+    lib.swz_linear_loss_workspace.argtypes = [i64, i64, i64, i32, i32, P(i64)]
+    lib.swz_linear_ce.argtypes = [vp, vp, i32, vp, vp, vp, vp, i64, i64, i64, vp, i64, vp]
+    lib.swz_linear_ce_grad.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, i64, vp]
+    lib.swz_linear_distill.argtypes = [vp, vp, i32, vp, vp, i32, f32, vp, vp, vp, i64, i64, i64, vp, i64, vp]
+    lib.swz_linear_distill_grad.argtypes = [vp, vp, i32, vp, vp, i32, f32, vp, vp, vp, vp, vp, i64, i64, i64, vp, i64, vp]
     for name in EXPORTS:
         if name != "swz_strerror":
             getattr(lib, name).restype = ctypes.c_int
@@ -358,6 +369,72 @@ def swz_gemm_f8(a, scale_a, b, scale_b, c, m: int, n: int, k: int, lda: Optional
          scale_b=(scale_b, _f8_scale_bytes(n, k, b_block, scale_type)), c=(c, (2 if c_type == C_BF16 else 4) * m * n))
     _check(lib.swz_gemm_f8(_ptr(a), _ptr(scale_a), _ptr(b), _ptr(scale_b), _ptr(c), m, n, k, lda, ldb, a_type, b_type,
                            a_block, b_block, scale_type, c_type, _stream(stream, a, b, c)), "swz_gemm_f8")
+
+
+def swz_linear_loss_workspace(n: int, v: int, k: int, top: int = 1, grad: bool = False) -> int:
+    """Bytes of workspace for the losses below (grad: for their gradients too)."""
+    out = ctypes.c_int64()
+    _check(lib.swz_linear_loss_workspace(n, v, k, top, 1 if grad else 0, ctypes.byref(out)), "swz_linear_loss_workspace")
+    return out.value
+
+
+def _ws_bytes(ws, need: int) -> int:
+    """Bytes of a workspace tensor (a raw address is taken to hold what the call needs)."""
+    return need if ws is None or isinstance(ws, int) else ws.numel() * ws.element_size()
+
+
+def _typed(call: str, **bufs) -> None:
+    """Raise ValueError for a tensor whose element size is not the one the call reads (name=(tensor, bytes per element))."""
+    for name, (t, size) in bufs.items():
+        if t is not None and not isinstance(t, int) and t.element_size() != size:
+            raise ValueError(f"{call}: {name} has {t.element_size()}-byte elements, the call reads {size}-byte ones")
+
+
+def swz_linear_ce(h, w, target, loss, lse, zt, n: int, v: int, k: int, ws, x_type: int = X_BF16, stream=None) -> None:
+    """loss[i] = lse[i] - zt[i] of the logits h w^T, which are not kept (target: int64)."""
+    need = swz_linear_loss_workspace(n, v, k)
+    _buf("swz_linear_ce", h=(h, 2 * n * k), w=(w, 2 * v * k), target=(target, 8 * n), loss=(loss, 4 * n), lse=(lse, 4 * n),
+         zt=(zt, 4 * n), ws=(ws, need))
+    _typed("swz_linear_ce", h=(h, 2), w=(w, 2), target=(target, 8))
+    _check(lib.swz_linear_ce(_ptr(h), _ptr(w), x_type, _ptr(target), _ptr(loss), _ptr(lse), _ptr(zt), n, v, k, _ptr(ws),
+                             _ws_bytes(ws, need), _stream(stream, h, w)), "swz_linear_ce")
+
+
+def swz_linear_ce_grad(h, w, target, lse, zt, upstream, dh, dw, n: int, v: int, k: int, ws, x_type: int = X_BF16,
+                       stream=None) -> None:
+    """dh [n][k] and dw [v][k] of sum(upstream * loss); either may be None."""
+    need = swz_linear_loss_workspace(n, v, k, grad=True)
+    _buf("swz_linear_ce_grad", h=(h, 2 * n * k), w=(w, 2 * v * k), target=(target, 8 * n), lse=(lse, 4 * n), zt=(zt, 4 * n),
+         upstream=(upstream, 4 * n), dh=(dh, 2 * n * k), dw=(dw, 2 * v * k), ws=(ws, need))
+    _typed("swz_linear_ce_grad", h=(h, 2), w=(w, 2), target=(target, 8), dh=(dh, 2), dw=(dw, 2))
+    _check(lib.swz_linear_ce_grad(_ptr(h), _ptr(w), x_type, _ptr(target), _ptr(lse), _ptr(zt), _ptr(upstream), _ptr(dh),
+                                  _ptr(dw), n, v, k, _ptr(ws), _ws_bytes(ws, need), _stream(stream, h, w)),
+           "swz_linear_ce_grad")
+
+
+def swz_linear_distill(h, w, index, teacher, loss, lse, zt, n: int, v: int, k: int, top: int, tau: float, ws,
+                       x_type: int = X_BF16, stream=None) -> None:
+    """tau^2 KL(teacher's top logits || softmax(h w^T / tau)) per row (index: int64 [n][top], teacher: fp32)."""
+    need = swz_linear_loss_workspace(n, v, k, top)
+    _buf("swz_linear_distill", h=(h, 2 * n * k), w=(w, 2 * v * k), index=(index, 8 * n * top), teacher=(teacher, 4 * n * top),
+         loss=(loss, 4 * n), lse=(lse, 4 * n), zt=(zt, 4 * n * top), ws=(ws, need))
+    _typed("swz_linear_distill", h=(h, 2), w=(w, 2), index=(index, 8), teacher=(teacher, 4))
+    _check(lib.swz_linear_distill(_ptr(h), _ptr(w), x_type, _ptr(index), _ptr(teacher), top, tau, _ptr(loss), _ptr(lse),
+                                  _ptr(zt), n, v, k, _ptr(ws), _ws_bytes(ws, need), _stream(stream, h, w)),
+           "swz_linear_distill")
+
+
+def swz_linear_distill_grad(h, w, index, teacher, lse, zt, upstream, dh, dw, n: int, v: int, k: int, top: int, tau: float,
+                            ws, x_type: int = X_BF16, stream=None) -> None:
+    """dh [n][k] and dw [v][k] of sum(upstream * loss); either may be None."""
+    need = swz_linear_loss_workspace(n, v, k, top, grad=True)
+    _buf("swz_linear_distill_grad", h=(h, 2 * n * k), w=(w, 2 * v * k), index=(index, 8 * n * top),
+         teacher=(teacher, 4 * n * top), lse=(lse, 4 * n), zt=(zt, 4 * n * top), upstream=(upstream, 4 * n),
+         dh=(dh, 2 * n * k), dw=(dw, 2 * v * k), ws=(ws, need))
+    _typed("swz_linear_distill_grad", h=(h, 2), w=(w, 2), index=(index, 8), teacher=(teacher, 4), dh=(dh, 2), dw=(dw, 2))
+    _check(lib.swz_linear_distill_grad(_ptr(h), _ptr(w), x_type, _ptr(index), _ptr(teacher), top, tau, _ptr(lse), _ptr(zt),
+                                       _ptr(upstream), _ptr(dh), _ptr(dw), n, v, k, _ptr(ws), _ws_bytes(ws, need),
+                                       _stream(stream, h, w)), "swz_linear_distill_grad")
 
 
 def swz_fold(params, base: int, active: int):

@@ -29,6 +29,7 @@ SOURCES = [
     "kernels_gemm_tiles.hip",
     "kernels_gemm_f8.hip",
     "kernels_quant.hip",
+    "kernels_loss.hip",
     "kernels_map.hip",
     "kernels_rows.hip",
     "kernels_copy.hip",

@@ -32,6 +32,8 @@ bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
 // unsigned, so that a huge n wraps instead of overflowing (16 divides 2^64).
 bool pitch16(int64_t n, int32_t esz) { return (static_cast<uint64_t>(n) * static_cast<uint64_t>(esz)) % 16 == 0; }
 
+int hip_status(hipError_t e) { return e == hipSuccess ? SWZ_OK : SWZ_EHIP; }
+
 // Row pitches of the products' operands stay below this many bytes, so that
 // the rows of a tile lie within 31-bit offsets (mma_core.h).
 constexpr int64_t kMaxPitch = int64_t(1) << 23;
@@ -42,6 +44,123 @@ bool f8_operand_bytes(int64_t rows, int64_t cols, int64_t ld, bool square, int32
     int64_t n;
     const int64_t srows = square ? rows / 128 + (rows % 128 != 0) : rows, scols = cols / 128 + (cols % 128 != 0);
     return mul_ok(rows, ld, data) && mul_ok(srows, scols, &n) && mul_ok(n, scale_type == SWZ_SCALE_F32 ? 4 : 1, scales);
+}
+
+// Sizes of an output-layer loss that the kernels' grids and offsets take:
+// SWZ_OK, or why not.
+int check_loss_sizes(int64_t n, int64_t v, int64_t k, int32_t top) {
+    if (n < 0 || v < 1 || k < 8 || k % 8 || top < 1) return SWZ_EINVAL;
+    if (top > swz::kMaxTop || 2 * k >= kMaxPitch || 2 * (n + 8) >= kMaxPitch || v >= int64_t(1) << 31) return SWZ_EUNSUPPORTED;
+    if ((n / 256 + 1) * (v / 256 + 1) > int64_t(1) << 22) return SWZ_EUNSUPPORTED;  // tiles of one launch
+    return SWZ_OK;
+}
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// The gradient's workspace.  dz of a piece stays within 2^27 values (256 MiB)
+// unless that leaves fewer than 8192 words; pieces are alike in size.  Where
+// dH has fewer tiles than the 256 compute units, its sum over a piece is split
+// into parts (of at least 8 stages) with buffers of their own.
+swz::LossPlan plan_loss(int64_t n, int64_t v, int64_t k, int32_t top) {
+    swz::LossPlan p{};
+    int64_t most = (int64_t(1) << 27) / (n ? n : 1) / 256 * 256;
+    most = most < 8192 ? 8192 : most > 32768 ? 32768 : most;
+    const int64_t pieces = (v + most - 1) / most;
+    p.piece = up((v + pieces - 1) / pieces, 256);
+    const int64_t tl = n <= 64 ? 64 : n <= 128 ? 128 : 256;
+    const int64_t tiles = ((n + tl - 1) / tl) * ((k + 255) / 256), stages = p.piece / 64;
+    p.parts = tiles >= 256 || tiles == 0 ? 1 : 256 / tiles;
+    if (p.parts > 16) p.parts = 16;
+    if (p.parts > stages / 8) p.parts = stages / 8 ? stages / 8 : 1;
+    const int64_t ldn = up(n, 8);
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += up(bytes, 256);
+        return here;
+    };
+    p.slots = take(64);
+    p.g = take(4 * n);
+    p.weight = take(4 * n * top);
+    p.dz = take(2 * n * p.piece);
+    p.dzt = take(2 * p.piece * ldn);
+    p.ht = take(2 * k * ldn);
+    p.wt = take(2 * k * p.piece);
+    p.sums = take(4 * p.parts * n * k);
+    p.bytes = at;
+    return p;
+}
+
+int64_t loss_forward_bytes(int64_t n, int64_t v) { return up(8 * n * ((v + 255) / 256), 256); }
+
+struct Span {
+    const void* p;
+    int64_t bytes;
+    uintptr_t align;
+    bool written;
+};
+
+// NULL, alignment and overlap of a call's buffers: nothing written may
+// overlap anything else.
+bool spans_ok(const Span* s, int count) {
+    for (int i = 0; i < count; ++i) {
+        if (s[i].bytes == 0) continue;
+        if (!s[i].p || reinterpret_cast<uintptr_t>(s[i].p) % s[i].align) return false;
+        for (int j = 0; j < i; ++j)
+            if ((s[i].written || s[j].written) && s[j].bytes && overlaps(s[i].p, s[i].bytes, s[j].p, s[j].bytes)) return false;
+    }
+    return true;
+}
+
+int loss_forward(const void* d_h, const void* d_w, int32_t x_type, const int64_t* index, const float* teacher, int32_t top,
+                 float tau, float* loss, float* lse, float* zt, int64_t n, int64_t v, int64_t k, void* ws, int64_t ws_bytes,
+                 void* stream) {
+    if (x_type != SWZ_X_BF16 && x_type != SWZ_X_F16) return SWZ_EINVAL;
+    if (!(tau > 0.f) || tau > 3.4e38f) return SWZ_EINVAL;
+    const int st = check_loss_sizes(n, v, k, top);
+    if (st != SWZ_OK) return st;
+    if (n == 0) return SWZ_OK;
+    const int64_t need = loss_forward_bytes(n, v);
+    if (ws_bytes < need) return SWZ_EINVAL;
+    const bool distill = teacher != nullptr;
+    const Span s[8] = {{d_h, 2 * n * k, 16, false},     {d_w, 2 * v * k, 16, false}, {index, 8 * n * top, 8, false},
+                       {teacher, distill ? 4 * n * top : 0, 4, false}, {loss, 4 * n, 4, true}, {lse, 4 * n, 4, true},
+                       {zt, 4 * n * top, 4, true},      {ws, need, 256, true}};
+    if (!spans_ok(s, 8)) return SWZ_EINVAL;
+    swz::LossJob j{};
+    j.h = d_h, j.w = d_w, j.bf16 = x_type == SWZ_X_BF16, j.n = n, j.v = v, j.k = k, j.index = index, j.teacher = teacher;
+    j.top = top, j.tau = tau, j.loss = loss, j.lse = lse, j.zt = zt, j.ws = ws;
+    return hip_status(swz::launch_loss(j, static_cast<hipStream_t>(stream)));
+}
+
+int loss_backward(const void* d_h, const void* d_w, int32_t x_type, const int64_t* index, const float* teacher, int32_t top,
+                  float tau, const float* lse, const float* zt, const float* upstream, void* dh, void* dw, int64_t n,
+                  int64_t v, int64_t k, void* ws, int64_t ws_bytes, void* stream) {
+    if (x_type != SWZ_X_BF16 && x_type != SWZ_X_F16) return SWZ_EINVAL;
+    if (!(tau > 0.f) || tau > 3.4e38f) return SWZ_EINVAL;
+    const int st = check_loss_sizes(n, v, k, top);
+    if (st != SWZ_OK) return st;
+    if (!dh && !dw) return SWZ_EINVAL;
+    if (n == 0 && !dw) return SWZ_OK;
+    const swz::LossPlan plan = plan_loss(n, v, k, top);
+    if (n > 0 && ws_bytes < plan.bytes) return SWZ_EINVAL;
+    const bool distill = teacher != nullptr;
+    const Span s[10] = {{d_h, 2 * n * k, 16, false},
+                        {d_w, n ? 2 * v * k : 0, 16, false},
+                        {index, 8 * n * top, 8, false},
+                        {teacher, distill ? 4 * n * top : 0, 4, false},
+                        {lse, 4 * n, 4, false},
+                        {zt, 4 * n * top, 4, false},
+                        {upstream, 4 * n, 4, false},
+                        {dh, dh ? 2 * n * k : 0, 16, true},
+                        {dw, dw ? 2 * v * k : 0, 16, true},
+                        {ws, n ? plan.bytes : 0, 256, true}};
+    if (!spans_ok(s, 10)) return SWZ_EINVAL;
+    swz::LossJob j{};
+    j.h = d_h, j.w = d_w, j.bf16 = x_type == SWZ_X_BF16, j.n = n, j.v = v, j.k = k, j.index = index, j.teacher = teacher;
+    j.top = top, j.tau = tau, j.lse = const_cast<float*>(lse), j.zt = const_cast<float*>(zt), j.upstream = upstream;
+    j.dh = dh, j.dw = dw, j.ws = ws;
+    return hip_status(swz::launch_loss_grad(j, plan, static_cast<hipStream_t>(stream)));
 }
 
 int ilog2(int64_t v) {
@@ -204,8 +323,6 @@ swz::LdsLayout layout_of(const swz_plan_info& pl) {
     return swz::LdsLayout{static_cast<uint32_t>(pl.tile_cols + pl.pad_elems), static_cast<uint32_t>(pl.params.B),
                           static_cast<uint32_t>(pl.params.M), pl.params.S};
 }
-
-int hip_status(hipError_t e) { return e == hipSuccess ? SWZ_OK : SWZ_EHIP; }
 
 // The order of a shape with none pinned, from sweeps of every order over
 // matrices of 32-512 MiB with sides from 1,024 to 16,384 (bench.py
@@ -627,6 +744,47 @@ SWZ_API int swz_gemm_f8(const void* d_a, const void* d_scale_a, const void* d_b,
     const swz::GemmF8Job job{d_a, d_scale_a, d_b, d_scale_b, d_c, m, n, k, lda, ldb, a_type == SWZ_F8_E5M2,
                              b_type == SWZ_F8_E5M2, sqa, sqb, scale_type == SWZ_SCALE_E8M0, c_type == SWZ_C_BF16};
     return hip_status(swz::launch_gemm_f8(job, static_cast<hipStream_t>(stream)));
+}
+
+SWZ_API int swz_linear_loss_workspace(int64_t n, int64_t v, int64_t k, int32_t top, int32_t grad, int64_t* bytes) {
+    if (!bytes || (grad != 0 && grad != 1)) return SWZ_EINVAL;
+    const int st = check_loss_sizes(n, v, k, top);
+    if (st != SWZ_OK) return st;
+    *bytes = loss_forward_bytes(n, v);
+    if (grad) {
+        const int64_t b = plan_loss(n, v, k, top).bytes;
+        if (b > *bytes) *bytes = b;
+    }
+    return SWZ_OK;
+}
+
+SWZ_API int swz_linear_ce(const void* d_h, const void* d_w, int32_t x_type, const int64_t* d_target, float* d_loss,
+                          float* d_lse, float* d_zt, int64_t n, int64_t v, int64_t k, void* d_ws, int64_t ws_bytes,
+                          void* stream) {
+    return loss_forward(d_h, d_w, x_type, d_target, nullptr, 1, 1.f, d_loss, d_lse, d_zt, n, v, k, d_ws, ws_bytes, stream);
+}
+
+SWZ_API int swz_linear_ce_grad(const void* d_h, const void* d_w, int32_t x_type, const int64_t* d_target,
+                               const float* d_lse, const float* d_zt, const float* d_upstream, void* d_dh, void* d_dw,
+                               int64_t n, int64_t v, int64_t k, void* d_ws, int64_t ws_bytes, void* stream) {
+    return loss_backward(d_h, d_w, x_type, d_target, nullptr, 1, 1.f, d_lse, d_zt, d_upstream, d_dh, d_dw, n, v, k, d_ws,
+                         ws_bytes, stream);
+}
+
+SWZ_API int swz_linear_distill(const void* d_h, const void* d_w, int32_t x_type, const int64_t* d_index,
+                               const float* d_teacher, int32_t top, float tau, float* d_loss, float* d_lse, float* d_zt,
+                               int64_t n, int64_t v, int64_t k, void* d_ws, int64_t ws_bytes, void* stream) {
+    if (n > 0 && !d_teacher) return SWZ_EINVAL;
+    return loss_forward(d_h, d_w, x_type, d_index, d_teacher, top, tau, d_loss, d_lse, d_zt, n, v, k, d_ws, ws_bytes, stream);
+}
+
+SWZ_API int swz_linear_distill_grad(const void* d_h, const void* d_w, int32_t x_type, const int64_t* d_index,
+                                    const float* d_teacher, int32_t top, float tau, const float* d_lse, const float* d_zt,
+                                    const float* d_upstream, void* d_dh, void* d_dw, int64_t n, int64_t v, int64_t k,
+                                    void* d_ws, int64_t ws_bytes, void* stream) {
+    if (n > 0 && !d_teacher) return SWZ_EINVAL;
+    return loss_backward(d_h, d_w, x_type, d_index, d_teacher, top, tau, d_lse, d_zt, d_upstream, d_dh, d_dw, n, v, k, d_ws,
+                         ws_bytes, stream);
 }
 
 SWZ_API int swz_fold(const swz_params* p, uint32_t base, uint32_t active, uint32_t* collision,

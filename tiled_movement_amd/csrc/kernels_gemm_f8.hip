@@ -11,9 +11,9 @@ namespace {
 
 using namespace mma;
 
-template <class C>
-__global__ __launch_bounds__(C::NT) void k_gemm_f8(Operand A, Operand B, void* __restrict__ c, int64_t ldc, int64_t k,
-                                                   uint32_t tiles_m, int bf16c, int vec) {
+template <class C, class CT>
+__global__ __launch_bounds__(C::NT) void k_gemm_f8(Operand A, Operand B, CT* __restrict__ c, int64_t ldc, int64_t k,
+                                                   uint32_t tiles_m, int vec) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
     const int64_t i0 = static_cast<int64_t>(blockIdx.x % tiles_m) * C::TL;
@@ -23,25 +23,31 @@ __global__ __launch_bounds__(C::NT) void k_gemm_f8(Operand A, Operand B, void* _
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     lds_f32* slice = (lds_f32*)(lds + wave * C::kSlice);
     const int64_t wi = i0 + wave / C::WR * C::BL * 16, wj = j0 + wave % C::WR * C::BR * 16;
-    auto same = [](float v) { return v; };
-    if (bf16c)
-        store_tile<C>(acc, slice, static_cast<__bf16*>(c), ldc, wi, wj, A.rows, B.rows, vec, lane, same);
-    else
-        store_tile<C>(acc, slice, static_cast<float*>(c), ldc, wi, wj, A.rows, B.rows, vec, lane, same);
+    store_tile<C>(acc, slice, c, ldc, wi, wj, A.rows, B.rows, vec, lane, [](float v) { return v; });
 }
 
-template <int LT, int RT, int SC>
-hipError_t launch_typed(const GemmF8Job& j, hipStream_t stream) {
-    using C = Config<kF8, LT, RT, SC, 4, 2, 4, 8>;
+template <int ELEM, int LT, int RT, int SC, class CT>
+hipError_t launch_tiles(const GemmF8Job& j, hipStream_t stream) {
+    // fp32 scales of both operands' rows on widened operands need more
+    // registers than a 64 x 128 wave tile leaves (145 spilled): half the rows.
+    constexpr int BL = ELEM == kF8Wide && SC == kF32Rows ? 2 : 4;
+    using C = Config<ELEM, LT, RT, SC, 4, 2, BL, 8>;
     const Operand A{static_cast<const uint8_t*>(j.a), j.lda, j.m, j.scale_a, (j.k + 127) / 128, j.a_square ? 7 : 0};
     const Operand B{static_cast<const uint8_t*>(j.b), j.ldb, j.n, j.scale_b, (j.k + 127) / 128, j.b_square ? 7 : 0};
     const int64_t tm = (j.m + C::TL - 1) / C::TL, tn = (j.n + C::TR - 1) / C::TR;
     if (tm > 0x7fffffff / C::NT / tn) return hipErrorInvalidValue;
-    const int esz = j.bf16c ? 2 : 4;
-    const int vec = j.n * esz % 16 == 0 && reinterpret_cast<uintptr_t>(j.c) % 16 == 0;
-    hipLaunchKernelGGL(k_gemm_f8<C>, dim3(static_cast<unsigned>(tm * tn)), dim3(C::NT), 0, stream, A, B, j.c, j.n, j.k,
-                       static_cast<uint32_t>(tm), j.bf16c ? 1 : 0, vec);
+    const int vec = j.n * static_cast<int64_t>(sizeof(CT)) % 16 == 0 && reinterpret_cast<uintptr_t>(j.c) % 16 == 0;
+    hipLaunchKernelGGL((k_gemm_f8<C, CT>), dim3(static_cast<unsigned>(tm * tn)), dim3(C::NT), 0, stream, A, B,
+                       static_cast<CT*>(j.c), j.n, j.k, static_cast<uint32_t>(tm), vec);
     return hipGetLastError();
+}
+
+// A bf16 result takes the one-byte instruction, whose dropped bits are a
+// hundredth of the rounding to bf16; an fp32 result is asked for its bits and
+// takes the bf16 instruction on widened operands.
+template <int LT, int RT, int SC>
+hipError_t launch_typed(const GemmF8Job& j, hipStream_t stream) {
+    return j.bf16c ? launch_tiles<kF8, LT, RT, SC, __bf16>(j, stream) : launch_tiles<kF8Wide, LT, RT, SC, float>(j, stream);
 }
 
 template <int SC>

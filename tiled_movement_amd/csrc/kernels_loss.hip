@@ -1,0 +1,619 @@
+// Losses of an output layer whose logits z = H W^T are never kept: softmax
+// cross entropy against one word a row, and distillation from a teacher's top
+// logits, with their gradients.
+//
+//   lse_i  = log sum_v exp(z_iv / tau)
+//   loss_i = tau^2 sum_j p_ij (log p_ij - (z_{i,t_ij} / tau - lse_i))
+//   dz_iv  = g_i tau (exp(z_iv / tau - lse_i) - sum_{j: t_ij = v} p_ij)
+//   dH = dz W,  dW = dz^T H
+//
+// with p_i the softmax of the row's teacher logits over tau; cross entropy is
+// one entry with p = 1 and tau = 1.
+//
+// Forward: the logits of a 256 x 256 tile stay in accumulators, and a tile
+// leaves only each row's maximum and sum of exponentials (8 bytes per row and
+// 256 words); a second kernel joins them.  The few logits at listed words are
+// dot products of their own.  Bound by the bf16 / fp16 matrix rate.
+//
+// Backward, a piece of the vocabulary at a time: the piece's logits again, dz
+// from them and the saved lse, then both gradient products.  Their operands
+// have to be contiguous along the summed axis, so dz, W's piece and H are
+// transposed through LDS on the way (3% of the time at 4096 x 65536 x 4096).
+//
+// Rounding: dz is held in fp16 (2^-11), not bf16 (2^-8), because the result
+// is rounded to its own type once more and a bf16 dz would add an error of
+// the same size.  Taken out of it first are max_i |g_i tau| (a mean's 1/n has
+// no rounding left then) and a factor of 2^14, which puts probabilities down
+// to 2^-28 in the normal range.  bf16 H and W are widened to fp16 by a power
+// of two that puts their largest value just below 2^15: exact for all values
+// down to 2^-29 of the largest, and off by at most 2^-40 of it below that.
+#include "launch.h"
+#include "mma_core.h"
+
+namespace swz {
+namespace {
+
+using namespace mma;
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kDzScale = 16384.f;
+constexpr int kSlots = 3;  // maxima, as bits: 0 |H|, 1 |W|, 2 |g tau|
+
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ float half_bits_to_f32(uint16_t b, bool bf16) {
+    return bf16 ? __uint_as_float(static_cast<uint32_t>(b) << 16)
+                : static_cast<float>(__builtin_bit_cast(_Float16, b));
+}
+
+// ------------------------------------------------------------------ forward
+// Rows [i0, i0 + TL) against words [j0, j0 + TR): part[tile][row] = (maximum,
+// sum of 2^(t - maximum)) of t = z log2(e) / tau.
+template <class C>
+__global__ __launch_bounds__(C::NT) void k_logit_stats(Operand H, Operand W, int64_t kbytes, float c2,
+                                                       float2* __restrict__ part, uint32_t tiles_m) {
+    __shared__ i32x4 lds_v[C::kLds / 16];
+    lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
+    const int64_t tn = blockIdx.x / tiles_m;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x % tiles_m) * C::TL, j0 = tn * C::TR;
+    f32x4 acc[C::BL][C::BR];
+    tile_product<C>(acc, H, W, i0, j0, kbytes, lds);
+    const int t = threadIdx.x, lane = t % 64, g = lane / 16, l16 = lane % 16;
+    const int wave = __builtin_amdgcn_readfirstlane(t / 64), wl = wave / C::WR, wr = wave % C::WR;
+    lds_f32* red = (lds_f32*)lds;  // [2][WR][TL]
+    const bool whole = j0 + C::TR <= W.rows;
+    const int64_t jw = j0 + wr * C::BR * 16 + 4 * g;
+#pragma unroll
+    for (int x = 0; x < C::BL; ++x) {
+        float m = -__builtin_inff();
+#pragma unroll
+        for (int y = 0; y < C::BR; ++y)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v = acc[x][y][i] * c2;
+                if (!whole && jw + 16 * y + i >= W.rows) v = -__builtin_inff();
+                acc[x][y][i] = v;
+                m = fmaxf(m, v);
+            }
+        m = fmaxf(m, __shfl_xor(m, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        const float mm = m == -__builtin_inff() ? 0.f : m;  // no words here: a sum of zeros
+        float s = 0.f;
+#pragma unroll
+        for (int y = 0; y < C::BR; ++y)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s += __builtin_amdgcn_exp2f(acc[x][y][i] - mm);
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if (g == 0) {
+            red[wr * C::TL + (wl * C::BL + x) * 16 + l16] = m;
+            red[(C::WR + wr) * C::TL + (wl * C::BL + x) * 16 + l16] = s;
+        }
+    }
+    __syncthreads();
+    for (int r = t; r < C::TL; r += C::NT) {
+        if (i0 + r >= H.rows) continue;
+        float m = red[r];
+#pragma unroll
+        for (int w = 1; w < C::WR; ++w) m = fmaxf(m, red[w * C::TL + r]);
+        const float mm = m == -__builtin_inff() ? 0.f : m;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < C::WR; ++w) s += red[(C::WR + w) * C::TL + r] * __builtin_amdgcn_exp2f(red[w * C::TL + r] - mm);
+        part[tn * H.rows + i0 + r] = make_float2(m, s);
+    }
+}
+
+// lse from the pieces: 32 rows a workgroup, eight threads a row.
+__global__ __launch_bounds__(256) void k_join_stats(const float2* __restrict__ part, int64_t tiles, int64_t n,
+                                                    float* __restrict__ lse) {
+    __shared__ float2 red[8][32];
+    const int r = threadIdx.x % 32, sub = threadIdx.x / 32;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + r;
+    float m = -__builtin_inff(), s = 0.f;
+    if (row < n) {
+#pragma unroll 4
+        for (int64_t i = sub; i < tiles; i += 8) {
+            const float2 p = part[i * n + row];
+            const float big = fmaxf(m, p.x);
+            const float b = big == -__builtin_inff() ? 0.f : big;
+            s = s * __builtin_amdgcn_exp2f(m - b) + p.y * __builtin_amdgcn_exp2f(p.x - b);
+            m = big;
+        }
+    }
+    red[sub][r] = make_float2(m, s);
+    __syncthreads();
+    if (sub == 0 && row < n) {
+        for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i][r].x);
+        const float b = m == -__builtin_inff() ? 0.f : m;
+        float total = 0.f;
+        for (int i = 0; i < 8; ++i) total += red[i][r].y * __builtin_amdgcn_exp2f(red[i][r].x - b);
+        lse[row] = m * kLn2 + logf(total);
+    }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+
+// Whether entry j of a row counts: its word exists and its teacher logit is
+// not the lowest.
+__device__ __forceinline__ bool entry_counts(int64_t word, float teacher, int64_t v) {
+    return word >= 0 && word < v && teacher != -__builtin_inff();
+}
+
+// One workgroup a row: the logits at its listed words, then its loss.
+__global__ __launch_bounds__(256) void k_target_loss(const uint16_t* __restrict__ h, const uint16_t* __restrict__ w,
+                                                     const int64_t* __restrict__ index,
+                                                     const float* __restrict__ teacher, int64_t v, int64_t k, int top,
+                                                     float tau, int bf16, const float* __restrict__ lse,
+                                                     float* __restrict__ zt, float* __restrict__ loss) {
+    __shared__ float z[kMaxTop];
+    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, waves = blockDim.x / 64;
+    const uint16_t* hr = h + row * k;
+    for (int j = wave; j < top; j += waves) {
+        const int64_t word = index[row * top + j];
+        float s = 0.f;
+        if (entry_counts(word, teacher ? teacher[row * top + j] : 0.f, v)) {
+            const uint16_t* wr = w + word * k;
+#pragma unroll 4
+            for (int64_t c = 8 * lane; c < k; c += 512) {
+                const u16x8 a = *reinterpret_cast<const u16x8*>(hr + c), b = *reinterpret_cast<const u16x8*>(wr + c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s = fmaf(half_bits_to_f32(a[i], bf16), half_bits_to_f32(b[i], bf16), s);
+            }
+            s = wave_sum(s);
+        }
+        if (lane == 0) {
+            z[j] = s;
+            zt[row * top + j] = s;
+        }
+    }
+    __syncthreads();
+    if (wave != 0) return;
+    const float l = lse[row];
+    float out = 0.f;
+    if (!teacher) {
+        const int64_t word = index[row];
+        out = word >= 0 && word < v ? l - z[0] : 0.f;
+    } else {
+        float m = -__builtin_inff();
+        bool any = false;
+        for (int j = lane; j < top; j += 64) {
+            const float t = teacher[row * top + j];
+            if (entry_counts(index[row * top + j], t, v)) m = fmaxf(m, t / tau), any = true;
+        }
+        if (__any(any)) {
+            m = wave_max(m);
+            float s = 0.f;
+            for (int j = lane; j < top; j += 64) {
+                const float t = teacher[row * top + j];
+                if (entry_counts(index[row * top + j], t, v)) s += expf(t / tau - m);
+            }
+            const float ls = logf(wave_sum(s));
+            for (int j = lane; j < top; j += 64) {
+                const float t = teacher[row * top + j];
+                if (!entry_counts(index[row * top + j], t, v)) continue;
+                const float lp = t / tau - m - ls, p = expf(lp);
+                out += p > 0.f || p != p ? p * (lp - (z[j] / tau - l)) : 0.f;
+            }
+            out = tau * tau * wave_sum(out);
+        }
+    }
+    if (lane == 0) loss[row] = out;
+}
+
+// ----------------------------------------------------------------- backward
+__global__ void k_clear_slots(uint32_t* slots) {
+    if (threadIdx.x < kSlots) slots[threadIdx.x] = 0;
+}
+
+// Largest finite magnitude of a bf16 array, as fp32 bits (the order of
+// atomic maxima does not matter).
+__global__ __launch_bounds__(256) void k_absmax(const uint16_t* __restrict__ x, int64_t pieces, uint32_t* slot) {
+    uint32_t m = 0;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+#pragma unroll 4
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < pieces; i += step) {
+        const u16x8 a = reinterpret_cast<const u16x8*>(x)[i];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t b = a[e] & 0x7fffu;
+            m = max(m, b < 0x7f80u ? b : 0u);
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d)));
+    if (threadIdx.x % 64 == 0) atomicMax(slot, m << 16);
+}
+
+// The power of two that takes a largest magnitude (bits) just below 2^15, as
+// its exponent; 0 where nothing was measured.
+__device__ __forceinline__ int widen_exponent(uint32_t bits) {
+    if (bits == 0) return 0;
+    const int e = 14 - (static_cast<int>(bits >> 23) - 127);  // subnormals: bits >> 23 == 0
+    return e < -113 ? -113 : e > 126 ? 126 : e;
+}
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Per row: the entries' weights with equal words joined (each holds the sum,
+// so writing it twice writes the same), and g tau, 0 for rows that do not
+// count.  One wave a row.
+__global__ __launch_bounds__(64) void k_loss_prep(const int64_t* __restrict__ index, const float* __restrict__ teacher,
+                                                  const float* __restrict__ upstream, int64_t v, int top, float tau,
+                                                  float* __restrict__ weight, float* __restrict__ g, uint32_t* slot) {
+    __shared__ float p[kMaxTop];
+    __shared__ int64_t words[kMaxTop];
+    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x;
+    bool any = false;
+    if (!teacher) {
+        any = index[row] >= 0 && index[row] < v;
+        if (lane == 0) weight[row] = any ? 1.f : 0.f;
+    } else {
+        float m = -__builtin_inff();
+        for (int j = lane; j < top; j += 64) {
+            const float t = teacher[row * top + j];
+            if (entry_counts(index[row * top + j], t, v)) m = fmaxf(m, t / tau), any = true;
+        }
+        any = __any(any);
+        m = wave_max(m);
+        float s = 0.f;
+        for (int j = lane; j < top; j += 64) {
+            const float t = teacher[row * top + j];
+            const bool here = entry_counts(index[row * top + j], t, v);
+            const float e = here ? expf(t / tau - m) : 0.f;
+            words[j] = here ? index[row * top + j] : -1;
+            p[j] = e;
+            s += e;
+        }
+        s = wave_sum(s);
+        __syncthreads();
+        for (int j = lane; j < top; j += 64) {
+            float sum = 0.f;
+            for (int i = 0; i < top; ++i) sum += words[i] == words[j] ? p[i] : 0.f;
+            weight[row * top + j] = any ? sum / s : 0.f;
+        }
+    }
+    if (lane == 0) {
+        const float gt = any ? upstream[row] * tau : 0.f;
+        g[row] = gt;
+        const uint32_t b = __float_as_uint(gt) & 0x7fffffffu;
+        if (b && b < 0x7f800000u) atomicMax(slot, b);
+    }
+}
+
+// g_i tau over the largest of them, times 2^14.
+__device__ __forceinline__ float row_factor(float g, uint32_t gmax) {
+    return g == 0.f ? 0.f : g / __uint_as_float(gmax) * kDzScale;
+}
+
+// A 128 x 128 tile of 2-byte values transposed through LDS: in [rows][ldin]
+// to fp16 [cols][ldout], times the power of two of `slot` (bf16 input) or as
+// they are (fp16).  Thread (i, h) takes the 8 x 8 block of columns 8i and rows
+// 8h, so each of its columns is one 16-byte piece of an output row; piece h
+// of output row c sits at slot h ^ (c / 8) of the row's 16 (Swizzle<4,0,7> on
+// slots), which spreads the 16 rows that 16 lanes write over all 64 banks.
+// Rows whose factor g is 0 become zeros: they may hold anything, and their
+// zeros in dz would not cancel a NaN.  ldin, ldout: elements, multiples of 8; pieces behind `rows` are written into
+// the output's padding (at most 7 elements, inside ldout).
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_transpose16(const uint16_t* __restrict__ in, int64_t ldin, int64_t rows,
+                                                     int64_t cols, uint16_t* __restrict__ out, int64_t ldout,
+                                                     int64_t tiles_c, const uint32_t* __restrict__ slot,
+                                                     const float* __restrict__ g) {
+    __shared__ u16x8 tile[128 * 16];
+    const int t = threadIdx.x, i = t % 16, h = t / 16;
+    const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
+    const int64_t r0 = tr * 128, c0 = tc * 128;
+    u16x8 v[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const int64_t r = r0 + 8 * h + p, c = c0 + 8 * i;
+        v[p] = r < rows && c < cols && (!g || g[r] != 0.f) ? *reinterpret_cast<const u16x8*>(in + r * ldin + c)
+                                                           : u16x8{0, 0, 0, 0, 0, 0, 0, 0};
+    }
+    if constexpr (BF16) {
+        const float f = pow2f(widen_exponent(*slot));
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[p][e] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(half_bits_to_f32(v[p][e], true) * f));
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        u16x8 o;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) o[p] = v[p][e];
+        tile[(8 * i + e) * 16 + (h ^ i)] = o;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = t; u < 128 * 16; u += 256) {
+        const int c = u / 16, s = u % 16;
+        const int64_t r = r0 + 8 * s;
+        if (c0 + c < cols && r < rows)
+            *reinterpret_cast<u16x8*>(out + (c0 + c) * ldout + r) = tile[c * 16 + (s ^ (c / 8))];
+    }
+}
+
+// dz of words [j0, ...) of a piece (W starts at the piece): fp16 [rows][ldz].
+template <class C>
+__global__ __launch_bounds__(C::NT) void k_dz(Operand H, Operand W, int64_t kbytes, float c2,
+                                              const float* __restrict__ lse, const float* __restrict__ g,
+                                              const uint32_t* __restrict__ slots, _Float16* __restrict__ dz, int64_t ldz,
+                                              uint32_t tiles_m) {
+    __shared__ i32x4 lds_v[C::kLds / 16];
+    lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x % tiles_m) * C::TL;
+    const int64_t j0 = static_cast<int64_t>(blockIdx.x / tiles_m) * C::TR;
+    f32x4 acc[C::BL][C::BR];
+    tile_product<C>(acc, H, W, i0, j0, kbytes, lds);
+    const int t = threadIdx.x, lane = t % 64, l16 = lane % 16;
+    const int wave = __builtin_amdgcn_readfirstlane(t / 64), wl = wave / C::WR, wr = wave % C::WR;
+    const uint32_t gmax = slots[2];
+#pragma unroll
+    for (int x = 0; x < C::BL; ++x) {
+        int64_t row = i0 + (wl * C::BL + x) * 16 + l16;
+        row = row < H.rows ? row : H.rows - 1;
+        const float f = row_factor(g[row], gmax), l2 = lse[row] * kLog2e;
+#pragma unroll
+        for (int y = 0; y < C::BR; ++y)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[x][y][i], c2, -l2));
+                acc[x][y][i] = f == 0.f ? 0.f : p * f;
+            }
+    }
+    // whole 16-byte pieces: ldz is a multiple of 8, and what a last piece
+    // writes behind the piece's words is not read
+    const int64_t cols = (W.rows + 7) / 8 * 8;
+    store_tile<C>(acc, (lds_f32*)(lds + wave * C::kSlice), dz, ldz, i0 + wl * C::BL * 16, j0 + wr * C::BR * 16, H.rows,
+                  cols, true, lane, [](float v) { return v; });
+}
+
+// dz at the listed words of a piece: the one place where the target's weight
+// enters, so its difference from the softmax is rounded once.
+__global__ __launch_bounds__(256) void k_dz_targets(const int64_t* __restrict__ index, const float* __restrict__ weight,
+                                                    const float* __restrict__ zt, const float* __restrict__ lse,
+                                                    const float* __restrict__ g, const uint32_t* __restrict__ slots,
+                                                    int64_t n, int top, float c2, int64_t v0, int64_t vc, int64_t v,
+                                                    const float* __restrict__ teacher, _Float16* __restrict__ dz,
+                                                    int64_t ldz) {
+    const int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (u >= n * top) return;
+    const int64_t row = u / top, word = index[u];
+    if (!entry_counts(word, teacher ? teacher[u] : 0.f, v) || word < v0 || word >= v0 + vc) return;
+    const float f = row_factor(g[row], slots[2]);
+    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(zt[u], c2, -lse[row] * kLog2e));
+    dz[row * ldz + word - v0] = static_cast<_Float16>(f == 0.f ? 0.f : (p - weight[u]) * f);
+}
+
+// dW of a piece: rows are words (L = dz^T), columns k (R = H^T).
+template <class C, class CT>
+__global__ __launch_bounds__(C::NT) void k_grad_w(Operand Z, Operand H, int64_t kbytes, CT* __restrict__ dw, int64_t k,
+                                                  const uint32_t* __restrict__ slots, uint32_t tiles_n) {
+    __shared__ i32x4 lds_v[C::kLds / 16];
+    lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x / tiles_n) * C::TL;
+    const int64_t j0 = static_cast<int64_t>(blockIdx.x % tiles_n) * C::TR;
+    f32x4 acc[C::BL][C::BR];
+    tile_product<C>(acc, Z, H, i0, j0, kbytes, lds);
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const float back = pow2f(-widen_exponent(slots[0])), gmax = __uint_as_float(slots[2]) / kDzScale;
+    store_tile<C>(acc, (lds_f32*)(lds + wave * C::kSlice), dw, k, i0 + wave / C::WR * C::BL * 16,
+                  j0 + wave % C::WR * C::BR * 16, Z.rows, H.rows, true, lane,
+                  [=](float v) { return v * back * gmax; });
+}
+
+// dH's sum over a part of a piece's words into its own fp32 buffer (blockIdx.y).
+template <class C>
+__global__ __launch_bounds__(C::NT) void k_grad_h(Operand Z, Operand W, int64_t kbytes, int64_t part_bytes,
+                                                  float* __restrict__ sums, int add, uint32_t tiles_m) {
+    __shared__ i32x4 lds_v[C::kLds / 16];
+    lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x % tiles_m) * C::TL;
+    const int64_t j0 = static_cast<int64_t>(blockIdx.x / tiles_m) * C::TR;
+    const int64_t k0 = static_cast<int64_t>(blockIdx.y) * part_bytes;
+    int64_t kb = kbytes - k0 < part_bytes ? kbytes - k0 : part_bytes;
+    if (kb < 0) kb = 0;
+    Z.data += kb ? k0 : 0;
+    W.data += kb ? k0 : 0;
+    f32x4 acc[C::BL][C::BR];
+    tile_product<C>(acc, Z, W, i0, j0, kb, lds);
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int64_t k = W.rows, n = Z.rows, wi = i0 + wave / C::WR * C::BL * 16, wj = j0 + wave % C::WR * C::BR * 16;
+    float* out = sums + static_cast<int64_t>(blockIdx.y) * n * k;
+    // k is a multiple of 8, so a lane's four columns are inside or outside together
+    const int g = lane / 16, l16 = lane % 16;
+#pragma unroll
+    for (int x = 0; x < C::BL; ++x)
+#pragma unroll
+        for (int y = 0; y < C::BR; ++y) {
+            const int64_t r = wi + 16 * x + l16, c = wj + 16 * y + 4 * g;
+            if (r >= n || c >= k) continue;
+            f32x4* p = reinterpret_cast<f32x4*>(out + r * k + c);
+            *p = add ? *p + acc[x][y] : acc[x][y];
+        }
+}
+
+template <class CT>
+__global__ __launch_bounds__(256) void k_finish_h(const float* __restrict__ sums, int parts, int64_t quads,
+                                                  const uint32_t* __restrict__ slots, CT* __restrict__ dh) {
+    typedef CT ct4 __attribute__((ext_vector_type(4)));
+    const int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (u >= quads) return;
+    f32x4 s = reinterpret_cast<const f32x4*>(sums)[u];
+    for (int p = 1; p < parts; ++p) s += reinterpret_cast<const f32x4*>(sums)[p * quads + u];
+    const float back = pow2f(-widen_exponent(slots[1])), gmax = __uint_as_float(slots[2]) / kDzScale;
+    ct4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = static_cast<CT>(s[i] * back * gmax);
+    reinterpret_cast<ct4*>(dh)[u] = o;
+}
+
+__global__ __launch_bounds__(256) void k_zero16(uint32_t* __restrict__ p, int64_t words) {
+    const int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (u < words) p[u] = 0;
+}
+
+unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); }
+
+// Tile of rows (tokens) x words.  Fewer rows than a 256-row tile leave its
+// instructions idle: 64- and 128-row tiles take over where they cover the rows.
+template <int ELEM> using Big = Config<ELEM, 0, 0, kNoScale, 4, 2, 4, 8>;
+template <int ELEM> using Mid = Config<ELEM, 0, 0, kNoScale, 2, 4, 4, 4>;
+template <int ELEM> using Low = Config<ELEM, 0, 0, kNoScale, 1, 8, 4, 2>;
+
+template <int ELEM, class F>
+hipError_t by_rows_of(int64_t n, F f) {
+    if (n <= 64) return f(Low<ELEM>{});
+    if (n <= 128) return f(Mid<ELEM>{});
+    return f(Big<ELEM>{});
+}
+template <class F>
+hipError_t by_rows(int64_t n, bool bf16, F f) {
+    return bf16 ? by_rows_of<kBf16>(n, f) : by_rows_of<kF16>(n, f);
+}
+
+hipError_t transpose16(const void* in, int64_t ldin, int64_t rows, int64_t cols, uint16_t* out, int64_t ldout, bool bf16,
+                       const uint32_t* slot, const float* g, hipStream_t stream) {
+    const int64_t tc = (cols + 127) / 128, tr = (rows + 127) / 128;
+    const dim3 grid(static_cast<unsigned>(tc * tr));
+    const auto* x = static_cast<const uint16_t*>(in);
+    if (bf16)
+        hipLaunchKernelGGL(k_transpose16<true>, grid, dim3(256), 0, stream, x, ldin, rows, cols, out, ldout, tc, slot, g);
+    else
+        hipLaunchKernelGGL(k_transpose16<false>, grid, dim3(256), 0, stream, x, ldin, rows, cols, out, ldout, tc, slot, g);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_loss(const LossJob& j, hipStream_t stream) {
+    const auto* h = static_cast<const uint8_t*>(j.h);
+    const auto* w = static_cast<const uint8_t*>(j.w);
+    auto* part = reinterpret_cast<float2*>(static_cast<uint8_t*>(j.ws));
+    const Operand H{h, 2 * j.k, j.n, nullptr, 0, 0}, W{w, 2 * j.k, j.v, nullptr, 0, 0};
+    const float c2 = kLog2e / j.tau;
+    int64_t tiles = 0;
+    const hipError_t e = by_rows(j.n, j.bf16, [&](auto cfg) {
+        using C = decltype(cfg);
+        const int64_t tm = (j.n + C::TL - 1) / C::TL;
+        tiles = (j.v + C::TR - 1) / C::TR;
+        hipLaunchKernelGGL(k_logit_stats<C>, dim3(static_cast<unsigned>(tm * tiles)), dim3(C::NT), 0, stream, H, W, 2 * j.k,
+                           c2, part, static_cast<uint32_t>(tm));
+        return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_join_stats, dim3(blocks_of(j.n, 32)), dim3(256), 0, stream, part, tiles, j.n, j.lse);
+    hipLaunchKernelGGL(k_target_loss, dim3(static_cast<unsigned>(j.n)), dim3(64 * (j.top < 4 ? j.top : 4)), 0, stream,
+                       static_cast<const uint16_t*>(j.h), static_cast<const uint16_t*>(j.w), j.index, j.teacher, j.v, j.k,
+                       j.top, j.tau, j.bf16 ? 1 : 0, j.lse, j.zt, j.loss);
+    return hipGetLastError();
+}
+
+hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t stream) {
+    auto* ws = static_cast<uint8_t*>(j.ws);
+    if (j.n == 0) {  // no rows: the weights' gradient is zero (v k is a multiple of 8)
+        if (j.dw) {
+            const int64_t words = j.v * j.k / 2;
+            hipLaunchKernelGGL(k_zero16, dim3(blocks_of(words, 256)), dim3(256), 0, stream, static_cast<uint32_t*>(j.dw), words);
+        }
+        return hipGetLastError();
+    }
+    auto* slots = reinterpret_cast<uint32_t*>(ws + p.slots);
+    auto* g = reinterpret_cast<float*>(ws + p.g);
+    auto* weight = reinterpret_cast<float*>(ws + p.weight);
+    auto* dz = reinterpret_cast<_Float16*>(ws + p.dz);
+    auto* dzt = reinterpret_cast<uint16_t*>(ws + p.dzt);
+    auto* ht = reinterpret_cast<uint16_t*>(ws + p.ht);
+    auto* wt = reinterpret_cast<uint16_t*>(ws + p.wt);
+    auto* sums = reinterpret_cast<float*>(ws + p.sums);
+    const float c2 = kLog2e / j.tau;
+    const int64_t ldn = (j.n + 7) / 8 * 8;
+    hipLaunchKernelGGL(k_clear_slots, dim3(1), dim3(64), 0, stream, slots);
+    if (j.bf16) {
+        auto absmax = [&](const void* x, int64_t elems, int slot) {
+            const int64_t pieces = elems / 8;
+            const unsigned grid = pieces > 2048 * 256 ? 2048u : blocks_of(pieces, 256);
+            hipLaunchKernelGGL(k_absmax, dim3(grid), dim3(256), 0, stream, static_cast<const uint16_t*>(x), pieces, slots + slot);
+        };
+        if (j.dw) absmax(j.h, j.n * j.k, 0);
+        if (j.dh) absmax(j.w, j.v * j.k, 1);
+    }
+    hipLaunchKernelGGL(k_loss_prep, dim3(static_cast<unsigned>(j.n)), dim3(64), 0, stream, j.index, j.teacher, j.upstream, j.v,
+                       j.top, j.tau, weight, g, slots + 2);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && j.dw) e = transpose16(j.h, j.k, j.n, j.k, ht, ldn, j.bf16, slots, g, stream);
+    for (int64_t v0 = 0; v0 < j.v && e == hipSuccess; v0 += p.piece) {
+        const int64_t vc = j.v - v0 < p.piece ? j.v - v0 : p.piece, ldz = (vc + 7) / 8 * 8;
+        const uint8_t* wp = static_cast<const uint8_t*>(j.w) + v0 * j.k * 2;
+        const Operand H{static_cast<const uint8_t*>(j.h), 2 * j.k, j.n, nullptr, 0, 0}, W{wp, 2 * j.k, vc, nullptr, 0, 0};
+        e = by_rows(j.n, j.bf16, [&](auto cfg) {
+            using C = decltype(cfg);
+            const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (vc + C::TR - 1) / C::TR;
+            hipLaunchKernelGGL(k_dz<C>, dim3(static_cast<unsigned>(tm * tn)), dim3(C::NT), 0, stream, H, W, 2 * j.k, c2, j.lse,
+                               g, slots, dz, ldz, static_cast<uint32_t>(tm));
+            return hipGetLastError();
+        });
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(k_dz_targets, dim3(blocks_of(j.n * j.top, 256)), dim3(256), 0, stream, j.index, weight, j.zt, j.lse, g,
+                           slots, j.n, j.top, c2, v0, vc, j.v, j.teacher, dz, ldz);
+        if (j.dw) {
+            e = transpose16(dz, ldz, j.n, vc, dzt, ldn, false, nullptr, nullptr, stream);
+            if (e != hipSuccess) return e;
+            using C = Big<kF16>;
+            const Operand Z{reinterpret_cast<const uint8_t*>(dzt), 2 * ldn, vc, nullptr, 0, 0};
+            const Operand HT{reinterpret_cast<const uint8_t*>(ht), 2 * ldn, j.k, nullptr, 0, 0};
+            const int64_t tm = (vc + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
+            const dim3 grid(static_cast<unsigned>(tm * tn));
+            const auto t_n = static_cast<uint32_t>(tn);
+            if (j.bf16)
+                hipLaunchKernelGGL((k_grad_w<C, __bf16>), grid, dim3(C::NT), 0, stream, Z, HT, 2 * j.n,
+                                   static_cast<__bf16*>(j.dw) + v0 * j.k, j.k, slots, t_n);
+            else
+                hipLaunchKernelGGL((k_grad_w<C, _Float16>), grid, dim3(C::NT), 0, stream, Z, HT, 2 * j.n,
+                                   static_cast<_Float16*>(j.dw) + v0 * j.k, j.k, slots, t_n);
+            e = hipGetLastError();
+        }
+        if (j.dh && e == hipSuccess) {
+            e = transpose16(wp, j.k, vc, j.k, wt, ldz, j.bf16, slots + 1, nullptr, stream);
+            if (e != hipSuccess) return e;
+            const Operand Z{reinterpret_cast<const uint8_t*>(dz), 2 * ldz, j.n, nullptr, 0, 0};
+            const Operand WT{reinterpret_cast<const uint8_t*>(wt), 2 * ldz, j.k, nullptr, 0, 0};
+            // whole stages of 128 bytes a part
+            const int64_t part_bytes = ((2 * vc + 127) / 128 + p.parts - 1) / p.parts * 128;
+            e = by_rows_of<kF16>(j.n, [&](auto cfg) {
+                using C = decltype(cfg);
+                const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
+                hipLaunchKernelGGL(k_grad_h<C>, dim3(static_cast<unsigned>(tm * tn), static_cast<unsigned>(p.parts)), dim3(C::NT), 0,
+                                   stream, Z, WT, 2 * vc, part_bytes, sums, v0 > 0 ? 1 : 0, static_cast<uint32_t>(tm));
+                return hipGetLastError();
+            });
+        }
+    }
+    if (e == hipSuccess && j.dh) {
+        const int64_t quads = j.n * j.k / 4;
+        const dim3 grid(blocks_of(quads, 256));
+        if (j.bf16)
+            hipLaunchKernelGGL(k_finish_h<__bf16>, grid, dim3(256), 0, stream, sums, static_cast<int>(p.parts), quads, slots,
+                               static_cast<__bf16*>(j.dh));
+        else
+            hipLaunchKernelGGL(k_finish_h<_Float16>, grid, dim3(256), 0, stream, sums, static_cast<int>(p.parts), quads, slots,
+                               static_cast<_Float16*>(j.dh));
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+}  // namespace swz

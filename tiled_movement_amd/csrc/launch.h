@@ -79,6 +79,31 @@ struct GemmF8Job {
     bool a_e5m2, b_e5m2, a_square, b_square, e8m0, bf16c;
 };
 hipError_t launch_gemm_f8(const GemmF8Job& job, hipStream_t stream);
+
+// swz_linear_ce, swz_linear_distill and their gradients.  teacher ==
+// nullptr: cross entropy (top 1, tau 1).
+constexpr int kMaxTop = 256;
+struct LossJob {
+    const void *h, *w;  // bf16 or fp16 [n][k], [v][k]
+    bool bf16;
+    int64_t n, v, k;
+    const int64_t* index;  // [n][top]
+    const float* teacher;  // [n][top]
+    int top;
+    float tau;
+    float *loss, *lse, *zt;  // the gradient reads lse and zt
+    const float* upstream;   // [n]
+    void *dh, *dw;           // either may be nullptr
+    void* ws;
+};
+// Workspace of the gradient: byte offsets, words of a piece of the
+// vocabulary, and the parts that dH's sum over a piece is split into.
+struct LossPlan {
+    int64_t slots, g, weight, dz, dzt, ht, wt, sums, bytes;
+    int64_t piece, parts;
+};
+hipError_t launch_loss(const LossJob& job, hipStream_t stream);
+hipError_t launch_loss_grad(const LossJob& job, const LossPlan& plan, hipStream_t stream);
 hipError_t launch_map(const int32_t* in, int32_t* out, int64_t n, swz_params p, hipStream_t stream);
 
 // Up to kMapBatch triples of one batched-map launch, passed by value.

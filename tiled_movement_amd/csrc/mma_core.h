@@ -43,7 +43,13 @@ typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 typedef __attribute__((address_space(3))) uint32_t lds_u32;
 typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
 
-enum Elem { kBf16, kF16, kF8 };
+// kF8Wide: one-byte operands widened to bf16 in registers (exact) and
+// multiplied by the bf16 instruction, at its rate.  The one-byte instructions
+// align the products of each group of eight values of k to the largest and
+// keep about 13 bits below it: 1.5e-5 of the result's norm on normal
+// operands (16x16x32 and 16x16x128 alike), against 4e-8 for bf16.
+enum Elem { kBf16, kF16, kF8, kF8Wide };
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 // Scales of one-byte operands, one per row (or 128 rows) and stage: none;
 // powers of two as exponent bytes, applied by the matrix instruction; fp32,
 // applied to the stage's product (kF32Square: R's scale is the same for all
@@ -68,7 +74,9 @@ struct Config {
     static constexpr int NT = 64 * WL * WR;
     static constexpr int TL = 16 * WL * BL, TR = 16 * WR * BR;
     static constexpr int kBuf = (TL + TR) * 128;
-    static constexpr int kScaleBuf = SC == kNoScale ? 0 : SC == kE8M0 ? (TL + TR + 63) / 64 * 64 : (TL + TR) * 4;
+    // E8M0 scales for the one-byte instruction stay bytes, the others are fp32
+    static constexpr bool kScaleBytes = SC == kE8M0 && ELEM == kF8;
+    static constexpr int kScaleBuf = SC == kNoScale ? 0 : kScaleBytes ? (TL + TR + 63) / 64 * 64 : (TL + TR) * 4;
     static constexpr int kMain = 2 * (kBuf + kScaleBuf);
     // a wave's slice of the epilogue: 16 rows of C, padded by 16 bytes
     static constexpr int kPitch = 16 * BR + 4;
@@ -169,7 +177,9 @@ struct Stager {
             for (int i = 0; i < C::NS; ++i) {
                 const int e = t + C::NT * i;
                 if (C::NS * C::NT == C::TL + C::TR || e < C::TL + C::TR) {
-                    if constexpr (C::SC == kE8M0)
+                    if constexpr (C::SC == kE8M0 && !C::kScaleBytes)
+                        reinterpret_cast<lds_u32*>(sbuf)[e] = sv[i] == 255 ? 0x7fc00000u : sv[i] ? sv[i] << 23 : 0x400000u;
+                    else if constexpr (C::kScaleBytes)
                         sbuf[e / 64 * 64 + e % 16 * 4 + e / 16 % 4] = static_cast<uint8_t>(sv[i]);
                     else
                         reinterpret_cast<lds_u32*>(sbuf)[e] = sv[i];
@@ -218,6 +228,16 @@ __device__ __forceinline__ f32x4 mfma_e8m0_r(i32x8 r, i32x8 l, f32x4 c, int sr, 
     }
 }
 
+// The stage's two 16x16x32 products of bf16 fragments.
+__device__ __forceinline__ f32x4 mfma_bf16_pair(i32x8 r, i32x8 l, f32x4 acc) {
+    const i32x4 r0 = __builtin_shufflevector(r, r, 0, 1, 2, 3), r1 = __builtin_shufflevector(r, r, 4, 5, 6, 7);
+    const i32x4 l0 = __builtin_shufflevector(l, l, 0, 1, 2, 3), l1 = __builtin_shufflevector(l, l, 4, 5, 6, 7);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r0), __builtin_bit_cast(bf16x8, l0), acc, 0,
+                                                  0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r1), __builtin_bit_cast(bf16x8, l1), acc, 0,
+                                                   0, 0);
+}
+
 // Adds one stage's product of block fragments: r rows (registers), l columns
 // (lanes).  ol, orr: bytes of the scale words (constants after unrolling).
 template <class C>
@@ -244,14 +264,11 @@ __device__ __forceinline__ void mma_stage(f32x4& acc, i32x8 r, i32x8 l, int sr, 
             }
         }
     } else {
-        const i32x4 r0 = __builtin_shufflevector(r, r, 0, 1, 2, 3), r1 = __builtin_shufflevector(r, r, 4, 5, 6, 7);
-        const i32x4 l0 = __builtin_shufflevector(l, l, 0, 1, 2, 3), l1 = __builtin_shufflevector(l, l, 4, 5, 6, 7);
         if constexpr (C::ELEM == kBf16) {
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r0), __builtin_bit_cast(bf16x8, l0),
-                                                          acc, 0, 0, 0);
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r1), __builtin_bit_cast(bf16x8, l1),
-                                                          acc, 0, 0, 0);
+            acc = mfma_bf16_pair(r, l, acc);
         } else {
+            const i32x4 r0 = __builtin_shufflevector(r, r, 0, 1, 2, 3), r1 = __builtin_shufflevector(r, r, 4, 5, 6, 7);
+            const i32x4 l0 = __builtin_shufflevector(l, l, 0, 1, 2, 3), l1 = __builtin_shufflevector(l, l, 4, 5, 6, 7);
             acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, r0), __builtin_bit_cast(f16x8, l0), acc,
                                                          0, 0, 0);
             acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, r1), __builtin_bit_cast(f16x8, l1), acc,
@@ -267,7 +284,7 @@ struct LaneScales {
     float lf[C::BL], rf;
     __device__ __forceinline__ void read(const lds_u8* sbuf, int wl, int wr, int lane) {
         const int l16 = lane % 16;
-        if constexpr (C::SC == kE8M0) {
+        if constexpr (C::kScaleBytes) {
 #pragma unroll
             for (int i = 0; i < (C::BL + 3) / 4; ++i) {
                 const int blk = wl * C::BL + 4 * i;
@@ -297,9 +314,69 @@ struct LaneScales {
     }
 };
 
+// 16 one-byte values times a power of two as two bf16 fragments.
+template <bool E5M2>
+__device__ __forceinline__ i32x8 widen(i32x4 v, float scale) {
+    i32x8 o;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        if constexpr (E5M2) {
+            o[2 * d] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(v[d], scale, false));
+            o[2 * d + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(v[d], scale, true));
+        } else {
+            o[2 * d] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[d], scale, false));
+            o[2 * d + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[d], scale, true));
+        }
+    }
+    return o;
+}
+
+// One stage of widened operands, 64 values of k at a time.  E8M0 scales go
+// into the conversions; fp32 scales multiply each half's product.
+template <class C, bool TAIL>
+__device__ __forceinline__ void stage_products_wide(f32x4 (&acc)[C::BL][C::BR], const lds_u8* buf, const lds_u8* sbuf,
+                                                    uint32_t lat, uint32_t rat, int wl, int wr, int lane, int rem) {
+    const int g = lane / 16;
+    LaneScales<C> sc;
+    sc.read(sbuf, wl, wr, lane);
+    const lds_f32* rs1 = reinterpret_cast<const lds_f32*>(sbuf) + C::TL + wr * C::BR * 16 + lane % 16;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        auto piece = [&](const lds_u8* tile, uint32_t at, uint32_t off) {
+            i32x4 v = *reinterpret_cast<const lds_i32x4*>(tile + (at ^ (64u * j)) + off);
+            if constexpr (TAIL) v = keep_bytes(v, rem - 16 * g - 64 * j);
+            return v;
+        };
+        i32x8 lf[C::BL];
+#pragma unroll
+        for (int x = 0; x < C::BL; ++x)
+            lf[x] = widen<C::LT == 1>(piece(buf, lat, 2048 * x), C::SC == kE8M0 ? sc.lf[x] : 1.f);
+#pragma unroll
+        for (int y = 0; y < C::BR; ++y) {
+            const i32x8 rf = widen<C::RT == 1>(piece(buf + C::TL * 128, rat, 2048 * y), C::SC == kE8M0 ? rs1[16 * y] : 1.f);
+            const f32x4 rs = sc.rvec(sbuf, wr, y, lane);
+#pragma unroll
+            for (int x = 0; x < C::BL; ++x) {
+                f32x4 p = C::SC == kE8M0 ? acc[x][y] : f32x4{0.f, 0.f, 0.f, 0.f};
+                p = mfma_bf16_pair(rf, lf[x], p);
+                if constexpr (C::SC == kE8M0) {
+                    acc[x][y] = p;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[x][y][i] = __builtin_fmaf(p[i], rs[i] * sc.lf[x], acc[x][y][i]);
+                }
+            }
+        }
+    }
+}
+
 template <class C, bool TAIL>
 __device__ __forceinline__ void stage_products(f32x4 (&acc)[C::BL][C::BR], const lds_u8* buf, const lds_u8* sbuf,
                                                uint32_t lat, uint32_t rat, int wl, int wr, int lane, int rem) {
+    if constexpr (C::ELEM == kF8Wide) {
+        stage_products_wide<C, TAIL>(acc, buf, sbuf, lat, rat, wl, wr, lane, rem);
+        return;
+    }
     const int g = lane / 16;
     LaneScales<C> sc;
     sc.read(sbuf, wl, wr, lane);
