@@ -393,6 +393,97 @@ __device__ __forceinline__ void stage_products(f32x4 (&acc)[C::BL][C::BR], const
     }
 }
 
+// Main loop of the 4 x 2 waves of 4 x 8 blocks: each wave alternates between a
+// slot of memory work and a slot of products, all slots ended by a barrier,
+// and the second half of the waves (one of each SIMD's two) runs one slot
+// behind, so that a SIMD's matrix unit works for one wave while the other
+// reads its next fragments.  A stage is four quadrants of 2 x 4 blocks in the
+// order (L0 R0) (L1 R0) (L1 R1) (L0 R1), each with one new operand half, which
+// the slot before it reads: L0, L1, R1, and R0 of the next stage.
+// Measured at 8192 x 8192 x 4096: 221 us, 2.48 PFLOP/s of one-byte operands
+// (236 us with all waves in step: reads, then products, one barrier a stage);
+// bf16 logits and gradients 1.17 to 1.25 PFLOP/s.  No better: the halves in
+// the order L0 R0, L0 R1, L1 R1, L1 R0 (12, 8, 4 and 0 reads a slot; 221 us),
+// and a pipelined loop with one barrier a stage whose reads run one quadrant
+// ahead (267 us with 21 registers spilled; two-byte operands, none spilled, 3%
+// behind).  Bound by LDS: the fragment reads (192 KiB) and fills (64 KiB) of a
+// stage take as long at 128 bytes a cycle as its products, 2048 cycles a
+// SIMD, and the matrix units are busy 53% of the cycles at 2.1 GHz.
+// Slots of stage s, counted from the leading waves' first (8 s; the second half
+// is one later):
+//   8s + 4: R1 is read, and then no fragment of stage s is missing; each wave
+//           waits for its reads and for its loads of stage s + 1;
+//   8s + 6: stage s + 1 has landed for all (the last wait is in slot 8s + 5)
+//           and its R0 is read; stage s + 2's loads may overwrite stage s.
+template <class C>
+__device__ __forceinline__ void pingpong(f32x4 (&acc)[C::BL][C::BR], Stager<C>& st, lds_u8* lds, lds_u8* sbufs, uint32_t lat,
+                                         uint32_t rat, int wl, int wr, int lane, int64_t full, int64_t stages) {
+    static_assert(C::BL == 4 && C::BR == 8 && C::WL * C::WR == 8, "two waves a SIMD");
+    const bool lag = st.wave >= 4;
+    auto slot = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        wg_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const int g = lane / 16;
+    i32x8 l[2][2], r[2][4];
+    auto read_r = [&](const lds_u8* buf, int h) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) r[h][y] = read_frag<false>(buf + C::TL * 128, rat, 2048 * (4 * h + y), g, 128);
+    };
+    auto read_l = [&](const lds_u8* buf, int h) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) l[h][x] = read_frag<false>(buf, lat, 2048 * (2 * h + x), g, 128);
+    };
+    // stage 0 has landed; stage 1 (or stage 0 again) on its way to the other buffer
+    st.issue(stages > 1 ? 1 : 0, lds + C::kBuf);
+    read_r(lds, 0);
+    if (lag) slot();
+    // No branch inside: across one the compiler moves products out of their
+    // slots.  Loads behind the last stage fetch it again into a buffer that is
+    // not read any more.
+    for (int64_t s = 0; s < full; ++s) {
+        lds_u8* buf = lds + (s & 1) * C::kBuf;
+        const lds_u8* sbuf = sbufs + (s & 1) * C::kScaleBuf;
+        LaneScales<C> sc;
+        auto products = [&](int lh, int rh) {
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const f32x4 rs = sc.rvec(sbuf, wr, 4 * rh + y, lane);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    mma_stage<C>(acc[2 * lh + x][4 * rh + y], r[rh][y], l[lh][x], sc.rw[rh], sc.lw[0], y, 2 * lh + x, rs,
+                                 sc.lf[2 * lh + x]);
+            }
+            __builtin_amdgcn_s_setprio(0);
+        };
+        sc.read(sbuf, wl, wr, lane);
+        read_l(buf, 0);
+        slot();
+        products(0, 0);
+        slot();
+        read_l(buf, 1);
+        slot();
+        products(1, 0);
+        slot();
+        read_r(buf, 1);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        st.put_scales(sbufs + ((s + 1) & 1) * C::kScaleBuf);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        slot();
+        products(1, 1);
+        slot();
+        read_r(lds + ((s + 1) & 1) * C::kBuf, 0);
+        st.issue(s + 2 < stages ? s + 2 : stages - 1, buf);
+        slot();
+        products(0, 1);
+        slot();
+    }
+    if (!lag) slot();
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
 // The whole product of one tile: rows l0 .. of L against rows r0 .. of R over
 // kbytes bytes of k.  Sums run over k in increasing order.
 template <class C>
@@ -424,12 +515,26 @@ __device__ __forceinline__ void tile_product(f32x4 (&acc)[C::BL][C::BR], const O
         wg_barrier();
         if (s + 1 < stages) st.issue(s + 1, lds + ((s + 1) & 1) * C::kBuf);
     };
-    for (int64_t s = 0; s < full; ++s) {
-        begin(s);
-        stage_products<C, false>(acc, lds + (s & 1) * C::kBuf, sbufs + (s & 1) * C::kScaleBuf, lat, rat, wl, wr, lane, 128);
+    constexpr bool kSlots = C::BL == 4 && C::BR == 8 && C::WL * C::WR == 8 && C::ELEM != kF8Wide;
+    bool waited = false;
+    if constexpr (kSlots) {
+        if (full > 0) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            st.put_scales(sbufs);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            wg_barrier();
+            pingpong<C>(acc, st, lds, sbufs, lat, rat, wl, wr, lane, full, stages);
+            waited = true;
+        }
+    } else {
+        for (int64_t s = 0; s < full; ++s) {
+            begin(s);
+            stage_products<C, false>(acc, lds + (s & 1) * C::kBuf, sbufs + (s & 1) * C::kScaleBuf, lat, rat, wl, wr, lane,
+                                     128);
+        }
     }
     if (full < stages) {
-        begin(full);
+        if (!waited) begin(full);
         stage_products<C, true>(acc, lds + (full & 1) * C::kBuf, sbufs + (full & 1) * C::kScaleBuf, lat, rat, wl, wr, lane,
                                 static_cast<int>(kbytes - full * 128));
     }
