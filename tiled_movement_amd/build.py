@@ -28,6 +28,7 @@ SOURCES = [
     "kernels_gemm.hip",
     "kernels_gemm_tiles.hip",
     "kernels_gemm_f8.hip",
+    "kernels_gemm_f8_few.hip",
     "kernels_quant.hip",
     "kernels_loss.hip",
     "kernels_map.hip",

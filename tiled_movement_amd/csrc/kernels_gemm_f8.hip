@@ -26,12 +26,8 @@ __global__ __launch_bounds__(C::NT) void k_gemm_f8(Operand A, Operand B, CT* __r
     store_tile<C>(acc, slice, c, ldc, wi, wj, A.rows, B.rows, vec, lane, [](float v) { return v; });
 }
 
-template <int ELEM, int LT, int RT, int SC, class CT>
+template <class C, class CT>
 hipError_t launch_tiles(const GemmF8Job& j, hipStream_t stream) {
-    // fp32 scales of both operands' rows on widened operands need more
-    // registers than a 64 x 128 wave tile leaves (145 spilled): half the rows.
-    constexpr int BL = ELEM == kF8Wide && SC == kF32Rows ? 2 : 4;
-    using C = Config<ELEM, LT, RT, SC, 4, 2, BL, 8>;
     const Operand A{static_cast<const uint8_t*>(j.a), j.lda, j.m, j.scale_a, (j.k + 127) / 128, j.a_square ? 7 : 0};
     const Operand B{static_cast<const uint8_t*>(j.b), j.ldb, j.n, j.scale_b, (j.k + 127) / 128, j.b_square ? 7 : 0};
     const int64_t tm = (j.m + C::TL - 1) / C::TL, tn = (j.n + C::TR - 1) / C::TR;
@@ -42,12 +38,21 @@ hipError_t launch_tiles(const GemmF8Job& j, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// fp32 scales of both operands' rows on widened operands need more registers
+// than a 64 x 128 wave tile leaves (145 spilled): half the rows.
+template <int ELEM, int LT, int RT, int SC, class CT>
+hipError_t launch_sized(const GemmF8Job& j, hipStream_t stream) {
+    const int64_t tiles = ((j.m + 255) / 256) * ((j.n + 255) / 256);
+    if (tiles <= 128) return launch_tiles<Config<ELEM, LT, RT, SC, 2, 2, 4, 4>, CT>(j, stream);
+    return launch_tiles<Config<ELEM, LT, RT, SC, 4, 2, ELEM == kF8Wide && SC == kF32Rows ? 2 : 4, 8>, CT>(j, stream);
+}
+
 // A bf16 result takes the one-byte instruction, whose dropped bits are a
 // hundredth of the rounding to bf16; an fp32 result is asked for its bits and
 // takes the bf16 instruction on widened operands.
 template <int LT, int RT, int SC>
 hipError_t launch_typed(const GemmF8Job& j, hipStream_t stream) {
-    return j.bf16c ? launch_tiles<kF8, LT, RT, SC, __bf16>(j, stream) : launch_tiles<kF8Wide, LT, RT, SC, float>(j, stream);
+    return j.bf16c ? launch_sized<kF8, LT, RT, SC, __bf16>(j, stream) : launch_sized<kF8Wide, LT, RT, SC, float>(j, stream);
 }
 
 template <int SC>
@@ -60,6 +65,7 @@ hipError_t launch_scaled(const GemmF8Job& j, hipStream_t stream) {
 
 hipError_t launch_gemm_f8(const GemmF8Job& j, hipStream_t stream) {
     if (j.m == 0 || j.n == 0) return hipSuccess;
+    if (j.m <= kFewRows) return launch_gemm_f8_few(j, stream);
     if (j.e8m0) return launch_scaled<kE8M0>(j, stream);
     return j.b_square ? launch_scaled<kF32Square>(j, stream) : launch_scaled<kF32Rows>(j, stream);
 }

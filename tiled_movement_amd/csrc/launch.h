@@ -79,6 +79,8 @@ struct GemmF8Job {
     bool a_e5m2, b_e5m2, a_square, b_square, e8m0, bf16c;
 };
 hipError_t launch_gemm_f8(const GemmF8Job& job, hipStream_t stream);
+hipError_t launch_gemm_f8_few(const GemmF8Job& job, hipStream_t stream);  // m <= kFewRows
+constexpr int64_t kFewRows = 128;
 
 // swz_linear_ce, swz_linear_distill and their gradients.  teacher ==
 // nullptr: cross entropy (top 1, tau 1).
