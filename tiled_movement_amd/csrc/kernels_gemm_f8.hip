@@ -11,13 +11,21 @@ namespace {
 
 using namespace mma;
 
+// Workgroups go to the eight XCDs in turn; this numbering gives each XCD a run
+// of consecutive tiles.
+__device__ __forceinline__ uint32_t xcd_tile(uint32_t id, uint32_t total) {
+    const uint32_t x = id % 8, each = total / 8, more = total % 8;
+    return x * each + (x < more ? x : more) + id / 8;
+}
+
 template <class C, class CT>
 __global__ __launch_bounds__(C::NT) void k_gemm_f8(Operand A, Operand B, CT* __restrict__ c, int64_t ldc, int64_t k,
-                                                   uint32_t tiles_m, int vec) {
+                                                   uint32_t tiles_m, int vec, int by_xcd) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x % tiles_m) * C::TL;
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x / tiles_m) * C::TR;
+    const uint32_t tile = by_xcd ? xcd_tile(blockIdx.x, gridDim.x) : blockIdx.x;
+    const int64_t i0 = static_cast<int64_t>(tile % tiles_m) * C::TL;
+    const int64_t j0 = static_cast<int64_t>(tile / tiles_m) * C::TR;
     f32x4 acc[C::BL][C::BR];
     tile_product<C>(acc, A, B, i0, j0, k, lds);
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -27,24 +35,37 @@ __global__ __launch_bounds__(C::NT) void k_gemm_f8(Operand A, Operand B, CT* __r
 }
 
 template <class C, class CT>
-hipError_t launch_tiles(const GemmF8Job& j, hipStream_t stream) {
+hipError_t launch_tiles(const GemmF8Job& j, bool by_xcd, hipStream_t stream) {
     const Operand A{static_cast<const uint8_t*>(j.a), j.lda, j.m, j.scale_a, (j.k + 127) / 128, j.a_square ? 7 : 0};
     const Operand B{static_cast<const uint8_t*>(j.b), j.ldb, j.n, j.scale_b, (j.k + 127) / 128, j.b_square ? 7 : 0};
     const int64_t tm = (j.m + C::TL - 1) / C::TL, tn = (j.n + C::TR - 1) / C::TR;
     if (tm > 0x7fffffff / C::NT / tn) return hipErrorInvalidValue;
     const int vec = j.n * static_cast<int64_t>(sizeof(CT)) % 16 == 0 && reinterpret_cast<uintptr_t>(j.c) % 16 == 0;
     hipLaunchKernelGGL((k_gemm_f8<C, CT>), dim3(static_cast<unsigned>(tm * tn)), dim3(C::NT), 0, stream, A, B,
-                       static_cast<CT*>(j.c), j.n, j.k, static_cast<uint32_t>(tm), vec);
+                       static_cast<CT*>(j.c), j.n, j.k, static_cast<uint32_t>(tm), vec, by_xcd ? 1 : 0);
     return hipGetLastError();
 }
 
+// Tile by the number of workgroups it leaves, 256 being one a compute unit.
+// A stage costs a workgroup at least its barrier, loads and fragment reads,
+// some 0.3 us for 64 x 64 and 0.8 us for 128 x 128, however few workgroups
+// run; so small tiles where all of them run at once (m x 4096 x 4096: m = 128,
+// 64 x 64 tiles 12 us, 64 x 128 16, 128 x 128 23, 256 x 256 45; m = 512: 16,
+// 17, 24, 48; 256 x 8192 x 8192: 43, 35, 46, 114), and 256 x 256, which reads
+// the least per product, where there is work for all units anyway (m = 2048:
+// 62, 61, 47, 49).  In the small grids the workgroups of an XCD take
+// neighbouring tiles, which share B's rows in its cache (512 x 8192 x 8192,
+// 128 x 128 tiles: 73 -> 47 us); 256 x 256 tiles lose by it (8192 x 8192 x
+// 4096: 237 -> 267 us).
 // fp32 scales of both operands' rows on widened operands need more registers
 // than a 64 x 128 wave tile leaves (145 spilled): half the rows.
 template <int ELEM, int LT, int RT, int SC, class CT>
 hipError_t launch_sized(const GemmF8Job& j, hipStream_t stream) {
-    const int64_t tiles = ((j.m + 255) / 256) * ((j.n + 255) / 256);
-    if (tiles <= 128) return launch_tiles<Config<ELEM, LT, RT, SC, 2, 2, 4, 4>, CT>(j, stream);
-    return launch_tiles<Config<ELEM, LT, RT, SC, 4, 2, ELEM == kF8Wide && SC == kF32Rows ? 2 : 4, 8>, CT>(j, stream);
+    auto tiles = [&](int64_t tm, int64_t tn) { return ((j.m + tm - 1) / tm) * ((j.n + tn - 1) / tn); };
+    if (tiles(64, 64) <= 256) return launch_tiles<Config<ELEM, LT, RT, SC, 2, 2, 2, 2>, CT>(j, true, stream);
+    if (tiles(64, 128) <= 256) return launch_tiles<Config<ELEM, LT, RT, SC, 2, 4, 2, 2>, CT>(j, true, stream);
+    if (tiles(128, 128) <= 256) return launch_tiles<Config<ELEM, LT, RT, SC, 2, 4, 4, 2>, CT>(j, true, stream);
+    return launch_tiles<Config<ELEM, LT, RT, SC, 4, 2, ELEM == kF8Wide && SC == kF32Rows ? 2 : 4, 8>, CT>(j, false, stream);
 }
 
 // A bf16 result takes the one-byte instruction, whose dropped bits are a

@@ -30,10 +30,6 @@ __device__ __forceinline__ i32x4 load_piece(const uint8_t* row, int64_t b, int j
     return *reinterpret_cast<const i32x4*>(row + b * 128 + at);
 }
 
-__device__ __forceinline__ float e8m0_value(uint8_t b) {
-    return __uint_as_float(b == 255 ? 0x7fc00000u : b ? static_cast<uint32_t>(b) << 23 : 0x400000u);
-}
-
 template <int LT, int RT, bool E8M0, class CT, int MB, int RB, int NW>
 __global__ __launch_bounds__(64 * NW) void k_gemm_f8_few(Operand A, Operand B, CT* __restrict__ c, int64_t ldc, int64_t k) {
     __shared__ f32x4 red[NW][MB * RB * 64];
@@ -151,10 +147,7 @@ hipError_t launch_few(const GemmF8Job& j, hipStream_t stream) {
 
 template <int LT, int RT, bool E8M0, class CT>
 hipError_t launch_rows_of(const GemmF8Job& j, hipStream_t stream) {
-    if (j.m <= 16) return launch_few<LT, RT, E8M0, CT, 1, 1, 8>(j, stream);
-    if (j.m <= 32) return launch_few<LT, RT, E8M0, CT, 2, 2, 8>(j, stream);
-    if (j.m <= 64) return launch_few<LT, RT, E8M0, CT, 4, 2, 8>(j, stream);
-    return launch_few<LT, RT, E8M0, CT, 8, 2, 4>(j, stream);
+    return launch_few<LT, RT, E8M0, CT, 1, 1, 8>(j, stream);
 }
 
 template <int LT, int RT>

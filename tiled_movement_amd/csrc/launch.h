@@ -80,7 +80,7 @@ struct GemmF8Job {
 };
 hipError_t launch_gemm_f8(const GemmF8Job& job, hipStream_t stream);
 hipError_t launch_gemm_f8_few(const GemmF8Job& job, hipStream_t stream);  // m <= kFewRows
-constexpr int64_t kFewRows = 128;
+constexpr int64_t kFewRows = 16;
 
 // swz_linear_ce, swz_linear_distill and their gradients.  teacher ==
 // nullptr: cross entropy (top 1, tau 1).

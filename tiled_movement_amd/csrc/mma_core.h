@@ -74,15 +74,22 @@ struct Config {
     static constexpr int NT = 64 * WL * WR;
     static constexpr int TL = 16 * WL * BL, TR = 16 * WR * BR;
     static constexpr int kBuf = (TL + TR) * 128;
-    // E8M0 scales for the one-byte instruction stay bytes, the others are fp32
-    static constexpr bool kScaleBytes = SC == kE8M0 && ELEM == kF8;
-    static constexpr int kScaleBuf = SC == kNoScale ? 0 : kScaleBytes ? (TL + TR + 63) / 64 * 64 : (TL + TR) * 4;
-    static constexpr int kMain = 2 * (kBuf + kScaleBuf);
+    // The 4 x 2 waves of 4 x 8 blocks run their own main loop (slots); the
+    // others keep several stages in flight (deep).
+    static constexpr bool kSlots = BL == 4 && BR == 8 && WL == 4 && WR == 2 && ELEM != kF8Wide;
+    static constexpr int NS = (TL + TR + NT - 1) / NT;  // scales a thread stages
+    // Scales of a stage in LDS: a word a row; slots with E8M0 a byte a row.
+    static constexpr bool kScaleBytes = SC == kE8M0 && kSlots;
+    static constexpr int kScaleBuf = SC == kNoScale ? 0 : kScaleBytes ? (TL + TR + 63) / 64 * 64 : NS * NT * 4;
+    static constexpr int kStage = kBuf + kScaleBuf;
+    static constexpr int kFit = 160 * 1024 / kStage;
+    static constexpr int NBUF = kSlots ? 2 : kFit < 4 ? kFit : 4;
+    static constexpr int kMain = NBUF * kStage;
     // a wave's slice of the epilogue: 16 rows of C, padded by 16 bytes
     static constexpr int kPitch = 16 * BR + 4;
     static constexpr int kSlice = 16 * kPitch * 4;
     static constexpr int kLds = kMain > WL * WR * kSlice ? kMain : WL * WR * kSlice;
-    static constexpr int NS = (TL + TR + NT - 1) / NT;  // scales a thread stages
+    static_assert(NBUF >= 2, "two stages fit in LDS");
     static_assert(TL * 8 % NT == 0 && TR * 8 % NT == 0 && NT % 128 == 0, "the fills split evenly");
     static_assert(kLds <= 160 * 1024, "the stages fit in LDS");
 };
@@ -169,6 +176,23 @@ struct Stager {
             for (int i = 0; i < C::NS; ++i) sv[i] = reinterpret_cast<const uint32_t*>(sp[i])[s];
         }
     }
+    // The same with the scales straight into LDS, so that a stage is a fixed
+    // number of loads into LDS and nothing else: the aligned word that holds
+    // an E8M0 scale's byte (in its page, and what else it holds is not used),
+    // or the fp32 scale.
+    static constexpr int kLoads = Fill<C::TL, C::NT>::Q + Fill<C::TR, C::NT>::Q + (C::SC == kNoScale ? 0 : C::NS);
+    __device__ __forceinline__ void issue_deep(int64_t s, lds_u8* buf) const {
+        fl.issue(s, kbytes - s * 128, buf, wave);
+        fr.issue(s, kbytes - s * 128, buf + C::TL * 128, wave);
+        if constexpr (C::SC != kNoScale) {
+#pragma unroll
+            for (int i = 0; i < C::NS; ++i) {
+                const uintptr_t at = reinterpret_cast<uintptr_t>(sp[i] + s * (C::SC == kE8M0 ? 1 : 4)) & ~uintptr_t(3);
+                __builtin_amdgcn_global_load_lds(reinterpret_cast<const uint8_t*>(at), buf + C::kBuf + 4 * (64 * wave + C::NT * i),
+                                                 4, 0, 0);
+            }
+        }
+    }
     // Scales that issue() fetched into their LDS buffer: fp32 by row; bytes so
     // that the four rows 16 apart of a 64-row group share a word.
     __device__ __forceinline__ void put_scales(lds_u8* sbuf) const {
@@ -177,9 +201,7 @@ struct Stager {
             for (int i = 0; i < C::NS; ++i) {
                 const int e = t + C::NT * i;
                 if (C::NS * C::NT == C::TL + C::TR || e < C::TL + C::TR) {
-                    if constexpr (C::SC == kE8M0 && !C::kScaleBytes)
-                        reinterpret_cast<lds_u32*>(sbuf)[e] = sv[i] == 255 ? 0x7fc00000u : sv[i] ? sv[i] << 23 : 0x400000u;
-                    else if constexpr (C::kScaleBytes)
+                    if constexpr (C::kScaleBytes)
                         sbuf[e / 64 * 64 + e % 16 * 4 + e / 16 % 4] = static_cast<uint8_t>(sv[i]);
                     else
                         reinterpret_cast<lds_u32*>(sbuf)[e] = sv[i];
@@ -277,25 +299,36 @@ __device__ __forceinline__ void mma_stage(f32x4& acc, i32x8 r, i32x8 l, int sr, 
     }
 }
 
-// This lane's scales of a stage.
+// This lane's scales of a stage: l(x), r(y) are words whose byte lsel(x),
+// rsel(y) is block x's or y's E8M0 scale; lf, rf and rvec are fp32.
 template <class C>
 struct LaneScales {
-    int lw[(C::BL + 3) / 4], rw[(C::BR + 3) / 4];  // E8M0: words of four blocks
+    static constexpr bool kWords = C::SC == kE8M0 && !C::kScaleBytes;
+    static constexpr bool kKept = C::ELEM == kF8;  // widened operands read their words when they convert
+    int lw[!kKept ? 1 : kWords ? C::BL : (C::BL + 3) / 4], rw[!kKept ? 1 : kWords ? C::BR : (C::BR + 3) / 4];
     float lf[C::BL], rf;
-    __device__ __forceinline__ void read(const lds_u8* sbuf, int wl, int wr, int lane) {
+    __device__ __forceinline__ int l(int x) const { return lw[kWords ? x : x / 4]; }
+    __device__ __forceinline__ int r(int y) const { return rw[kWords ? y : y / 4]; }
+    static __device__ __forceinline__ constexpr int sel(int b) { return kWords ? 0 : b % 4; }
+    // skew: kWords: where the scales of this lane's rows begin, modulo 4
+    // (ScaleSkew); s: the stage.
+    template <class K>
+    __device__ __forceinline__ void read(const lds_u8* sbuf, int wl, int wr, int lane, const K& skew, int s) {
         const int l16 = lane % 16;
+        const lds_u32* w = reinterpret_cast<const lds_u32*>(sbuf);
         if constexpr (C::kScaleBytes) {
 #pragma unroll
-            for (int i = 0; i < (C::BL + 3) / 4; ++i) {
-                const int blk = wl * C::BL + 4 * i;
-                lw[i] = static_cast<int>(*reinterpret_cast<const lds_u32*>(sbuf + blk / 4 * 64 + l16 * 4) >>
-                                         (C::BL % 4 ? 8 * (blk % 4) : 0));
-            }
+            for (int i = 0; i < (C::BL + 3) / 4; ++i) lw[i] = static_cast<int>(w[(wl * C::BL / 4 + i) * 16 + l16]);
 #pragma unroll
-            for (int i = 0; i < (C::BR + 3) / 4; ++i) {
-                const int blk = C::TL / 16 + wr * C::BR + 4 * i;
-                rw[i] = static_cast<int>(*reinterpret_cast<const lds_u32*>(sbuf + blk / 4 * 64 + l16 * 4) >>
-                                         (C::BR % 4 || C::TL % 64 ? 8 * (blk % 4) : 0));
+            for (int i = 0; i < (C::BR + 3) / 4; ++i)
+                rw[i] = static_cast<int>(w[(C::TL / 64 + wr * C::BR / 4 + i) * 16 + l16]);
+        } else if constexpr (C::SC == kE8M0) {
+            if constexpr (kKept) {
+#pragma unroll
+                for (int x = 0; x < C::BL; ++x) lw[x] = static_cast<int>(skew.word(sbuf, (wl * C::BL + x) * 16 + l16, x, s));
+#pragma unroll
+                for (int y = 0; y < C::BR; ++y)
+                    rw[y] = static_cast<int>(skew.word(sbuf, C::TL + (wr * C::BR + y) * 16 + l16, C::BL + y, s));
             }
         } else if constexpr (C::SC != kNoScale) {
             const lds_f32* f = reinterpret_cast<const lds_f32*>(sbuf);
@@ -313,6 +346,35 @@ struct LaneScales {
             return f32x4{0.f, 0.f, 0.f, 0.f};
     }
 };
+
+struct NoSkew {
+    __device__ __forceinline__ uint32_t word(const lds_u8*, int, int, int) const { return 0; }
+};
+template <class C>
+struct ScaleSkew {
+    static_assert(C::BL + C::BR <= 16, "two bits a block");
+    uint32_t at = 0;
+    // The word of a tile row whose low byte is its E8M0 scale of stage s.
+    __device__ __forceinline__ uint32_t word(const lds_u8* sbuf, int row, int block, int s) const {
+        return reinterpret_cast<const lds_u32*>(sbuf)[row] >> (8 * (((at >> (2 * block)) + s) & 3u));
+    }
+    __device__ __forceinline__ void init(const Operand& L, const Operand& R, int64_t l0, int64_t r0, int wl, int wr, int l16) {
+        auto begin = [](const Operand& o, int64_t row) {
+            row = row < o.rows ? row : o.rows - 1;
+            return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(o.scale) + (row >> o.scale_shift) * o.scale_ld) & 3u;
+        };
+#pragma unroll
+        for (int x = 0; x < C::BL; ++x) at |= begin(L, l0 + (wl * C::BL + x) * 16 + l16) << (2 * x);
+#pragma unroll
+        for (int y = 0; y < C::BR; ++y) at |= begin(R, r0 + (wr * C::BR + y) * 16 + l16) << (2 * (C::BL + y));
+    }
+};
+
+// 2^(b - 127) of the low byte of a word; 255 is NaN.
+__device__ __forceinline__ float e8m0_value(uint32_t w) {
+    const uint32_t b = w & 255u;
+    return __uint_as_float(b == 255u ? 0x7fc00000u : b ? b << 23 : 0x400000u);
+}
 
 // 16 one-byte values times a power of two as two bf16 fragments.
 template <bool E5M2>
@@ -333,13 +395,11 @@ __device__ __forceinline__ i32x8 widen(i32x4 v, float scale) {
 
 // One stage of widened operands, 64 values of k at a time.  E8M0 scales go
 // into the conversions; fp32 scales multiply each half's product.
-template <class C, bool TAIL>
+template <class C, bool TAIL, class K>
 __device__ __forceinline__ void stage_products_wide(f32x4 (&acc)[C::BL][C::BR], const lds_u8* buf, const lds_u8* sbuf,
-                                                    uint32_t lat, uint32_t rat, int wl, int wr, int lane, int rem) {
+                                                    const LaneScales<C>& sc, uint32_t lat, uint32_t rat, int wl, int wr,
+                                                    int lane, int rem, const K& skew, int s) {
     const int g = lane / 16;
-    LaneScales<C> sc;
-    sc.read(sbuf, wl, wr, lane);
-    const lds_f32* rs1 = reinterpret_cast<const lds_f32*>(sbuf) + C::TL + wr * C::BR * 16 + lane % 16;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         auto piece = [&](const lds_u8* tile, uint32_t at, uint32_t off) {
@@ -350,10 +410,12 @@ __device__ __forceinline__ void stage_products_wide(f32x4 (&acc)[C::BL][C::BR], 
         i32x8 lf[C::BL];
 #pragma unroll
         for (int x = 0; x < C::BL; ++x)
-            lf[x] = widen<C::LT == 1>(piece(buf, lat, 2048 * x), C::SC == kE8M0 ? sc.lf[x] : 1.f);
+            lf[x] = widen<C::LT == 1>(piece(buf, lat, 2048 * x), C::SC == kE8M0 ? e8m0_value(skew.word(sbuf, (wl * C::BL + x) * 16 + lane % 16, x, s)) : 1.f);
 #pragma unroll
         for (int y = 0; y < C::BR; ++y) {
-            const i32x8 rf = widen<C::RT == 1>(piece(buf + C::TL * 128, rat, 2048 * y), C::SC == kE8M0 ? rs1[16 * y] : 1.f);
+            const float rscale =
+                C::SC == kE8M0 ? e8m0_value(skew.word(sbuf, C::TL + (wr * C::BR + y) * 16 + lane % 16, C::BL + y, s)) : 1.f;
+            const i32x8 rf = widen<C::RT == 1>(piece(buf + C::TL * 128, rat, 2048 * y), rscale);
             const f32x4 rs = sc.rvec(sbuf, wr, y, lane);
 #pragma unroll
             for (int x = 0; x < C::BL; ++x) {
@@ -370,26 +432,25 @@ __device__ __forceinline__ void stage_products_wide(f32x4 (&acc)[C::BL][C::BR], 
     }
 }
 
-template <class C, bool TAIL>
+template <class C, bool TAIL, class K>
 __device__ __forceinline__ void stage_products(f32x4 (&acc)[C::BL][C::BR], const lds_u8* buf, const lds_u8* sbuf,
-                                               uint32_t lat, uint32_t rat, int wl, int wr, int lane, int rem) {
+                                               const LaneScales<C>& sc, uint32_t lat, uint32_t rat, int wl, int wr, int lane,
+                                               int rem, const K& skew, int s) {
     if constexpr (C::ELEM == kF8Wide) {
-        stage_products_wide<C, TAIL>(acc, buf, sbuf, lat, rat, wl, wr, lane, rem);
-        return;
-    }
-    const int g = lane / 16;
-    LaneScales<C> sc;
-    sc.read(sbuf, wl, wr, lane);
-    i32x8 lf[C::BL];
+        stage_products_wide<C, TAIL>(acc, buf, sbuf, sc, lat, rat, wl, wr, lane, rem, skew, s);
+    } else {
+        const int g = lane / 16;
+        i32x8 lf[C::BL];
 #pragma unroll
-    for (int x = 0; x < C::BL; ++x) lf[x] = read_frag<TAIL>(buf, lat, 2048 * x, g, rem);
+        for (int x = 0; x < C::BL; ++x) lf[x] = read_frag<TAIL>(buf, lat, 2048 * x, g, rem);
 #pragma unroll
-    for (int y = 0; y < C::BR; ++y) {
-        const i32x8 rf = read_frag<TAIL>(buf + C::TL * 128, rat, 2048 * y, g, rem);
-        const f32x4 rs = sc.rvec(sbuf, wr, y, lane);
+        for (int y = 0; y < C::BR; ++y) {
+            const i32x8 rf = read_frag<TAIL>(buf + C::TL * 128, rat, 2048 * y, g, rem);
+            const f32x4 rs = sc.rvec(sbuf, wr, y, lane);
 #pragma unroll
-        for (int x = 0; x < C::BL; ++x)
-            mma_stage<C>(acc[x][y], rf, lf[x], sc.rw[y / 4], sc.lw[x / 4], y % 4, x % 4, rs, sc.lf[x]);
+            for (int x = 0; x < C::BL; ++x)
+                mma_stage<C>(acc[x][y], rf, lf[x], sc.r(y), sc.l(x), sc.sel(y), sc.sel(x), rs, sc.lf[x]);
+        }
     }
 }
 
@@ -453,12 +514,12 @@ __device__ __forceinline__ void pingpong(f32x4 (&acc)[C::BL][C::BR], Stager<C>& 
                 const f32x4 rs = sc.rvec(sbuf, wr, 4 * rh + y, lane);
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                    mma_stage<C>(acc[2 * lh + x][4 * rh + y], r[rh][y], l[lh][x], sc.rw[rh], sc.lw[0], y, 2 * lh + x, rs,
+                    mma_stage<C>(acc[2 * lh + x][4 * rh + y], r[rh][y], l[lh][x], sc.r(4 * rh + y), sc.l(0), y, 2 * lh + x, rs,
                                  sc.lf[2 * lh + x]);
             }
             __builtin_amdgcn_s_setprio(0);
         };
-        sc.read(sbuf, wl, wr, lane);
+        sc.read(sbuf, wl, wr, lane, NoSkew{}, 0);
         read_l(buf, 0);
         slot();
         products(0, 0);
@@ -500,46 +561,58 @@ __device__ __forceinline__ void tile_product(f32x4 (&acc)[C::BL][C::BR], const O
     if (stages == 0) return;
     Stager<C> st;
     st.init(L, R, l0, r0, kbytes, t);
-    lds_u8* sbufs = lds + 2 * C::kBuf;
-    const int l16 = lane % 16;
+    const int l16 = lane % 16, rem = static_cast<int>(kbytes - full * 128);
     const uint32_t at = l16 * 128 + 16 * ((lane / 16) ^ ((l16 >> 1) & 7));
     const uint32_t lat = wl * C::BL * 2048 + at, rat = wr * C::BR * 2048 + at;
-    st.issue(0, lds);
-    // Stage s: wait until this wave's loads of it have landed (the barrier
-    // covers the others') and every wave is done with stage s - 1, whose
-    // buffer the next loads reuse; then start stage s + 1's loads.
-    auto begin = [&](int64_t s) {
+    LaneScales<C> sc;
+    if constexpr (C::kSlots) {
+        lds_u8* sbufs = lds + 2 * C::kBuf;
+        st.issue(0, lds);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        st.put_scales(sbufs + (s & 1) * C::kScaleBuf);
+        st.put_scales(sbufs);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         wg_barrier();
-        if (s + 1 < stages) st.issue(s + 1, lds + ((s + 1) & 1) * C::kBuf);
-    };
-    constexpr bool kSlots = C::BL == 4 && C::BR == 8 && C::WL * C::WR == 8 && C::ELEM != kF8Wide;
-    bool waited = false;
-    if constexpr (kSlots) {
-        if (full > 0) {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            st.put_scales(sbufs);
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            wg_barrier();
-            pingpong<C>(acc, st, lds, sbufs, lat, rat, wl, wr, lane, full, stages);
-            waited = true;
+        if (full > 0) pingpong<C>(acc, st, lds, sbufs, lat, rat, wl, wr, lane, full, stages);
+        if (full < stages) {
+            const lds_u8* sbuf = sbufs + (full & 1) * C::kScaleBuf;
+            sc.read(sbuf, wl, wr, lane, NoSkew{}, 0);
+            stage_products<C, true>(acc, lds + (full & 1) * C::kBuf, sbuf, sc, lat, rat, wl, wr, lane, rem, NoSkew{}, 0);
         }
     } else {
+        // NBUF - 1 stages in flight: with few workgroups a stage's products are
+        // short against the way of its loads.  A wave waits for its own loads
+        // of stage s (those of the NBUF - 2 behind it may still be on their
+        // way; every stage is kLoads of them, the ones behind the last stage
+        // fetch it again), the barrier covers the other waves', and with it all
+        // are done with stage s - 1, whose buffer the next loads take.
+        constexpr int N = C::NBUF;
+        std::conditional_t<LaneScales<C>::kWords, ScaleSkew<C>, NoSkew> skew;
+        if constexpr (LaneScales<C>::kWords) skew.init(L, R, l0, r0, wl, wr, l16);
+#pragma unroll
+        for (int i = 0; i < N - 1; ++i) st.issue_deep(i < stages ? i : stages - 1, lds + i * C::kStage);
+        int at_buf = 0;
+        auto begin = [&](int64_t s) {
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((N - 2) * Stager<C>::kLoads) : "memory");
+            wg_barrier();
+            const int prev = at_buf == 0 ? N - 1 : at_buf - 1;
+            st.issue_deep(s + N - 1 < stages ? s + N - 1 : stages - 1, lds + prev * C::kStage);
+            const lds_u8* buf = lds + at_buf * C::kStage;
+            at_buf = at_buf + 1 == N ? 0 : at_buf + 1;
+            sc.read(buf + C::kBuf, wl, wr, lane, skew, static_cast<int>(s));
+            return buf;
+        };
         for (int64_t s = 0; s < full; ++s) {
-            begin(s);
-            stage_products<C, false>(acc, lds + (s & 1) * C::kBuf, sbufs + (s & 1) * C::kScaleBuf, lat, rat, wl, wr, lane,
-                                     128);
+            const lds_u8* buf = begin(s);
+            stage_products<C, false>(acc, buf, buf + C::kBuf, sc, lat, rat, wl, wr, lane, 128, skew, static_cast<int>(s));
+        }
+        if (full < stages) {
+            const lds_u8* buf = begin(full);
+            stage_products<C, true>(acc, buf, buf + C::kBuf, sc, lat, rat, wl, wr, lane, rem, skew, static_cast<int>(full));
         }
     }
-    if (full < stages) {
-        if (!waited) begin(full);
-        stage_products<C, true>(acc, lds + (full & 1) * C::kBuf, sbufs + (full & 1) * C::kScaleBuf, lat, rat, wl, wr, lane,
-                                static_cast<int>(kbytes - full * 128));
-    }
-    // every wave is done reading before the epilogue reuses the buffers
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    // every wave is done reading, and nothing is on its way into LDS, before
+    // the epilogue reuses the buffers
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     wg_barrier();
 }
 
