@@ -57,17 +57,38 @@ int check_loss_sizes(int64_t n, int64_t v, int64_t k, int32_t top) {
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
+// Words of a piece, at most `most` (a multiple of 256), for row_tiles tiles of
+// rows.  A piece's products run in rounds of 256 tiles, one a compute unit, and
+// a started round takes as long as a full one: pieces of whole rounds with a
+// short last one (of smaller tiles' cost, at least a third of a round a piece)
+// against pieces alike in size, whichever has fewer.
+int64_t piece_words(int64_t v, int64_t most, int64_t row_tiles) {
+    auto cost = [&](int64_t piece) {
+        double rounds = 0;
+        for (int64_t at = 0; at < v; at += piece) {
+            const int64_t words = v - at < piece ? v - at : piece;
+            rounds += static_cast<double>(((words + 255) / 256 * row_tiles + 255) / 256) + 0.34;
+        }
+        return rounds;
+    };
+    const int64_t pieces = (v + most - 1) / most;
+    const int64_t alike = up((v + pieces - 1) / pieces, 256);
+    int64_t whole = 256;  // word tiles of whole rounds
+    for (int64_t t = row_tiles; whole > 1 && t % 2 == 0; t /= 2) whole /= 2;
+    const int64_t aligned = most / (256 * whole) * (256 * whole);
+    return aligned > 0 && aligned < alike * pieces && v / aligned < 4096 && cost(aligned) < cost(alike) ? aligned : alike;
+}
+
 // The gradient's workspace.  dz of a piece stays within 2^27 values (256 MiB)
-// unless that leaves fewer than 8192 words; pieces are alike in size.  Where
+// unless that leaves fewer than 8192 words.  Where
 // dH has fewer tiles than the 256 compute units, its sum over a piece is split
 // into parts (of at least 8 stages) with buffers of their own.
 swz::LossPlan plan_loss(int64_t n, int64_t v, int64_t k, int32_t top) {
     swz::LossPlan p{};
     int64_t most = (int64_t(1) << 27) / (n ? n : 1) / 256 * 256;
     most = most < 8192 ? 8192 : most > 32768 ? 32768 : most;
-    const int64_t pieces = (v + most - 1) / most;
-    p.piece = up((v + pieces - 1) / pieces, 256);
     const int64_t tl = n <= 64 ? 64 : n <= 128 ? 128 : 256;
+    p.piece = piece_words(v, most, (n + tl - 1) / tl + (n == 0));
     const int64_t tiles = ((n + tl - 1) / tl) * ((k + 255) / 256), stages = p.piece / 64;
     p.parts = tiles >= 256 || tiles == 0 ? 1 : 256 / tiles;
     if (p.parts > 16) p.parts = 16;

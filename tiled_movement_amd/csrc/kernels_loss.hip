@@ -217,22 +217,26 @@ __global__ void k_clear_slots(uint32_t* slots) {
 }
 
 // Largest finite magnitude of a bf16 array, as fp32 bits (the order of
-// atomic maxima does not matter).
+// atomic maxima does not matter).  One atomic a workgroup: with one a wave the
+// atomics took four fifths of the time (200 MB: 190 us).
 __global__ __launch_bounds__(256) void k_absmax(const uint16_t* __restrict__ x, int64_t pieces, uint32_t* slot) {
-    uint32_t m = 0;
+    __shared__ uint32_t part[4];
+    u16x8 m = 0;
     const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
 #pragma unroll 4
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < pieces; i += step) {
-        const u16x8 a = reinterpret_cast<const u16x8*>(x)[i];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t b = a[e] & 0x7fffu;
-            m = max(m, b < 0x7f80u ? b : 0u);
-        }
+        u16x8 a = reinterpret_cast<const u16x8*>(x)[i] & uint16_t(0x7fff);
+        a = a < uint16_t(0x7f80) ? a : u16x8(0);
+        m = a > m ? a : m;
     }
+    uint32_t best = 0;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d)));
-    if (threadIdx.x % 64 == 0) atomicMax(slot, m << 16);
+    for (int e = 0; e < 8; ++e) best = max(best, static_cast<uint32_t>(m[e]));
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) best = max(best, static_cast<uint32_t>(__shfl_xor(static_cast<int>(best), d)));
+    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = best;
+    __syncthreads();
+    if (threadIdx.x == 0) atomicMax(slot, max(max(part[0], part[1]), max(part[2], part[3])) << 16);
 }
 
 // The power of two that takes a largest magnitude (bits) just below 2^15, as

@@ -85,6 +85,9 @@ struct Config {
     static constexpr int kFit = 160 * 1024 / kStage;
     static constexpr int NBUF = kSlots ? 2 : kFit < 4 ? kFit : 4;
     static constexpr int kMain = NBUF * kStage;
+    // Two stages: scales go through registers, and E8M0 ones of widened
+    // operands become fp32 on the way, once a row instead of once a fragment.
+    static constexpr bool kPutScales = NBUF == 2;
     // a wave's slice of the epilogue: 16 rows of C, padded by 16 bytes
     static constexpr int kPitch = 16 * BR + 4;
     static constexpr int kSlice = 16 * kPitch * 4;
@@ -134,6 +137,12 @@ struct Fill {
             __builtin_amdgcn_global_load_lds(b + (off[q] - back), dst + 16 * (64 * wave + NT * q), 16, 0, 0);
     }
 };
+
+// 2^(b - 127) of the low byte of a word; 255 is NaN.
+__device__ __forceinline__ float e8m0_value(uint32_t w) {
+    const uint32_t b = w & 255u;
+    return __uint_as_float(b == 255u ? 0x7fc00000u : b ? b << 23 : 0x400000u);
+}
 
 template <class C>
 struct Stager {
@@ -201,7 +210,9 @@ struct Stager {
             for (int i = 0; i < C::NS; ++i) {
                 const int e = t + C::NT * i;
                 if (C::NS * C::NT == C::TL + C::TR || e < C::TL + C::TR) {
-                    if constexpr (C::kScaleBytes)
+                    if constexpr (C::SC == kE8M0 && !C::kScaleBytes)
+                        reinterpret_cast<lds_f32*>(sbuf)[e] = e8m0_value(sv[i]);
+                    else if constexpr (C::kScaleBytes)
                         sbuf[e / 64 * 64 + e % 16 * 4 + e / 16 % 4] = static_cast<uint8_t>(sv[i]);
                     else
                         reinterpret_cast<lds_u32*>(sbuf)[e] = sv[i];
@@ -303,7 +314,7 @@ __device__ __forceinline__ void mma_stage(f32x4& acc, i32x8 r, i32x8 l, int sr, 
 // rsel(y) is block x's or y's E8M0 scale; lf, rf and rvec are fp32.
 template <class C>
 struct LaneScales {
-    static constexpr bool kWords = C::SC == kE8M0 && !C::kScaleBytes;
+    static constexpr bool kWords = C::SC == kE8M0 && !C::kPutScales;
     static constexpr bool kKept = C::ELEM == kF8;  // widened operands read their words when they convert
     int lw[!kKept ? 1 : kWords ? C::BL : (C::BL + 3) / 4], rw[!kKept ? 1 : kWords ? C::BR : (C::BR + 3) / 4];
     float lf[C::BL], rf;
@@ -370,12 +381,6 @@ struct ScaleSkew {
     }
 };
 
-// 2^(b - 127) of the low byte of a word; 255 is NaN.
-__device__ __forceinline__ float e8m0_value(uint32_t w) {
-    const uint32_t b = w & 255u;
-    return __uint_as_float(b == 255u ? 0x7fc00000u : b ? b << 23 : 0x400000u);
-}
-
 // 16 one-byte values times a power of two as two bf16 fragments.
 template <bool E5M2>
 __device__ __forceinline__ i32x8 widen(i32x4 v, float scale) {
@@ -400,8 +405,17 @@ __device__ __forceinline__ void stage_products_wide(f32x4 (&acc)[C::BL][C::BR], 
                                                     const LaneScales<C>& sc, uint32_t lat, uint32_t rat, int wl, int wr,
                                                     int lane, int rem, const K& skew, int s) {
     const int g = lane / 16;
+    auto scale = [&](int tile_row, int block) {  // E8M0, of this lane's row of a block
+        if constexpr (C::SC != kE8M0)
+            return 1.f;
+        else if constexpr (C::kPutScales)
+            return reinterpret_cast<const lds_f32*>(sbuf)[tile_row + lane % 16];
+        else
+            return e8m0_value(skew.word(sbuf, tile_row + lane % 16, block, s));
+    };
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
+        __builtin_amdgcn_sched_barrier(0);  // both halves' fragments at once would not fit in registers
         auto piece = [&](const lds_u8* tile, uint32_t at, uint32_t off) {
             i32x4 v = *reinterpret_cast<const lds_i32x4*>(tile + (at ^ (64u * j)) + off);
             if constexpr (TAIL) v = keep_bytes(v, rem - 16 * g - 64 * j);
@@ -410,12 +424,11 @@ __device__ __forceinline__ void stage_products_wide(f32x4 (&acc)[C::BL][C::BR], 
         i32x8 lf[C::BL];
 #pragma unroll
         for (int x = 0; x < C::BL; ++x)
-            lf[x] = widen<C::LT == 1>(piece(buf, lat, 2048 * x), C::SC == kE8M0 ? e8m0_value(skew.word(sbuf, (wl * C::BL + x) * 16 + lane % 16, x, s)) : 1.f);
+            lf[x] = widen<C::LT == 1>(piece(buf, lat, 2048 * x), scale((wl * C::BL + x) * 16, x));
 #pragma unroll
         for (int y = 0; y < C::BR; ++y) {
-            const float rscale =
-                C::SC == kE8M0 ? e8m0_value(skew.word(sbuf, C::TL + (wr * C::BR + y) * 16 + lane % 16, C::BL + y, s)) : 1.f;
-            const i32x8 rf = widen<C::RT == 1>(piece(buf + C::TL * 128, rat, 2048 * y), rscale);
+            const i32x8 rf = widen<C::RT == 1>(piece(buf + C::TL * 128, rat, 2048 * y),
+                                               scale(C::TL + (wr * C::BR + y) * 16, C::BL + y));
             const f32x4 rs = sc.rvec(sbuf, wr, y, lane);
 #pragma unroll
             for (int x = 0; x < C::BL; ++x) {
@@ -586,16 +599,26 @@ __device__ __forceinline__ void tile_product(f32x4 (&acc)[C::BL][C::BR], const O
         // fetch it again), the barrier covers the other waves', and with it all
         // are done with stage s - 1, whose buffer the next loads take.
         constexpr int N = C::NBUF;
+        auto issue = [&](int64_t s, lds_u8* buf) {
+            if constexpr (C::kPutScales)
+                st.issue(s, buf);
+            else
+                st.issue_deep(s, buf);
+        };
         std::conditional_t<LaneScales<C>::kWords, ScaleSkew<C>, NoSkew> skew;
         if constexpr (LaneScales<C>::kWords) skew.init(L, R, l0, r0, wl, wr, l16);
 #pragma unroll
-        for (int i = 0; i < N - 1; ++i) st.issue_deep(i < stages ? i : stages - 1, lds + i * C::kStage);
+        for (int i = 0; i < N - 1; ++i) issue(i < stages ? i : stages - 1, lds + i * C::kStage);
         int at_buf = 0;
         auto begin = [&](int64_t s) {
             asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((N - 2) * Stager<C>::kLoads) : "memory");
+            if constexpr (C::kPutScales) {
+                st.put_scales(lds + at_buf * C::kStage + C::kBuf);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
             wg_barrier();
             const int prev = at_buf == 0 ? N - 1 : at_buf - 1;
-            st.issue_deep(s + N - 1 < stages ? s + N - 1 : stages - 1, lds + prev * C::kStage);
+            issue(s + N - 1 < stages ? s + N - 1 : stages - 1, lds + prev * C::kStage);
             const lds_u8* buf = lds + at_buf * C::kStage;
             at_buf = at_buf + 1 == N ? 0 : at_buf + 1;
             sc.read(buf + C::kBuf, wl, wr, lane, skew, static_cast<int>(s));
