@@ -86,40 +86,47 @@ def test_quant_equals_definition(xt, kind, square, r, c):
     check_quant(qt, st, np.ascontiguousarray(xf.T), kind, square)
 
 
+@pytest.mark.parametrize("xt", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
-def test_every_rounding_and_tie(kind):
+def test_every_rounding_and_tie(kind, xt):
     """Every bf16 significand at every distance from the block's largest value."""
     announce("quant ties", kind)
     m = np.arange(128, 256) / 128.0
     rows = []
-    for d in range(0, 24):
+    for d in range(0, 24 if xt != "fp16" else 7):  # what a fp16 still holds exactly
         rows.append(np.concatenate([[1.75], (m * 2.0 ** -d)[:127]]))
         rows.append(np.concatenate([[-1.0], -(m * 2.0 ** -d)[1:]]) if d else np.concatenate([[-1.9921875], -m[:127]]))
     x = np.stack(rows)
-    t = torch.from_numpy(x).to(torch.bfloat16)
+    dt, code = XT[xt]
+    t = torch.from_numpy(x).to(dt)
     assert np.array_equal(t.double().numpy(), x)
-    q, s, qt, st = quant(t.to(DEV), kind, False, T.SCALE_E8M0, x_type=T.X_BF16)
+    q, s, qt, st = quant(t.to(DEV), kind, False, T.SCALE_E8M0, x_type=code)
     check_quant(q, s, x, kind, False)
     check_quant(qt, st, np.ascontiguousarray(x.T), kind, False)
 
 
+@pytest.mark.parametrize("xt", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("square", [False, True])
-def test_special_values(kind, square):
-    announce("quant special", kind, square)
-    x = values(140, 260, 3).astype(np.float32)
+def test_special_values(kind, square, xt):
+    announce("quant special", kind, square, xt)
+    dt, code = XT[xt]
+    x = values(140, 260, 3, spread=0.5).astype(np.float32)
     x[0, :] = 0
     x[1, 5], x[2, 7], x[3, 130] = np.inf, -np.inf, np.nan
     x[4, :] = np.nan
     x[5, :128] = np.inf
-    x[6, :] = 1e-42  # subnormal
-    x[7, 3] = 3.4e38
+    x[6, :] = {"bf16": 1e-40, "fp16": 1e-7, "fp32": 1e-42}[xt]  # subnormal
+    x[7, 3] = {"bf16": 3.3e38, "fp16": 65504.0, "fp32": 3.4e38}[xt]
     x[8, :] = -0.0
     x[9, :128] = 448.0
     x[9, 128:] = np.nextafter(np.float32(448.0), np.float32(1e9))
-    q, s, qt, st = quant(torch.from_numpy(x).to(DEV), kind, square, T.SCALE_E8M0, x_type=T.X_F32)
-    check_quant(q, s, x.astype(np.float64), kind, square)
-    check_quant(qt, st, np.ascontiguousarray(x.T.astype(np.float64)), kind, square)
+    x[10, :] = {"bf16": 2.0 ** -126, "fp16": 2.0 ** -24, "fp32": 2.0 ** -149}[xt]
+    t = torch.from_numpy(x).to(dt)
+    q, s, qt, st = quant(t.to(DEV), kind, square, T.SCALE_E8M0, x_type=code)
+    xf = t.double().numpy()
+    check_quant(q, s, xf, kind, square)
+    check_quant(qt, st, np.ascontiguousarray(xf.T), kind, square)
 
 
 @pytest.mark.parametrize("off,ld", [(0, 264), (1, 264), (0, 261), (4, 300)])
