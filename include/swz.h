@@ -487,13 +487,13 @@ int swz_quant_f8(const void* d_x, int32_t x_type, int64_t rows, int64_t cols, in
  *               inputs.
  * A forward product takes activations in rows (1x128) and weights in squares
  * (128x128); the data gradient the weight's transpose; the weight gradient
- * both transposes in rows.  Any m, n, k >= 0: calls with few rows of A (up to
- * 64) go to kernels that stream B once.  d_a, d_b 16-byte aligned, fp32 scales
+ * both transposes in rows.  Any m, n, k >= 0; calls with up to 16 rows of A go
+ * to a kernel that streams B once.  d_a, d_b 16-byte aligned, fp32 scales
  * 4-byte, d_c aligned to its element; rows of C whose pitch and start are
  * multiples of 16 bytes are written in 16-byte pieces.
  * A float C is summed in fp32 from exact products (the operands widened to
  * bf16, at the bf16 rate); with SWZ_SCALE_E8M0 a value times its scale has to
- * be a normal bf16 number for that.  A bf16 C takes the 8-bit matrix
+ * be a normal bf16 number for that.  So is a bf16 C of at most 16 rows; any other takes the 8-bit matrix
  * instruction, which adds the products of each eight consecutive k after
  * dropping what lies more than 13 bits below the largest of them (1.5e-5 of
  * the norm of a product of normal operands, a hundredth of the rounding to
@@ -501,7 +501,8 @@ int swz_quant_f8(const void* d_x, int32_t x_type, int64_t rows, int64_t cols, in
  * multiply fp32 sums within their block.
  * NaN and infinities in the used elements and scales propagate.
  * Errors: SWZ_EINVAL (sizes, pitches, alignment, NULL, overlap, enum values),
- * SWZ_EUNSUPPORTED (lda or ldb of 2^23 and more, or over 2^22 tiles of C). */
+ * SWZ_EUNSUPPORTED (lda or ldb of 2^23 and more; n of 2^26 and more; over 2^22
+ * tiles of 256 x 256 of C). */
 int swz_gemm_f8(const void* d_a, const void* d_scale_a, const void* d_b, const void* d_scale_b, void* d_c, int64_t m,
                 int64_t n, int64_t k, int64_t lda, int64_t ldb, int32_t a_type, int32_t b_type, int32_t a_block,
                 int32_t b_block, int32_t scale_type, int32_t c_type, void* stream);

@@ -317,3 +317,80 @@ def test_gradient_against_differences():
     move = np.abs(w @ direction.T).max(axis=0)
     tol = eps ** 2 / 6 * (2 * move) ** 3 + 64 * 30 * U / eps + 2.0 ** -7 * np.abs(d["dh"].double().cpu().numpy()).sum(axis=1)
     assert np.all(np.abs(diff - slope) <= tol)
+
+
+def test_vocabulary_behind_2_to_32_bytes():
+    """W and dW of 4.6 GB: losses, dh and the first and last rows of dW against torch in 64 bits on the GPU, with the
+    tolerances of one rounding of dz (2^-11) and of the result (2^-8), and fp32 sums of k and v products."""
+    announce("ce 2^32")
+    n, v, k = 8, 140001, 16392
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    w = torch.empty(v, k, dtype=torch.bfloat16, device=DEV)
+    for i in range(0, v, 20000):
+        w[i:i + 20000] = torch.randn(min(20000, v - i), k, generator=g, device=DEV) / 128
+    h = torch.randn(n, k, generator=g, device=DEV).bfloat16()
+    target = torch.tensor([0, 131071, 131072, v - 1, -1, 7, 140000, 65536], device=DEV)
+    up = torch.full((n,), 0.125, device=DEV)
+    f = [torch.empty(n, device=DEV) for _ in range(3)]
+    ws = torch.empty(T.swz_linear_loss_workspace(n, v, k, grad=True), dtype=torch.uint8, device=DEV)
+    dh, dw = torch.empty_like(h), torch.empty_like(w)
+    T.swz_linear_ce(h, w, target, *f, n, v, k, ws)
+    T.swz_linear_ce_grad(h, w, target, f[1], f[2], up, dh, dw, n, v, k, ws)
+    z = torch.cat([h.double() @ w[i:i + 20000].double().t() for i in range(0, v, 20000)], dim=1)
+    lse = torch.logsumexp(z, dim=1)
+    counts = target >= 0
+    at = target.clamp(min=0)
+    loss = torch.where(counts, lse - z[torch.arange(n, device=DEV), at], 0.0)
+    ez = (k + 2) * U * (h.double().abs().sum(1) * w.abs().max().double()).max().item() + 1100 * U
+    assert (f[1].double() - lse).abs().max().item() <= ez and (f[0].double() - loss).abs().max().item() <= 2 * ez
+    p = torch.exp(z - lse[:, None])
+    p[torch.arange(n, device=DEV), at] -= 1
+    dz = torch.where(counts[:, None], 0.125 * p, 0.0)
+    rel = 2.0 ** -11 + 2 * ez + 2.0 ** -8
+    rows = torch.tensor([0, 1, 7, 65536, 131071, 131072, v - 2, v - 1], device=DEV)
+    ref, size = dz[:, rows].t() @ h.double(), dz[:, rows].t().abs() @ h.double().abs()
+    assert bool(((dw[rows].double() - ref).abs() <= rel * size + 1e-30).all())
+    ref = sum(dz[:, i:i + 20000] @ w[i:i + 20000].double() for i in range(0, v, 20000))
+    size = sum(dz[:, i:i + 20000].abs() @ w[i:i + 20000].double().abs() for i in range(0, v, 20000))
+    assert bool(((dh.double() - ref).abs() <= rel * size + 1e-30).all())
+
+
+def test_layer_and_loss_as_a_step():
+    """The 8-bit layer, the loss on its output, and back through both: what a training step runs."""
+    announce("step")
+    rng = np.random.default_rng(30)
+    tok, hid, v = 200, 256, 1111
+    x = torch.from_numpy(rng.standard_normal((tok, hid))).bfloat16().to(DEV)
+    w1 = torch.from_numpy(rng.standard_normal((hid, hid)) / 16).float().to(DEV)
+    w2 = torch.from_numpy(rng.standard_normal((v, hid)) / 16).bfloat16().to(DEV)
+    target = torch.from_numpy(rng.integers(0, v, tok)).to(DEV)
+    u8 = lambda *s: torch.empty(s, dtype=torch.uint8, device=DEV)  # noqa: E731
+    xq, xs, xt, xts = u8(tok, hid), u8(tok, 2), u8(hid, 208), u8(hid, 2)
+    wq, wsc, wt, wts = u8(hid, hid), u8(2, 2), u8(hid, hid), u8(2, 2)
+    T.swz_quant_f8(x, xq, xs, tok, hid, qt=xt, scale_t=xts)
+    T.swz_quant_f8(w1, wq, wsc, hid, hid, x_type=T.X_F32, block=T.BLOCK_128X128, qt=wt, scale_t=wts)
+    h = torch.empty(tok, hid, dtype=torch.bfloat16, device=DEV)
+    T.swz_gemm_f8(xq, xs, wq, wsc, h, tok, hid, hid)
+    ws = u8(T.swz_linear_loss_workspace(tok, v, hid, grad=True))
+    loss, lse, zt = (torch.empty(tok, device=DEV) for _ in range(3))
+    dh, dw2 = torch.empty_like(h), torch.empty_like(w2)
+    up = torch.full((tok,), 1 / tok, device=DEV)
+    T.swz_linear_ce(h, w2, target, loss, lse, zt, tok, v, hid, ws)
+    T.swz_linear_ce_grad(h, w2, target, lse, zt, up, dh, dw2, tok, v, hid, ws)
+    gq, gs, gt, gts = u8(tok, hid), u8(tok, 2), u8(hid, 208), u8(hid, 2)
+    T.swz_quant_f8(dh, gq, gs, tok, hid, f8_type=T.F8_E5M2, qt=gt, scale_t=gts)
+    dx, dw1 = torch.empty_like(x), torch.empty_like(w1)
+    T.swz_gemm_f8(gq, gs, wt, wts, dx, tok, hid, hid, a_type=T.F8_E5M2)
+    T.swz_gemm_f8(gt, gts, xt, xts, dw1, hid, hid, tok, a_type=T.F8_E5M2, b_block=T.BLOCK_1X128, c_type=T.C_F32)
+    torch.cuda.synchronize()
+    hd = h.double().cpu().numpy()
+    ref = P.linear_loss(hd, w2.double().cpu().numpy(), target.cpu().numpy(), None, 1.0, np.full(tok, 1 / tok))
+    assert np.abs(loss.double().cpu().numpy() - ref["loss"]).max() < 1e-4
+    for got, r in ((dh, ref["dh"]), (dw2, ref["dw"])):
+        assert np.linalg.norm(got.double().cpu().numpy() - r) <= 2.0 ** -8 * np.linalg.norm(r)
+    deq = lambda q, s, c, kind, sq: P.dequantize(q.cpu().numpy()[:, :c], kind, s.cpu().numpy(), sq)  # noqa: E731
+    rdx = deq(gq, gs, hid, "e5m2", False) @ deq(wt, wts, hid, "e4m3", True).T
+    rdw = deq(gt, gts, tok, "e5m2", False) @ deq(xt, xts, tok, "e4m3", False).T
+    assert np.linalg.norm(dx.double().cpu().numpy() - rdx) <= 2.0 ** -8 * np.linalg.norm(rdx)
+    assert np.linalg.norm(dw1.double().cpu().numpy() - rdw) <= 2.0 ** -18 * np.linalg.norm(rdw)

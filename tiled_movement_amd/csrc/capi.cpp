@@ -761,7 +761,7 @@ SWZ_API int swz_gemm_f8(const void* d_a, const void* d_scale_a, const void* d_b,
             return SWZ_EINVAL;
     }
     if (lda >= kMaxPitch || ldb >= kMaxPitch) return SWZ_EUNSUPPORTED;
-    if ((m - 1) / 16 + 1 > (int64_t(1) << 30) / ((n - 1) / 16 + 1)) return SWZ_EUNSUPPORTED;
+    if (n >= int64_t(1) << 26 || (m - 1) / 256 + 1 > ((int64_t(1) << 22) - 1) / ((n - 1) / 256 + 1)) return SWZ_EUNSUPPORTED;
     const swz::GemmF8Job job{d_a, d_scale_a, d_b, d_scale_b, d_c, m, n, k, lda, ldb, a_type == SWZ_F8_E5M2,
                              b_type == SWZ_F8_E5M2, sqa, sqb, scale_type == SWZ_SCALE_E8M0, c_type == SWZ_C_BF16};
     return hip_status(swz::launch_gemm_f8(job, static_cast<hipStream_t>(stream)));

@@ -175,7 +175,11 @@ struct Stager {
         }
     }
     __device__ __forceinline__ void issue(int64_t s, lds_u8* buf) {
-        fl.issue(s, kbytes - s * 128, buf, wave);
+        issue_l(s, buf);
+        issue_r(s, buf);
+    }
+    __device__ __forceinline__ void issue_l(int64_t s, lds_u8* buf) const { fl.issue(s, kbytes - s * 128, buf, wave); }
+    __device__ __forceinline__ void issue_r(int64_t s, lds_u8* buf) {
         fr.issue(s, kbytes - s * 128, buf + C::TL * 128, wave);
         if constexpr (C::SC == kE8M0) {
 #pragma unroll
@@ -474,21 +478,27 @@ __device__ __forceinline__ void stage_products(f32x4 (&acc)[C::BL][C::BR], const
 // reads its next fragments.  A stage is four quadrants of 2 x 4 blocks in the
 // order (L0 R0) (L1 R0) (L1 R1) (L0 R1), each with one new operand half, which
 // the slot before it reads: L0, L1, R1, and R0 of the next stage.
-// Measured at 8192 x 8192 x 4096: 221 us, 2.48 PFLOP/s of one-byte operands
-// (236 us with all waves in step: reads, then products, one barrier a stage);
-// bf16 logits and gradients 1.17 to 1.25 PFLOP/s.  No better: the halves in
-// the order L0 R0, L0 R1, L1 R1, L1 R0 (12, 8, 4 and 0 reads a slot; 221 us),
-// and a pipelined loop with one barrier a stage whose reads run one quadrant
-// ahead (267 us with 21 registers spilled; two-byte operands, none spilled, 3%
-// behind).  Bound by LDS: the fragment reads (192 KiB) and fills (64 KiB) of a
-// stage take as long at 128 bytes a cycle as its products, 2048 cycles a
-// SIMD, and the matrix units are busy 53% of the cycles at 2.1 GHz.
+// Measured at 8192 x 8192 x 4096 with one-byte operands, in turn on one box:
+// 229 us (2.40 PFLOP/s), 240 with all of a stage's loads in one slot; before
+// that 236 with all waves in step (reads, then products, one barrier a stage).
+// No better: the halves in the order L0 R0, L0 R1, L1 R1, L1 R0 (12, 8, 4 and 0
+// reads a slot), a pipelined loop with one barrier a stage whose reads run one
+// quadrant ahead (267 us, 21 registers spilled), and L's loads two slots before
+// R's (269 us).  What bounds it, from builds that leave one thing out: without
+// the loads into LDS 161 us, with half of them 175, without waiting for them
+// 219, without the fragment reads 222, without barriers 209.  So it is the rate
+// of the loads into LDS, 64 KiB a stage and workgroup; the matrix units are
+// busy 53% of the cycles at 2.1 GHz.
 // Slots of stage s, counted from the leading waves' first (8 s; the second half
 // is one later):
 //   8s + 4: R1 is read, and then no fragment of stage s is missing; each wave
 //           waits for its reads and for its loads of stage s + 1;
 //   8s + 6: stage s + 1 has landed for all (the last wait is in slot 8s + 5)
 //           and its R0 is read; stage s + 2's loads may overwrite stage s.
+//           Two-byte operands issue all of them here; one-byte operands R's
+//           here and L's in slot 8s + 8 (8192 x 8192 x 4096: 213 us, all at
+//           once 220; cross entropy with gradients at 4096 x 65536 x 4096 in
+//           bf16 8.22 ms so split, 7.63 at once; both in turn on one box).
 template <class C>
 __device__ __forceinline__ void pingpong(f32x4 (&acc)[C::BL][C::BR], Stager<C>& st, lds_u8* lds, lds_u8* sbufs, uint32_t lat,
                                          uint32_t rat, int wl, int wr, int lane, int64_t full, int64_t stages) {
@@ -509,8 +519,10 @@ __device__ __forceinline__ void pingpong(f32x4 (&acc)[C::BL][C::BR], Stager<C>& 
 #pragma unroll
         for (int x = 0; x < 2; ++x) l[h][x] = read_frag<false>(buf, lat, 2048 * (2 * h + x), g, 128);
     };
-    // stage 0 has landed; stage 1 (or stage 0 again) on its way to the other buffer
-    st.issue(stages > 1 ? 1 : 0, lds + C::kBuf);
+    // stage 0 has landed; stage 1 (or stage 0 again) goes to the other buffer
+    constexpr bool kSplit = C::ELEM == kF8;
+    if constexpr (!kSplit) st.issue_l(stages > 1 ? 1 : 0, lds + C::kBuf);
+    st.issue_r(stages > 1 ? 1 : 0, lds + C::kBuf);
     read_r(lds, 0);
     if (lag) slot();
     // No branch inside: across one the compiler moves products out of their
@@ -532,6 +544,7 @@ __device__ __forceinline__ void pingpong(f32x4 (&acc)[C::BL][C::BR], Stager<C>& 
             }
             __builtin_amdgcn_s_setprio(0);
         };
+        if constexpr (kSplit) st.issue_l(s + 1 < stages ? s + 1 : s, lds + ((s + 1) & 1) * C::kBuf);
         sc.read(sbuf, wl, wr, lane, NoSkew{}, 0);
         read_l(buf, 0);
         slot();
@@ -549,7 +562,8 @@ __device__ __forceinline__ void pingpong(f32x4 (&acc)[C::BL][C::BR], Stager<C>& 
         products(1, 1);
         slot();
         read_r(lds + ((s + 1) & 1) * C::kBuf, 0);
-        st.issue(s + 2 < stages ? s + 2 : stages - 1, buf);
+        if constexpr (!kSplit) st.issue_l(s + 2 < stages ? s + 2 : stages - 1, buf);
+        st.issue_r(s + 2 < stages ? s + 2 : stages - 1, buf);
         slot();
         products(0, 1);
         slot();
