@@ -91,7 +91,7 @@ swz::LossPlan plan_loss(int64_t n, int64_t v, int64_t k, int32_t top) {
     p.piece = piece_words(v, most, (n + tl - 1) / tl + (n == 0));
     const int64_t tiles = ((n + tl - 1) / tl) * ((k + 255) / 256), stages = p.piece / 64;
     p.parts = tiles >= 256 || tiles == 0 ? 1 : 256 / tiles;
-    if (p.parts > 16) p.parts = 16;
+    if (p.parts > 32) p.parts = 32;
     if (p.parts > stages / 8) p.parts = stages / 8 ? stages / 8 : 1;
     const int64_t ldn = up(n, 8);
     int64_t at = 0;
