@@ -251,6 +251,47 @@ def test_gemm_nan_stays_in_its_row_and_column(m):
     assert np.array_equal(got, ref, equal_nan=True)
 
 
+@pytest.mark.parametrize("m", [4, 90, 300])
+@pytest.mark.parametrize("c_type", [T.C_F32, T.C_BF16])
+@pytest.mark.parametrize("scale_type", [T.SCALE_F32, T.SCALE_E8M0])
+def test_gemm_nan_scales_and_infinities(m, c_type, scale_type):
+    """A NaN scale makes its row (or its 128 rows of B) NaN; an e5m2 infinity its row infinite."""
+    announce("gemm nan scale", m, c_type, scale_type)
+    n, k = 300, 392
+    a = operand(m, k, "e5m2", False, scale_type, 8, exact=True)
+    b = operand(n, k, "e4m3", True, scale_type, 9, exact=True)
+    b[0][:, 5] = 0x38  # ones where the infinity meets them
+    bad = float("nan") if scale_type == T.SCALE_F32 else 255
+    a[1][1, 2] = bad
+    b[1][1, 3] = bad
+    a[0][2, 5] = 0x7C
+    got = gemm(a, b, m, n, k, "e5m2", "e4m3", False, True, scale_type, c_type)
+    assert np.all(np.isnan(got[1])) and np.all(np.isnan(got[:, 128:256]))
+    rest = np.r_[0:128, 256:n]
+    assert np.all(np.isposinf(got[2, rest]))
+    rows = np.array([r for r in range(m) if r not in (1, 2)])
+    assert np.all(np.isfinite(got[np.ix_(rows, rest)]))
+
+
+@pytest.mark.parametrize("m", [4, 90])
+@pytest.mark.parametrize("ea,eb", [(1, 200), (253, 60), (30, 30), (127, 127)])
+def test_gemm_far_scales(m, ea, eb):
+    """E8M0 scales far from one (their values times them stay normal bf16 numbers): exact where the result is normal."""
+    announce("gemm far scales", m, ea, eb)
+    n, k = 140, 256
+    a = operand(m, k, "e4m3", False, T.SCALE_E8M0, 8, exact=True)
+    b = operand(n, k, "e4m3", True, T.SCALE_E8M0, 9, exact=True)
+    raw = P.product_f8(P.f8_decode(a[0].cpu().numpy()[:, :k], "e4m3"), P.f8_decode(b[0].cpu().numpy()[:, :k], "e4m3"))
+    a[1].fill_(ea)
+    b[1].fill_(eb)
+    ref = raw * 2.0 ** (ea + eb - 254)
+    got = gemm(a, b, m, n, k, "e4m3", "e4m3", False, True, T.SCALE_E8M0, T.C_F32)
+    if ea + eb - 254 > -120:
+        assert np.array_equal(got, ref)
+    else:  # products below the normal range of fp32: nothing but zero or the rounded value
+        assert np.all(np.abs(got - ref) <= 2.0 ** -126 * k)
+
+
 # ------------------------------------------------------------- as they are used
 def test_training_layer_with_its_gradients():
     """x -> quantize -> y = x w^T; dy -> dx = dy w, dw = dy^T x, all of 8-bit operands, chained as a training step

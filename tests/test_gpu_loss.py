@@ -163,6 +163,27 @@ def test_no_row_counts(top):
     assert torch.all(torch.isfinite(d["lse"]))
 
 
+@pytest.mark.parametrize("tau", [0.5, 1.0, 4.0])
+def test_teacher_entries_masked_by_the_lowest_float(tau):
+    """Entries at the lowest float have no weight beside others, and equal weights among themselves."""
+    announce("lowest float", tau)
+    c = Case(20, 300, 64, top=6, tau=tau, seed=13, absent=0.0)
+    c.teacher[:] = np.random.default_rng(0).standard_normal(c.teacher.shape)
+    low = np.finfo(np.float32).min
+    c.teacher[3, 2:] = low
+    c.teacher[4, :] = low
+    c.teacher[5, 1:] = -np.inf
+    d = c.device()
+    c.forward(d)
+    c.backward(d)
+    torch.cuda.synchronize()
+    assert torch.all(torch.isfinite(d["loss"])) and torch.all(torch.isfinite(d["dw"]))
+    # the same weights without the overflow that the bounds would meet
+    c.teacher[3, 2:] = -200 * tau
+    c.teacher[4, :] = 0
+    c.check(d)
+
+
 def test_rows_that_do_not_count_may_hold_anything():
     """NaN in a row whose target is absent stays in its lse."""
     announce("nan in an ignored row")

@@ -189,20 +189,22 @@ __global__ __launch_bounds__(256) void k_target_loss(const uint16_t* __restrict_
         bool any = false;
         for (int j = lane; j < top; j += 64) {
             const float t = teacher[row * top + j];
-            if (entry_counts(index[row * top + j], t, v)) m = fmaxf(m, t / tau), any = true;
+            if (entry_counts(index[row * top + j], t, v)) m = fmaxf(m, t), any = true;
         }
+        // (t - m) / tau, not t / tau - m / tau: the lowest float over a tau below
+        // one would overflow
         if (__any(any)) {
             m = wave_max(m);
             float s = 0.f;
             for (int j = lane; j < top; j += 64) {
                 const float t = teacher[row * top + j];
-                if (entry_counts(index[row * top + j], t, v)) s += expf(t / tau - m);
+                if (entry_counts(index[row * top + j], t, v)) s += expf((t - m) / tau);
             }
             const float ls = logf(wave_sum(s));
             for (int j = lane; j < top; j += 64) {
                 const float t = teacher[row * top + j];
                 if (!entry_counts(index[row * top + j], t, v)) continue;
-                const float lp = t / tau - m - ls, p = expf(lp);
+                const float lp = (t - m) / tau - ls, p = expf(lp);
                 out += p > 0.f || p != p ? p * (lp - (z[j] / tau - l)) : 0.f;
             }
             out = tau * tau * wave_sum(out);
@@ -270,7 +272,7 @@ __global__ __launch_bounds__(64) void k_loss_prep(const int64_t* __restrict__ in
         float m = -__builtin_inff();
         for (int j = lane; j < top; j += 64) {
             const float t = teacher[row * top + j];
-            if (entry_counts(index[row * top + j], t, v)) m = fmaxf(m, t / tau), any = true;
+            if (entry_counts(index[row * top + j], t, v)) m = fmaxf(m, t), any = true;
         }
         any = __any(any);
         m = wave_max(m);
@@ -278,7 +280,7 @@ __global__ __launch_bounds__(64) void k_loss_prep(const int64_t* __restrict__ in
         for (int j = lane; j < top; j += 64) {
             const float t = teacher[row * top + j];
             const bool here = entry_counts(index[row * top + j], t, v);
-            const float e = here ? expf(t / tau - m) : 0.f;
+            const float e = here ? expf((t - m) / tau) : 0.f;
             words[j] = here ? index[row * top + j] : -1;
             p[j] = e;
             s += e;
@@ -295,7 +297,8 @@ __global__ __launch_bounds__(64) void k_loss_prep(const int64_t* __restrict__ in
         const float gt = any ? upstream[row] * tau : 0.f;
         g[row] = gt;
         const uint32_t b = __float_as_uint(gt) & 0x7fffffffu;
-        if (b && b < 0x7f800000u) atomicMax(slot, b);
+        // (one atomic a row took most of the kernel's time; a mean's upstream is the same for all rows)
+        if (b < 0x7f800000u && b > __hip_atomic_load(slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(slot, b);
     }
 }
 
