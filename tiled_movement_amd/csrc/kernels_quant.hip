@@ -14,7 +14,10 @@
 // a scale of a / F.  Infinities and NaN stay out of a and are stored as NaN
 // (e5m2 keeps infinities): one bad element does not spoil its block.
 //
-// The kernel is bound by HBM: 2 or 4 bytes read, 1 or 2 written per element.
+// The kernels are bound by HBM: 2 or 4 bytes read, 1 or 2 written per element.
+// 8192 x 4096 bf16 with the transpose 29 us, 4.6 TB/s (35 us when every element
+// was unpacked, multiplied and tested for NaN by itself); 5001 x 6008 fp32 in
+// squares with the transpose 36 us, 5.0 TB/s.
 #include "launch.h"
 
 namespace swz {
