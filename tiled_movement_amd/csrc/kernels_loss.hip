@@ -51,11 +51,12 @@ __device__ __forceinline__ float half_bits_to_f32(uint16_t b, bool bf16) {
 // sum of 2^(t - maximum)) of t = z log2(e) / tau.
 template <class C>
 __global__ __launch_bounds__(C::NT) void k_logit_stats(Operand H, Operand W, int64_t kbytes, float c2,
-                                                       float2* __restrict__ part, uint32_t tiles_m) {
+                                                       float2* __restrict__ part, TileMap map) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
-    const int64_t tn = blockIdx.x / tiles_m;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x % tiles_m) * C::TL, j0 = tn * C::TR;
+    int64_t tm, tn;
+    if (!map.at(blockIdx.x, &tm, &tn)) return;
+    const int64_t i0 = tm * C::TL, j0 = tn * C::TR;
     f32x4 acc[C::BL][C::BR];
     tile_product<C>(acc, H, W, i0, j0, kbytes, lds);
     const int t = threadIdx.x, lane = t % 64, g = lane / 16, l16 = lane % 16;
@@ -362,11 +363,12 @@ template <class C>
 __global__ __launch_bounds__(C::NT) void k_dz(Operand H, Operand W, int64_t kbytes, float c2,
                                               const float* __restrict__ lse, const float* __restrict__ g,
                                               const uint32_t* __restrict__ slots, _Float16* __restrict__ dz, int64_t ldz,
-                                              uint32_t tiles_m) {
+                                              TileMap map) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x % tiles_m) * C::TL;
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x / tiles_m) * C::TR;
+    int64_t tm, tn;
+    if (!map.at(blockIdx.x, &tm, &tn)) return;
+    const int64_t i0 = tm * C::TL, j0 = tn * C::TR;
     f32x4 acc[C::BL][C::BR];
     tile_product<C>(acc, H, W, i0, j0, kbytes, lds);
     const int t = threadIdx.x, lane = t % 64, l16 = lane % 16;
@@ -412,11 +414,12 @@ __global__ __launch_bounds__(256) void k_dz_targets(const int64_t* __restrict__ 
 // dW of a piece: rows are words (L = dz^T), columns k (R = H^T).
 template <class C, class CT>
 __global__ __launch_bounds__(C::NT) void k_grad_w(Operand Z, Operand H, int64_t kbytes, CT* __restrict__ dw, int64_t k,
-                                                  const uint32_t* __restrict__ slots, uint32_t tiles_n) {
+                                                  const uint32_t* __restrict__ slots, TileMap map) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x / tiles_n) * C::TL;
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x % tiles_n) * C::TR;
+    int64_t tm, tn;
+    if (!map.at(blockIdx.x, &tn, &tm)) return;
+    const int64_t i0 = tm * C::TL, j0 = tn * C::TR;
     f32x4 acc[C::BL][C::BR];
     tile_product<C>(acc, Z, H, i0, j0, kbytes, lds);
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -429,11 +432,12 @@ __global__ __launch_bounds__(C::NT) void k_grad_w(Operand Z, Operand H, int64_t 
 // dH's sum over a part of a piece's words into its own fp32 buffer (blockIdx.y).
 template <class C>
 __global__ __launch_bounds__(C::NT) void k_grad_h(Operand Z, Operand W, int64_t kbytes, int64_t part_bytes,
-                                                  float* __restrict__ sums, int add, uint32_t tiles_m) {
+                                                  float* __restrict__ sums, int add, TileMap map) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x % tiles_m) * C::TL;
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x / tiles_m) * C::TR;
+    int64_t tm, tn;
+    if (!map.at(blockIdx.x, &tm, &tn)) return;
+    const int64_t i0 = tm * C::TL, j0 = tn * C::TR;
     const int64_t k0 = static_cast<int64_t>(blockIdx.y) * part_bytes;
     int64_t kb = kbytes - k0 < part_bytes ? kbytes - k0 : part_bytes;
     if (kb < 0) kb = 0;
@@ -521,8 +525,8 @@ hipError_t launch_loss(const LossJob& j, hipStream_t stream) {
         using C = decltype(cfg);
         const int64_t tm = (j.n + C::TL - 1) / C::TL;
         tiles = (j.v + C::TR - 1) / C::TR;
-        hipLaunchKernelGGL(k_logit_stats<C>, dim3(static_cast<unsigned>(tm * tiles)), dim3(C::NT), 0, stream, H, W, 2 * j.k,
-                           c2, part, static_cast<uint32_t>(tm));
+        const TileMap map = TileMap::make(tm, tiles);
+        hipLaunchKernelGGL(k_logit_stats<C>, dim3(map.grid), dim3(C::NT), 0, stream, H, W, 2 * j.k, c2, part, map);
         return hipGetLastError();
     });
     if (e != hipSuccess) return e;
@@ -573,8 +577,8 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
         e = by_rows(j.n, j.bf16, [&](auto cfg) {
             using C = decltype(cfg);
             const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (vc + C::TR - 1) / C::TR;
-            hipLaunchKernelGGL(k_dz<C>, dim3(static_cast<unsigned>(tm * tn)), dim3(C::NT), 0, stream, H, W, 2 * j.k, c2, j.lse,
-                               g, slots, dz, ldz, static_cast<uint32_t>(tm));
+            const TileMap map = TileMap::make(tm, tn);
+            hipLaunchKernelGGL(k_dz<C>, dim3(map.grid), dim3(C::NT), 0, stream, H, W, 2 * j.k, c2, j.lse, g, slots, dz, ldz, map);
             return hipGetLastError();
         });
         if (e != hipSuccess) return e;
@@ -587,14 +591,14 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
             const Operand Z{reinterpret_cast<const uint8_t*>(dzt), 2 * ldn, vc, nullptr, 0, 0};
             const Operand HT{reinterpret_cast<const uint8_t*>(ht), 2 * ldn, j.k, nullptr, 0, 0};
             const int64_t tm = (vc + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
-            const dim3 grid(static_cast<unsigned>(tm * tn));
-            const auto t_n = static_cast<uint32_t>(tn);
+            const TileMap map = TileMap::make(tn, tm);
+            const dim3 grid(map.grid);
             if (j.bf16)
                 hipLaunchKernelGGL((k_grad_w<C, __bf16>), grid, dim3(C::NT), 0, stream, Z, HT, 2 * j.n,
-                                   static_cast<__bf16*>(j.dw) + v0 * j.k, j.k, slots, t_n);
+                                   static_cast<__bf16*>(j.dw) + v0 * j.k, j.k, slots, map);
             else
                 hipLaunchKernelGGL((k_grad_w<C, _Float16>), grid, dim3(C::NT), 0, stream, Z, HT, 2 * j.n,
-                                   static_cast<_Float16*>(j.dw) + v0 * j.k, j.k, slots, t_n);
+                                   static_cast<_Float16*>(j.dw) + v0 * j.k, j.k, slots, map);
             e = hipGetLastError();
         }
         if (j.dh && e == hipSuccess) {
@@ -607,8 +611,9 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
             e = by_rows_of<kF16>(j.n, [&](auto cfg) {
                 using C = decltype(cfg);
                 const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
-                hipLaunchKernelGGL(k_grad_h<C>, dim3(static_cast<unsigned>(tm * tn), static_cast<unsigned>(p.parts)), dim3(C::NT), 0,
-                                   stream, Z, WT, 2 * vc, part_bytes, sums, v0 > 0 ? 1 : 0, static_cast<uint32_t>(tm));
+                const TileMap map = TileMap::make(tm, tn);
+                hipLaunchKernelGGL(k_grad_h<C>, dim3(map.grid, static_cast<unsigned>(p.parts)), dim3(C::NT), 0, stream, Z, WT,
+                                   2 * vc, part_bytes, sums, v0 > 0 ? 1 : 0, map);
                 return hipGetLastError();
             });
         }
