@@ -20,12 +20,17 @@ __device__ __forceinline__ uint32_t xcd_tile(uint32_t id, uint32_t total) {
 
 template <class C, class CT>
 __global__ __launch_bounds__(C::NT) void k_gemm_f8(Operand A, Operand B, CT* __restrict__ c, int64_t ldc, int64_t k,
-                                                   uint32_t tiles_m, int vec, int by_xcd) {
+                                                   TileMap map, int vec, int by_xcd) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
-    const uint32_t tile = by_xcd ? xcd_tile(blockIdx.x, gridDim.x) : blockIdx.x;
-    const int64_t i0 = static_cast<int64_t>(tile % tiles_m) * C::TL;
-    const int64_t j0 = static_cast<int64_t>(tile / tiles_m) * C::TR;
+    int64_t tm, tn;
+    if (by_xcd) {
+        const uint32_t tile = xcd_tile(blockIdx.x, gridDim.x);
+        tm = tile % map.f, tn = tile / map.f;
+    } else if (!map.at(blockIdx.x, &tm, &tn)) {
+        return;
+    }
+    const int64_t i0 = tm * C::TL, j0 = tn * C::TR;
     f32x4 acc[C::BL][C::BR];
     tile_product<C>(acc, A, B, i0, j0, k, lds);
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -41,8 +46,9 @@ hipError_t launch_tiles(const GemmF8Job& j, bool by_xcd, hipStream_t stream) {
     const int64_t tm = (j.m + C::TL - 1) / C::TL, tn = (j.n + C::TR - 1) / C::TR;
     if (tm > 0x7fffffff / C::NT / tn) return hipErrorInvalidValue;
     const int vec = j.n * static_cast<int64_t>(sizeof(CT)) % 16 == 0 && reinterpret_cast<uintptr_t>(j.c) % 16 == 0;
-    hipLaunchKernelGGL((k_gemm_f8<C, CT>), dim3(static_cast<unsigned>(tm * tn)), dim3(C::NT), 0, stream, A, B,
-                       static_cast<CT*>(j.c), j.n, j.k, static_cast<uint32_t>(tm), vec, by_xcd ? 1 : 0);
+    const TileMap map = TileMap::make(tm, tn);
+    hipLaunchKernelGGL((k_gemm_f8<C, CT>), dim3(by_xcd ? static_cast<unsigned>(tm * tn) : map.grid), dim3(C::NT), 0, stream, A, B,
+                       static_cast<CT*>(j.c), j.n, j.k, map, vec, by_xcd ? 1 : 0);
     return hipGetLastError();
 }
 
