@@ -90,6 +90,7 @@ swz::LossPlan plan_loss(int64_t n, int64_t v, int64_t k, int32_t top) {
     const int64_t tl = n <= 64 ? 64 : n <= 128 ? 128 : 256;
     p.piece = piece_words(v, most, (n + tl - 1) / tl + (n == 0));
     const int64_t tiles = ((n + tl - 1) / tl) * ((k + 255) / 256), stages = p.piece / 64;
+    p.h_rows = tl;  // parts fill the card, so the largest tile that the rows fill
     p.parts = tiles >= 256 || tiles == 0 ? 1 : 256 / tiles;
     if (p.parts > 32) p.parts = 32;
     if (p.parts > stages / 8) p.parts = stages / 8 ? stages / 8 : 1;

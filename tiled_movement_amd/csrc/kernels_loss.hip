@@ -483,21 +483,20 @@ __global__ __launch_bounds__(256) void k_zero16(uint32_t* __restrict__ p, int64_
 
 unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); }
 
-// Tile of rows (tokens) x words.  Fewer rows than a 256-row tile leave its
-// instructions idle: 64- and 128-row tiles take over where they cover the rows.
+// Tiles of 256, 128 and 64 rows by 256 columns.
 template <int ELEM> using Big = Config<ELEM, 0, 0, kNoScale, 4, 2, 4, 8>;
 template <int ELEM> using Mid = Config<ELEM, 0, 0, kNoScale, 2, 4, 4, 4>;
 template <int ELEM> using Low = Config<ELEM, 0, 0, kNoScale, 1, 8, 4, 2>;
 
 template <int ELEM, class F>
-hipError_t by_rows_of(int64_t n, F f) {
-    if (n <= 64) return f(Low<ELEM>{});
-    if (n <= 128) return f(Mid<ELEM>{});
+hipError_t by_rows_of(int64_t tile_rows, F f) {
+    if (tile_rows == 64) return f(Low<ELEM>{});
+    if (tile_rows == 128) return f(Mid<ELEM>{});
     return f(Big<ELEM>{});
 }
 template <class F>
-hipError_t by_rows(int64_t n, bool bf16, F f) {
-    return bf16 ? by_rows_of<kBf16>(n, f) : by_rows_of<kF16>(n, f);
+hipError_t by_rows(int64_t tile_rows, bool bf16, F f) {
+    return bf16 ? by_rows_of<kBf16>(tile_rows, f) : by_rows_of<kF16>(tile_rows, f);
 }
 
 hipError_t transpose16(const void* in, int64_t ldin, int64_t rows, int64_t cols, uint16_t* out, int64_t ldout, bool bf16,
@@ -521,7 +520,7 @@ hipError_t launch_loss(const LossJob& j, hipStream_t stream) {
     const Operand H{h, 2 * j.k, j.n, nullptr, 0, 0}, W{w, 2 * j.k, j.v, nullptr, 0, 0};
     const float c2 = kLog2e / j.tau;
     int64_t tiles = 0;
-    const hipError_t e = by_rows(j.n, j.bf16, [&](auto cfg) {
+    const hipError_t e = by_rows(loss_tile_rows(j.n, (j.v + 255) / 256), j.bf16, [&](auto cfg) {
         using C = decltype(cfg);
         const int64_t tm = (j.n + C::TL - 1) / C::TL;
         tiles = (j.v + C::TR - 1) / C::TR;
@@ -574,7 +573,7 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
         const int64_t vc = j.v - v0 < p.piece ? j.v - v0 : p.piece, ldz = (vc + 7) / 8 * 8;
         const uint8_t* wp = static_cast<const uint8_t*>(j.w) + v0 * j.k * 2;
         const Operand H{static_cast<const uint8_t*>(j.h), 2 * j.k, j.n, nullptr, 0, 0}, W{wp, 2 * j.k, vc, nullptr, 0, 0};
-        e = by_rows(j.n, j.bf16, [&](auto cfg) {
+        e = by_rows(loss_tile_rows(j.n, (vc + 255) / 256), j.bf16, [&](auto cfg) {
             using C = decltype(cfg);
             const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (vc + C::TR - 1) / C::TR;
             const TileMap map = TileMap::make(tm, tn);
@@ -587,19 +586,20 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
         if (j.dw) {
             e = transpose16(dz, ldz, j.n, vc, dzt, ldn, false, nullptr, nullptr, stream);
             if (e != hipSuccess) return e;
-            using C = Big<kF16>;
             const Operand Z{reinterpret_cast<const uint8_t*>(dzt), 2 * ldn, vc, nullptr, 0, 0};
             const Operand HT{reinterpret_cast<const uint8_t*>(ht), 2 * ldn, j.k, nullptr, 0, 0};
-            const int64_t tm = (vc + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
-            const TileMap map = TileMap::make(tn, tm);
-            const dim3 grid(map.grid);
-            if (j.bf16)
-                hipLaunchKernelGGL((k_grad_w<C, __bf16>), grid, dim3(C::NT), 0, stream, Z, HT, 2 * j.n,
-                                   static_cast<__bf16*>(j.dw) + v0 * j.k, j.k, slots, map);
-            else
-                hipLaunchKernelGGL((k_grad_w<C, _Float16>), grid, dim3(C::NT), 0, stream, Z, HT, 2 * j.n,
-                                   static_cast<_Float16*>(j.dw) + v0 * j.k, j.k, slots, map);
-            e = hipGetLastError();
+            e = by_rows_of<kF16>(loss_tile_rows(vc, (j.k + 255) / 256), [&](auto cfg) {
+                using C = decltype(cfg);
+                const int64_t tm = (vc + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
+                const TileMap map = TileMap::make(tn, tm);
+                if (j.bf16)
+                    hipLaunchKernelGGL((k_grad_w<C, __bf16>), dim3(map.grid), dim3(C::NT), 0, stream, Z, HT, 2 * j.n,
+                                       static_cast<__bf16*>(j.dw) + v0 * j.k, j.k, slots, map);
+                else
+                    hipLaunchKernelGGL((k_grad_w<C, _Float16>), dim3(map.grid), dim3(C::NT), 0, stream, Z, HT, 2 * j.n,
+                                       static_cast<_Float16*>(j.dw) + v0 * j.k, j.k, slots, map);
+                return hipGetLastError();
+            });
         }
         if (j.dh && e == hipSuccess) {
             e = transpose16(wp, j.k, vc, j.k, wt, ldz, j.bf16, slots + 1, nullptr, stream);
@@ -608,7 +608,7 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
             const Operand WT{reinterpret_cast<const uint8_t*>(wt), 2 * ldz, j.k, nullptr, 0, 0};
             // whole stages of 128 bytes a part
             const int64_t part_bytes = ((2 * vc + 127) / 128 + p.parts - 1) / p.parts * 128;
-            e = by_rows_of<kF16>(j.n, [&](auto cfg) {
+            e = by_rows_of<kF16>(p.h_rows, [&](auto cfg) {
                 using C = decltype(cfg);
                 const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
                 const TileMap map = TileMap::make(tm, tn);

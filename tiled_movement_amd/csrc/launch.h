@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "swz_common.h"
 
 namespace swz {
@@ -99,11 +101,25 @@ struct LossJob {
     void* ws;
 };
 // Workspace of the gradient: byte offsets, words of a piece of the
-// vocabulary, and the parts that dH's sum over a piece is split into.
+// vocabulary, the parts that dH's sum over a piece is split into, and the rows
+// of its tiles.
 struct LossPlan {
     int64_t slots, g, weight, dz, dzt, ht, wt, sums, bytes;
-    int64_t piece, parts;
+    int64_t piece, parts, h_rows;
 };
+// Rows of the losses' product tiles (columns: 256), for col_tiles tiles of
+// columns: the smallest of 64, 128 and 256 that covers the rows or leaves no
+// more than 256 workgroups, one a compute unit, so that all run at once.
+// Forward and gradient calls, us: 250 x 32000 x 2048 in tiles of 64 rows 55 and
+// 298, 128 (250 tiles) 44 and 268, 256 57 and 287; 1000 x 8192 x 1024: 35 and
+// 172, 27 and 156 (256 tiles), 35 and 180; 306 x 1264 x 656: 19 and 74 (25
+// tiles), 20 and 82, 27 and 98; but 509 x 32000 x 2048: 98 and 426, 77 and 370,
+// 65 and 352.
+inline int64_t loss_tile_rows(int64_t n, int64_t col_tiles) {
+    for (const int64_t t : {int64_t(64), int64_t(128)})
+        if (n <= t || (n + t - 1) / t * col_tiles <= 256) return t;
+    return 256;
+}
 hipError_t launch_loss(const LossJob& job, hipStream_t stream);
 hipError_t launch_loss_grad(const LossJob& job, const LossPlan& plan, hipStream_t stream);
 hipError_t launch_map(const int32_t* in, int32_t* out, int64_t n, swz_params p, hipStream_t stream);
