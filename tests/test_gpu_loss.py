@@ -12,7 +12,7 @@ operation, half of it where it rounds to nearest):
   of the largest upstream below the normal range);
 * H and W widened to fp16: 2^-40 of the largest where not exact;
 * gradients: fp32 sums of v (or n) products, one rounding to the result's
-  type (2^-8 bf16, 2^-11 fp16; fp16 below its normal range 2^-25).
+  type (2^-8 bf16, 2^-11 fp16; below their normal ranges 2^-134 and 2^-25).
 """
 
 import numpy as np
@@ -27,7 +27,7 @@ import tiled_movement_amd as T
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 U = 2.0 ** -23
-DT = {"bf16": (torch.bfloat16, T.X_BF16, 2.0 ** -8, 0.0), "fp16": (torch.float16, T.X_F16, 2.0 ** -11, 2.0 ** -25)}
+DT = {"bf16": (torch.bfloat16, T.X_BF16, 2.0 ** -8, 2.0 ** -134), "fp16": (torch.float16, T.X_F16, 2.0 ** -11, 2.0 ** -25)}
 
 
 def announce(*what):
@@ -246,10 +246,12 @@ def test_upstream_of_any_size(scale):
     assert torch.equal(d["dh"].double(), base * s)
 
 
-@pytest.mark.parametrize("size", [1e-4, 1e4])
-def test_operands_far_from_one(size):
-    announce("operand size", size)
+@pytest.mark.parametrize("size,upstream", [(1e-4, 1.0), (1e4, 1.0), (2.0 ** 118, 2.0 ** -60), (2.0 ** -110, 2.0 ** 10)])
+def test_operands_far_from_one(size, upstream):
+    """Also where the largest operand times the gradient's other factors would leave fp32's range on the way."""
+    announce("operand size", size, upstream)
     c = Case(60, 500, 64, seed=9)
+    c.upstream = (c.upstream * upstream).astype(np.float32)
     c.h = (c.h.double() * size).to(torch.bfloat16)
     c.w = (c.w.double() / size).to(torch.bfloat16)
     d = c.device()

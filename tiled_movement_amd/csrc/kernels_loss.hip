@@ -303,6 +303,21 @@ __global__ __launch_bounds__(64) void k_loss_prep(const int64_t* __restrict__ in
     }
 }
 
+// What a gradient's sum is multiplied by at the end: the largest upstream,
+// 2^-14, and the power of two of its widened operand.  Exponents are added
+// before they are applied, so nothing on the way leaves the range that the
+// result is in.
+struct Unscale {
+    float m;
+    int e;
+    __device__ __forceinline__ Unscale(uint32_t gmax, uint32_t operand_max) {
+        int ge;
+        m = frexpf(__uint_as_float(gmax), &ge);
+        e = ge - 14 - widen_exponent(operand_max);
+    }
+    __device__ __forceinline__ float operator()(float v) const { return ldexpf(v * m, e); }
+};
+
 // g_i tau over the largest of them, times 2^14.
 __device__ __forceinline__ float row_factor(float g, uint32_t gmax) {
     return g == 0.f ? 0.f : g / __uint_as_float(gmax) * kDzScale;
@@ -423,10 +438,10 @@ __global__ __launch_bounds__(C::NT) void k_grad_w(Operand Z, Operand H, int64_t 
     f32x4 acc[C::BL][C::BR];
     tile_product<C>(acc, Z, H, i0, j0, kbytes, lds);
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const float back = pow2f(-widen_exponent(slots[0])), gmax = __uint_as_float(slots[2]) / kDzScale;
+    const Unscale unscale(slots[2], slots[0]);
     store_tile<C>(acc, (lds_f32*)(lds + wave * C::kSlice), dw, k, i0 + wave / C::WR * C::BL * 16,
                   j0 + wave % C::WR * C::BR * 16, Z.rows, H.rows, true, lane,
-                  [=](float v) { return v * back * gmax; });
+                  unscale);
 }
 
 // dH's sum over a part of a piece's words into its own fp32 buffer (blockIdx.y).
@@ -469,10 +484,10 @@ __global__ __launch_bounds__(256) void k_finish_h(const float* __restrict__ sums
     if (u >= quads) return;
     f32x4 s = reinterpret_cast<const f32x4*>(sums)[u];
     for (int p = 1; p < parts; ++p) s += reinterpret_cast<const f32x4*>(sums)[p * quads + u];
-    const float back = pow2f(-widen_exponent(slots[1])), gmax = __uint_as_float(slots[2]) / kDzScale;
+    const Unscale unscale(slots[2], slots[1]);
     ct4 o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = static_cast<CT>(s[i] * back * gmax);
+    for (int i = 0; i < 4; ++i) o[i] = static_cast<CT>(unscale(s[i]));
     reinterpret_cast<ct4*>(dh)[u] = o;
 }
 
