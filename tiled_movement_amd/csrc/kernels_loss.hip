@@ -223,8 +223,14 @@ __global__ void k_clear_slots(uint32_t* slots) {
 // atomic maxima does not matter).  At most one atomic a workgroup, and none
 // where the slot already holds as much: with one a wave the atomics took four
 // fifths of the time (200 MB: 190 us).
-__global__ __launch_bounds__(256) void k_absmax(const uint16_t* __restrict__ x, int64_t pieces, uint32_t* slot) {
+// Grid row 0 takes H, row 1 W; a side that no gradient needs has no pieces.
+__global__ __launch_bounds__(256) void k_absmax(const uint16_t* __restrict__ h, int64_t h_pieces,
+                                                const uint16_t* __restrict__ w, int64_t w_pieces, uint32_t* slots) {
     __shared__ uint32_t part[4];
+    const uint16_t* x = blockIdx.y ? w : h;
+    const int64_t pieces = blockIdx.y ? w_pieces : h_pieces;
+    uint32_t* slot = slots + blockIdx.y;
+    if (static_cast<int64_t>(blockIdx.x) * 256 >= pieces) return;
     u16x8 m = 0;
     const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
 #pragma unroll 4
@@ -572,13 +578,10 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
     const int64_t ldn = (j.n + 7) / 8 * 8;
     hipLaunchKernelGGL(k_clear_slots, dim3(1), dim3(64), 0, stream, slots);
     if (j.bf16) {
-        auto absmax = [&](const void* x, int64_t elems, int slot) {
-            const int64_t pieces = elems / 8;
-            const unsigned grid = pieces > 1024 * 256 ? 1024u : blocks_of(pieces, 256);
-            hipLaunchKernelGGL(k_absmax, dim3(grid), dim3(256), 0, stream, static_cast<const uint16_t*>(x), pieces, slots + slot);
-        };
-        if (j.dw) absmax(j.h, j.n * j.k, 0);
-        if (j.dh) absmax(j.w, j.v * j.k, 1);
+        const int64_t hp = j.dw ? j.n * j.k / 8 : 0, wp = j.dh ? j.v * j.k / 8 : 0, most = hp > wp ? hp : wp;
+        const unsigned grid = most > 1024 * 256 ? 1024u : blocks_of(most, 256);
+        hipLaunchKernelGGL(k_absmax, dim3(grid, 2), dim3(256), 0, stream, static_cast<const uint16_t*>(j.h), hp,
+                           static_cast<const uint16_t*>(j.w), wp, slots);
     }
     hipLaunchKernelGGL(k_loss_prep, dim3(static_cast<unsigned>(j.n)), dim3(64), 0, stream, j.index, j.teacher, j.upstream, j.v,
                        j.top, j.tau, weight, g, slots + 2);
