@@ -219,6 +219,12 @@ __global__ void k_clear_slots(uint32_t* slots) {
     if (threadIdx.x < kSlots) slots[threadIdx.x] = 0;
 }
 
+// Raises a slot to a magnitude's bits if that is finite and more than it holds.
+__device__ __forceinline__ void raise_slot(uint32_t* slot, uint32_t bits) {
+    if (bits < 0x7f800000u && bits > __hip_atomic_load(slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(slot, bits);
+}
+__device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
 // Largest finite magnitude of a bf16 array, as fp32 bits (the order of
 // atomic maxima does not matter).  At most one atomic a workgroup, and none
 // where the slot already holds as much: with one a wave the atomics took four
@@ -248,7 +254,7 @@ __global__ __launch_bounds__(256) void k_absmax(const uint16_t* __restrict__ h, 
     __syncthreads();
     if (threadIdx.x == 0) {
         const uint32_t all = max(max(part[0], part[1]), max(part[2], part[3])) << 16;
-        if (all > __hip_atomic_load(slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(slot, all);
+        raise_slot(slot, all);
     }
 }
 
@@ -261,51 +267,63 @@ __device__ __forceinline__ int widen_exponent(uint32_t bits) {
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// Per row: the entries' weights with equal words joined (each holds the sum,
-// so writing it twice writes the same), and g tau, 0 for rows that do not
-// count.  One wave a row.
-__global__ __launch_bounds__(64) void k_loss_prep(const int64_t* __restrict__ index, const float* __restrict__ teacher,
-                                                  const float* __restrict__ upstream, int64_t v, int top, float tau,
-                                                  float* __restrict__ weight, float* __restrict__ g, uint32_t* slot) {
+// Cross entropy, a thread a row: the target's weight and g, 0 for rows that do
+// not count.
+__global__ __launch_bounds__(256) void k_ce_prep(const int64_t* __restrict__ index, const float* __restrict__ upstream,
+                                                 int64_t n, int64_t v, float* __restrict__ weight, float* __restrict__ g,
+                                                 uint32_t* slot) {
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    uint32_t b = 0;
+    if (row < n) {
+        const bool counts = index[row] >= 0 && index[row] < v;
+        const float gt = counts ? upstream[row] : 0.f;
+        weight[row] = counts ? 1.f : 0.f;
+        g[row] = gt;
+        b = magnitude_bits(gt);
+        b = b < 0x7f800000u ? b : 0u;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) b = max(b, static_cast<uint32_t>(__shfl_xor(static_cast<int>(b), d)));
+    if (threadIdx.x % 64 == 0) raise_slot(slot, b);
+}
+
+// Distillation, a wave a row: the entries' weights with equal words joined
+// (each holds the sum, so writing it twice writes the same), and g tau.
+__global__ __launch_bounds__(64) void k_distill_prep(const int64_t* __restrict__ index, const float* __restrict__ teacher,
+                                                     const float* __restrict__ upstream, int64_t v, int top, float tau,
+                                                     float* __restrict__ weight, float* __restrict__ g, uint32_t* slot) {
     __shared__ float p[kMaxTop];
     __shared__ int64_t words[kMaxTop];
     const int64_t row = blockIdx.x;
     const int lane = threadIdx.x;
+    float m = -__builtin_inff();
     bool any = false;
-    if (!teacher) {
-        any = index[row] >= 0 && index[row] < v;
-        if (lane == 0) weight[row] = any ? 1.f : 0.f;
-    } else {
-        float m = -__builtin_inff();
-        for (int j = lane; j < top; j += 64) {
-            const float t = teacher[row * top + j];
-            if (entry_counts(index[row * top + j], t, v)) m = fmaxf(m, t), any = true;
-        }
-        any = __any(any);
-        m = wave_max(m);
-        float s = 0.f;
-        for (int j = lane; j < top; j += 64) {
-            const float t = teacher[row * top + j];
-            const bool here = entry_counts(index[row * top + j], t, v);
-            const float e = here ? expf((t - m) / tau) : 0.f;
-            words[j] = here ? index[row * top + j] : -1;
-            p[j] = e;
-            s += e;
-        }
-        s = wave_sum(s);
-        __syncthreads();
-        for (int j = lane; j < top; j += 64) {
-            float sum = 0.f;
-            for (int i = 0; i < top; ++i) sum += words[i] == words[j] ? p[i] : 0.f;
-            weight[row * top + j] = any ? sum / s : 0.f;
-        }
+    for (int j = lane; j < top; j += 64) {
+        const float t = teacher[row * top + j];
+        if (entry_counts(index[row * top + j], t, v)) m = fmaxf(m, t), any = true;
+    }
+    any = __any(any);
+    m = wave_max(m);
+    float s = 0.f;
+    for (int j = lane; j < top; j += 64) {
+        const float t = teacher[row * top + j];
+        const bool here = entry_counts(index[row * top + j], t, v);
+        const float e = here ? expf((t - m) / tau) : 0.f;
+        words[j] = here ? index[row * top + j] : -1;
+        p[j] = e;
+        s += e;
+    }
+    s = wave_sum(s);
+    __syncthreads();
+    for (int j = lane; j < top; j += 64) {
+        float sum = 0.f;
+        for (int i = 0; i < top; ++i) sum += words[i] == words[j] ? p[i] : 0.f;
+        weight[row * top + j] = any ? sum / s : 0.f;
     }
     if (lane == 0) {
         const float gt = any ? upstream[row] * tau : 0.f;
         g[row] = gt;
-        const uint32_t b = __float_as_uint(gt) & 0x7fffffffu;
-        // (one atomic a row took most of the kernel's time; a mean's upstream is the same for all rows)
-        if (b < 0x7f800000u && b > __hip_atomic_load(slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(slot, b);
+        raise_slot(slot, magnitude_bits(gt));
     }
 }
 
@@ -583,8 +601,12 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
         hipLaunchKernelGGL(k_absmax, dim3(grid, 2), dim3(256), 0, stream, static_cast<const uint16_t*>(j.h), hp,
                            static_cast<const uint16_t*>(j.w), wp, slots);
     }
-    hipLaunchKernelGGL(k_loss_prep, dim3(static_cast<unsigned>(j.n)), dim3(64), 0, stream, j.index, j.teacher, j.upstream, j.v,
-                       j.top, j.tau, weight, g, slots + 2);
+    if (j.teacher)
+        hipLaunchKernelGGL(k_distill_prep, dim3(static_cast<unsigned>(j.n)), dim3(64), 0, stream, j.index, j.teacher, j.upstream,
+                           j.v, j.top, j.tau, weight, g, slots + 2);
+    else
+        hipLaunchKernelGGL(k_ce_prep, dim3(blocks_of(j.n, 256)), dim3(256), 0, stream, j.index, j.upstream, j.n, j.v, weight, g,
+                           slots + 2);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && j.dw) e = transpose16(j.h, j.k, j.n, j.k, ht, ldn, j.bf16, slots, g, stream);
     for (int64_t v0 = 0; v0 < j.v && e == hipSuccess; v0 += p.piece) {
