@@ -152,6 +152,19 @@ def test_loss_refusals(which):
         assert losses(which, n=0) == OK
 
 
+@pytest.mark.parametrize("big", [1 << 31, 1 << 40, 1 << 61, 1 << 62, (1 << 63) - 8])
+def test_loss_sizes_of_any_magnitude_are_refused(big):
+    """Sizes whose products with an element's bytes leave 64 bits are compared before they are multiplied."""
+    for grad in (0, 1):
+        assert workspace(1, 10, big, 1, grad)[0] == EUNSUP
+        assert workspace(big, 10, 8, 1, grad)[0] == EUNSUP
+        assert workspace(1, big, 8, 1, grad)[0] == EUNSUP
+        assert workspace(big, big, big, 256, grad)[0] == EUNSUP
+    for which in ("ce", "ce_grad", "distill", "distill_grad"):
+        for kw in (dict(n=big), dict(v=big), dict(k=big)):
+            assert losses(which, wsb=1 << 45, **kw) == EUNSUP, (which, kw)
+
+
 class FakeCuda:
     is_cuda = True
 

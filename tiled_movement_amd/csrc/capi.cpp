@@ -47,10 +47,11 @@ bool f8_operand_bytes(int64_t rows, int64_t cols, int64_t ld, bool square, int32
 }
 
 // Sizes of an output-layer loss that the kernels' grids and offsets take:
-// SWZ_OK, or why not.
+// SWZ_OK, or why not.  Each size is bounded by itself before it enters a
+// product.
 int check_loss_sizes(int64_t n, int64_t v, int64_t k, int32_t top) {
     if (n < 0 || v < 1 || k < 8 || k % 8 || top < 1) return SWZ_EINVAL;
-    if (top > swz::kMaxTop || 2 * k >= kMaxPitch || 2 * (n + 8) >= kMaxPitch || v >= int64_t(1) << 31) return SWZ_EUNSUPPORTED;
+    if (top > swz::kMaxTop || k >= kMaxPitch / 2 || n >= kMaxPitch / 2 - 8 || v >= int64_t(1) << 31) return SWZ_EUNSUPPORTED;
     if ((n / 256 + 1) * (v / 256 + 1) > int64_t(1) << 22) return SWZ_EUNSUPPORTED;  // tiles of one launch
     return SWZ_OK;
 }
