@@ -225,25 +225,42 @@ __device__ __forceinline__ void raise_slot(uint32_t* slot, uint32_t bits) {
 }
 __device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// Largest finite magnitude of a bf16 array, as fp32 bits (the order of
-// atomic maxima does not matter).  At most one atomic a workgroup, and none
-// where the slot already holds as much: with one a wave the atomics took four
-// fifths of the time (200 MB: 190 us).
+// Largest finite magnitude of bf16 arrays, as fp32 bits (the order of atomic
+// maxima does not matter).  At most one atomic a workgroup, and none where the
+// slot already holds as much: with one a wave the atomics took four fifths of
+// the time (200 MB: 190 us).
 // Grid row 0 takes H, row 1 W; a side that no gradient needs has no pieces.
-__global__ __launch_bounds__(256) void k_absmax(const uint16_t* __restrict__ h, int64_t h_pieces,
-                                                const uint16_t* __restrict__ w, int64_t w_pieces, uint32_t* slots) {
+// H's rows of factor g = 0 stay out (row_pieces: 16-byte pieces a row): they
+// may hold anything, and their largest value would push the others' digits
+// out of the widened range.
+__global__ __launch_bounds__(256) void k_absmax(const uint16_t* __restrict__ h, int64_t h_pieces, uint32_t row_pieces,
+                                                const float* __restrict__ g, const uint16_t* __restrict__ w,
+                                                int64_t w_pieces, uint32_t* slots) {
     __shared__ uint32_t part[4];
     const uint16_t* x = blockIdx.y ? w : h;
     const int64_t pieces = blockIdx.y ? w_pieces : h_pieces;
     uint32_t* slot = slots + blockIdx.y;
     if (static_cast<int64_t>(blockIdx.x) * 256 >= pieces) return;
     u16x8 m = 0;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
-#pragma unroll 4
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < pieces; i += step) {
+    const uint32_t step = gridDim.x * 256, first = blockIdx.x * 256 + threadIdx.x;
+    auto take = [&](int64_t i) {
         u16x8 a = reinterpret_cast<const u16x8*>(x)[i] & uint16_t(0x7fff);
         a = a < uint16_t(0x7f80) ? a : u16x8(0);
         m = a > m ? a : m;
+    };
+    if (blockIdx.y) {
+#pragma unroll 4
+        for (int64_t i = first; i < pieces; i += step) take(i);
+    } else {
+        // the row of a piece by steps: a division a piece would cost more than its load
+        const uint32_t rows = step / row_pieces, rest = step % row_pieces;
+        uint32_t row = first / row_pieces, at = first % row_pieces;
+        for (int64_t i = first; i < pieces; i += step) {
+            if (g[row] != 0.f) take(i);
+            row += rows;
+            at += rest;
+            if (at >= row_pieces) at -= row_pieces, ++row;
+        }
     }
     uint32_t best = 0;
 #pragma unroll
@@ -595,18 +612,18 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
     const float c2 = kLog2e / j.tau;
     const int64_t ldn = (j.n + 7) / 8 * 8;
     hipLaunchKernelGGL(k_clear_slots, dim3(1), dim3(64), 0, stream, slots);
-    if (j.bf16) {
-        const int64_t hp = j.dw ? j.n * j.k / 8 : 0, wp = j.dh ? j.v * j.k / 8 : 0, most = hp > wp ? hp : wp;
-        const unsigned grid = most > 1024 * 256 ? 1024u : blocks_of(most, 256);
-        hipLaunchKernelGGL(k_absmax, dim3(grid, 2), dim3(256), 0, stream, static_cast<const uint16_t*>(j.h), hp,
-                           static_cast<const uint16_t*>(j.w), wp, slots);
-    }
     if (j.teacher)
         hipLaunchKernelGGL(k_distill_prep, dim3(static_cast<unsigned>(j.n)), dim3(64), 0, stream, j.index, j.teacher, j.upstream,
                            j.v, j.top, j.tau, weight, g, slots + 2);
     else
         hipLaunchKernelGGL(k_ce_prep, dim3(blocks_of(j.n, 256)), dim3(256), 0, stream, j.index, j.upstream, j.n, j.v, weight, g,
                            slots + 2);
+    if (j.bf16) {
+        const int64_t hp = j.dw ? j.n * j.k / 8 : 0, wp = j.dh ? j.v * j.k / 8 : 0, most = hp > wp ? hp : wp;
+        const unsigned grid = most > 1024 * 256 ? 1024u : blocks_of(most, 256);
+        hipLaunchKernelGGL(k_absmax, dim3(grid, 2), dim3(256), 0, stream, static_cast<const uint16_t*>(j.h), hp,
+                           static_cast<uint32_t>(j.k / 8), g, static_cast<const uint16_t*>(j.w), wp, slots);
+    }
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && j.dw) e = transpose16(j.h, j.k, j.n, j.k, ht, ldn, j.bf16, slots, g, stream);
     for (int64_t v0 = 0; v0 < j.v && e == hipSuccess; v0 += p.piece) {
