@@ -537,12 +537,17 @@ int swz_linear_ce(const void* d_h, const void* d_w, int32_t x_type, const int64_
 
 /* Its gradients, for upstream[i] = d(total) / d(loss[i]) (float [n]):
  *   dz[i][v] = upstream[i] (exp(z[i][v] - lse[i]) - [v = target[i]]),
- *   dh = dz W ([n][k]), dw = dz^T H ([v][k]), both x_type, rounded once,
- * overwritten; either may be NULL.  The logits are computed again, a piece of
- * the vocabulary at a time.  dz is held in fp16 with the largest upstream
- * taken out, H and W in fp16 with a power of two; sums are fp32.  n = 0
- * writes a zero dw.  Results do not depend on the order of anything: the same
- * call gives the same bits.
+ *   dh = dz W ([n][k]), dw = dz^T H ([v][k]), both x_type, overwritten; either
+ * may be NULL.  The logits are computed again, a piece of the vocabulary at a
+ * time.  Sums are fp32 and rounded to x_type at the end; their operands are
+ * held in fp16 (half a step 2^-11): dz with its row's upstream taken out but
+ * for a factor between 1/2 and 1, so that a row of dh keeps its digits however
+ * small its upstream is beside the others' (absolutely, dz / upstream is good
+ * to 2^-38); W, and H's rows times their upstream's power of two, with a power
+ * of two that keeps values down to 2^-28 of the largest exact.  With fp16
+ * results that rounding of dz is as large as the result's own.  Rows that do
+ * not count may hold any numbers or NaN.  n = 0 writes a zero dw.  Results do
+ * not depend on the order of anything: the same call gives the same bits.
  * Errors: as swz_linear_ce. */
 int swz_linear_ce_grad(const void* d_h, const void* d_w, int32_t x_type, const int64_t* d_target, const float* d_lse,
                        const float* d_zt, const float* d_upstream, void* d_dh, void* d_dw, int64_t n, int64_t v,

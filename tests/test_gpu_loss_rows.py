@@ -1,9 +1,10 @@
 """What one row of a loss call may not do to another."""
 
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_loss import Case
+from test_gpu_loss import DT, U, Case
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -11,6 +12,55 @@ DEV = "cuda:0"
 
 def announce(*what):
     print("case:", *what, flush=True)
+
+
+def check_rows(c, d):
+    """c's losses and gradients in d against their 64-bit values with the tolerances of test_gpu_loss.py, but each row's dz
+    by its own upstream: rounding to fp16, 2^-11 of the value, below the normal range 2^-25 of what 2^14 times at least
+    half the upstream stands for, so 2^-38 of it.  Operands widened to fp16: 2^-25 where the largest is at least 2^14."""
+    t = {x: torch.as_tensor(np.asarray(getattr(c, x))).to(DEV) for x in ("index", "upstream")}
+    h, w, tau, top = c.h.to(DEV).double(), c.w.to(DEV).double(), c.tau, max(c.top, 1)
+    here = (t["index"] >= 0) & (t["index"] < c.v)
+    at = torch.where(here, t["index"], 0)
+    z = h @ w.t() / tau
+    lse = torch.logsumexp(z, dim=1)
+    entropy = torch.zeros(c.n, dtype=torch.float64, device=DEV)
+    teach = torch.zeros(c.n, dtype=torch.float64, device=DEV)
+    if c.top:
+        teacher = torch.from_numpy(c.teacher).to(DEV).double() / tau
+        here &= teacher > -np.inf
+        at = torch.where(here, t["index"], 0)
+        p = torch.softmax(teacher.masked_fill(~here, -np.inf), dim=1).nan_to_num(0.0)
+        entropy = -torch.special.entr(p).sum(dim=1)
+        teach = (6 * torch.where(here, teacher.abs(), 0.0).amax(dim=1) + top + 16) * U
+    else:
+        p = here.double()
+    counts = here.any(dim=1)
+    y = torch.zeros_like(z).scatter_add_(1, at, p * here)
+    loss = torch.where(counts, tau * tau * (entropy + lse * y.sum(dim=1) - (y * z).sum(dim=1)), 0.0)
+    ez = (c.k + 2) * U * (h.abs() @ w.abs().t()) / tau
+    size = z.abs().amax(dim=1) + lse.abs()
+    elog = ez.amax(dim=1) + 4 * U * size + 520 * U
+    assert bool(((d["lse"].double() - lse).abs() <= elog).all())
+    eloss = tau * tau * (elog + ez.amax(dim=1) + 4 * U * size + teach * (2 * size + 2 + np.log(top)))
+    assert bool(((d["loss"].double() - loss).abs() <= torch.where(counts, eloss, 0.0)).all())
+    step, tiny = DT[c.dt][2], DT[c.dt][3]
+    up = t["upstream"].double().abs() * tau * counts
+    sm = torch.exp(z - lse[:, None])
+    off = (sm - y).abs()
+    edz = 2.0 ** -11 * off + (1 + 2.0 ** -11) * (((elog + 4 * U * size)[:, None] + ez + 8 * U) * sm + teach[:, None] * y + 4 * U * off)
+    edz = (edz + 2.0 ** -38) * counts[:, None]  # of a row's own upstream
+    dz = (sm - y) * (t["upstream"].double() * tau * counts)[:, None]
+    wide_w = 2.0 ** -39 * w.abs().max() if c.dt == "bf16" else 0.0
+    wide_h = 2.0 ** -39 * (h.abs().amax(dim=1) * counts).max()
+    results = {"dh": (dz @ w, (up[:, None] * edz) @ w.abs() + (up[:, None] * (off + edz)) @ (wide_w + (c.v + 24) * U * w.abs())),
+               "dw": (dz.t() @ h, (up[:, None] * edz).t() @ h.abs() + (up[:, None] * (off + edz)).t() @ ((c.n + 24) * U * h.abs())
+                      + (up.max() * (off + edz) * counts[:, None]).sum(dim=0)[:, None] * wide_h)}
+    for name, (ref, bound) in results.items():
+        bound = bound + step * (ref.abs() + bound) + tiny
+        err = (d[name].double() - ref).abs()
+        assert bool((err <= bound).all()), (name, float((err / bound.clamp(min=1e-300)).max()))
+    assert bool((d["dh"][~counts] == 0).all())
 
 
 @pytest.mark.parametrize("top", [0, 5])
@@ -30,3 +80,22 @@ def test_values_of_rows_that_do_not_count_change_nothing(dt, top):
         got = {x: d[x].clone() for x in ("loss", "dh", "dw")}
         want = want or got
         assert all(torch.equal(got[x], want[x]) for x in want), [x for x in want if not torch.equal(got[x], want[x])]
+
+
+@pytest.mark.parametrize("dt,decades", [("bf16", 60), ("bf16", 20), ("fp16", 20)])
+@pytest.mark.parametrize("top,tau", [(0, 1.0), (6, 0.6)])
+@pytest.mark.parametrize("n,v,k", [(41, 3000, 64), (200, 5000, 136)])
+def test_upstreams_far_apart(n, v, k, top, tau, dt, decades):
+    """Weights of the rows from 2^0 down to 2^-decades in one call: every row of dH keeps its own digits."""
+    announce("upstreams", n, v, k, top, dt, decades)
+    c = Case(n, v, k, dt, top=top, tau=tau, seed=22, absent=0.1)
+    rng = np.random.default_rng(23)
+    c.w = (c.w.double() + 0.3).to(c.w.dtype)  # softmax part and target part of a row of dH do not cancel
+    c.upstream = (rng.choice([-1.0, 1.0], n) * rng.uniform(1, 2, n) * 2.0 ** -np.linspace(0, decades, n)).astype(np.float32)
+    if dt == "fp16":
+        c.upstream *= 2.0 ** 10  # results of the smallest rows stay normal numbers
+    d = c.device()
+    c.forward(d)
+    c.backward(d)
+    torch.cuda.synchronize()
+    check_rows(c, d)

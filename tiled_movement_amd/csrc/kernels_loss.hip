@@ -22,11 +22,15 @@
 //
 // Rounding: dz is held in fp16 (2^-11), not bf16 (2^-8), because the result
 // is rounded to its own type once more and a bf16 dz would add an error of
-// the same size.  Taken out of it first are max_i |g_i tau| (a mean's 1/n has
-// no rounding left then) and a factor of 2^14, which puts probabilities down
-// to 2^-28 in the normal range.  bf16 H and W are widened to fp16 by a power
-// of two that puts their largest value just below 2^15: exact for all values
-// down to 2^-29 of the largest, and off by at most 2^-40 of it below that.
+// the same size.  A row's g_i tau is split into f_i 2^s_i max_j |g_j tau| with
+// 1/2 < |f_i| <= 1: f_i enters dz (1 where all rows weigh the same, so a mean's
+// 1/n leaves no rounding), 2^s_i is exact and enters behind it, in dH at the
+// end and in dW with H's row.  So every row of dz has all of fp16's range,
+// however little the row weighs, and a factor of 2^14 puts probabilities down
+// to 2^-27 in its normal part.  H (its rows times 2^s_i) and bf16 W are widened
+// to fp16 by a power of two that puts their largest value into [2^14, 2^15):
+// exact for all values down to 2^-28 of the largest, and off by at most 2^-39
+// of it below that.
 #include "launch.h"
 #include "mma_core.h"
 
@@ -225,14 +229,31 @@ __device__ __forceinline__ void raise_slot(uint32_t* slot, uint32_t bits) {
 }
 __device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// Largest finite magnitude of bf16 arrays, as fp32 bits (the order of atomic
-// maxima does not matter).  At most one atomic a workgroup, and none where the
-// slot already holds as much: with one a wave the atomics took four fifths of
-// the time (200 MB: 190 us).
+// g_i tau as f 2^s times the largest of them (its bits), 1/2 < |f| <= 1 and
+// s <= 0.  0, and what is not finite, is its own f.
+struct RowScale {
+    float f;
+    int s;
+    __device__ __forceinline__ RowScale(float g, uint32_t gmax) : f(g), s(0) {
+        if (g == 0.f || magnitude_bits(g) >= 0x7f800000u) return;
+        int eg, em;
+        float mg = frexpf(g, &eg);
+        const float mm = frexpf(__uint_as_float(gmax), &em);
+        s = eg - em;
+        if (fabsf(mg) > mm) mg *= 0.5f, ++s;
+        f = mg / mm;
+    }
+};
+
+// Largest finite magnitudes, as fp32 bits (the order of atomic maxima does not
+// matter): of H's rows times their 2^s_i, and of a bf16 W.  At most one atomic
+// a workgroup, and none where the slot already holds as much: with one a wave
+// the atomics took four fifths of the time (200 MB: 190 us).
 // Grid row 0 takes H, row 1 W; a side that no gradient needs has no pieces.
 // H's rows of factor g = 0 stay out (row_pieces: 16-byte pieces a row): they
 // may hold anything, and their largest value would push the others' digits
 // out of the widened range.
+template <bool BF16>
 __global__ __launch_bounds__(256) void k_absmax(const uint16_t* __restrict__ h, int64_t h_pieces, uint32_t row_pieces,
                                                 const float* __restrict__ g, const uint16_t* __restrict__ w,
                                                 int64_t w_pieces, uint32_t* slots) {
@@ -241,38 +262,44 @@ __global__ __launch_bounds__(256) void k_absmax(const uint16_t* __restrict__ h, 
     const int64_t pieces = blockIdx.y ? w_pieces : h_pieces;
     uint32_t* slot = slots + blockIdx.y;
     if (static_cast<int64_t>(blockIdx.x) * 256 >= pieces) return;
-    u16x8 m = 0;
     const uint32_t step = gridDim.x * 256, first = blockIdx.x * 256 + threadIdx.x;
-    auto take = [&](int64_t i) {
-        u16x8 a = reinterpret_cast<const u16x8*>(x)[i] & uint16_t(0x7fff);
-        a = a < uint16_t(0x7f80) ? a : u16x8(0);
-        m = a > m ? a : m;
+    auto magnitudes = [&](int64_t i) {
+        const u16x8 a = reinterpret_cast<const u16x8*>(x)[i] & uint16_t(0x7fff);
+        return a < uint16_t(BF16 ? 0x7f80 : 0x7c00) ? a : u16x8(0);
     };
+    auto largest = [](u16x8 m) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) best = max(best, static_cast<uint32_t>(m[e]));
+        return half_bits_to_f32(static_cast<uint16_t>(best), BF16);
+    };
+    uint32_t best = 0;
     if (blockIdx.y) {
+        u16x8 m = 0;
 #pragma unroll 4
-        for (int64_t i = first; i < pieces; i += step) take(i);
+        for (int64_t i = first; i < pieces; i += step) {
+            const u16x8 a = magnitudes(i);
+            m = a > m ? a : m;
+        }
+        best = __float_as_uint(largest(m));
     } else {
         // the row of a piece by steps: a division a piece would cost more than its load
-        const uint32_t rows = step / row_pieces, rest = step % row_pieces;
+        const uint32_t rows = step / row_pieces, rest = step % row_pieces, gmax = slots[2];
         uint32_t row = first / row_pieces, at = first % row_pieces;
+#pragma unroll 4
         for (int64_t i = first; i < pieces; i += step) {
-            if (g[row] != 0.f) take(i);
+            const float gr = g[row];
+            if (gr != 0.f) best = max(best, __float_as_uint(ldexpf(largest(magnitudes(i)), RowScale(gr, gmax).s)));
             row += rows;
             at += rest;
             if (at >= row_pieces) at -= row_pieces, ++row;
         }
     }
-    uint32_t best = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) best = max(best, static_cast<uint32_t>(m[e]));
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) best = max(best, static_cast<uint32_t>(__shfl_xor(static_cast<int>(best), d)));
     if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = best;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        const uint32_t all = max(max(part[0], part[1]), max(part[2], part[3])) << 16;
-        raise_slot(slot, all);
-    }
+    if (threadIdx.x == 0) raise_slot(slot, max(max(part[0], part[1]), max(part[2], part[3])));
 }
 
 // The power of two that takes a largest magnitude (bits) just below 2^15, as
@@ -282,7 +309,6 @@ __device__ __forceinline__ int widen_exponent(uint32_t bits) {
     const int e = 14 - (static_cast<int>(bits >> 23) - 127);  // subnormals: bits >> 23 == 0
     return e < -113 ? -113 : e > 126 ? 126 : e;
 }
-__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // Cross entropy, a thread a row: the target's weight and g, 0 for rows that do
 // not count.
@@ -345,39 +371,34 @@ __global__ __launch_bounds__(64) void k_distill_prep(const int64_t* __restrict__
 }
 
 // What a gradient's sum is multiplied by at the end: the largest upstream,
-// 2^-14, and the power of two of its widened operand.  Exponents are added
-// before they are applied, so nothing on the way leaves the range that the
-// result is in.
+// 2^-14, the power of two of its widened operand, and of dH's row (s).
+// Exponents are added before they are applied, so nothing on the way leaves
+// the range that the result is in.
 struct Unscale {
     float m;
     int e;
-    __device__ __forceinline__ Unscale(uint32_t gmax, uint32_t operand_max) {
+    __device__ __forceinline__ Unscale(uint32_t gmax, uint32_t operand_max, int s = 0) {
         int ge;
         m = frexpf(__uint_as_float(gmax), &ge);
-        e = ge - 14 - widen_exponent(operand_max);
+        e = ge - 14 - widen_exponent(operand_max) + s;
     }
     __device__ __forceinline__ float operator()(float v) const { return ldexpf(v * m, e); }
 };
 
-// g_i tau over the largest of them, times 2^14.
-__device__ __forceinline__ float row_factor(float g, uint32_t gmax) {
-    return g == 0.f ? 0.f : g / __uint_as_float(gmax) * kDzScale;
-}
-
 // A 128 x 128 tile of 2-byte values transposed through LDS: in [rows][ldin]
-// to fp16 [cols][ldout], times the power of two of `slot` (bf16 input) or as
-// they are (fp16).  Thread (i, h) takes the 8 x 8 block of columns 8i and rows
+// to fp16 [cols][ldout], WIDEN: times the power of two of `slot` and, where g is
+// given, 2^s of the row; else as they are.  Thread (i, h) takes the 8 x 8 block of columns 8i and rows
 // 8h, so each of its columns is one 16-byte piece of an output row; piece h
 // of output row c sits at slot h ^ (c / 8) of the row's 16 (Swizzle<4,0,7> on
 // slots), which spreads the 16 rows that 16 lanes write over all 64 banks.
 // Rows whose factor g is 0 become zeros: they may hold anything, and their
 // zeros in dz would not cancel a NaN.  ldin, ldout: elements, multiples of 8; pieces behind `rows` are written into
 // the output's padding (at most 7 elements, inside ldout).
-template <bool BF16>
+template <bool BF16, bool WIDEN>
 __global__ __launch_bounds__(256) void k_transpose16(const uint16_t* __restrict__ in, int64_t ldin, int64_t rows,
                                                      int64_t cols, uint16_t* __restrict__ out, int64_t ldout,
                                                      int64_t tiles_c, const uint32_t* __restrict__ slot,
-                                                     const float* __restrict__ g) {
+                                                     const float* __restrict__ g, const uint32_t* __restrict__ gmax) {
     __shared__ u16x8 tile[128 * 16];
     const int t = threadIdx.x, i = t % 16, h = t / 16;
     const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
@@ -389,13 +410,16 @@ __global__ __launch_bounds__(256) void k_transpose16(const uint16_t* __restrict_
         v[p] = r < rows && c < cols && (!g || g[r] != 0.f) ? *reinterpret_cast<const u16x8*>(in + r * ldin + c)
                                                            : u16x8{0, 0, 0, 0, 0, 0, 0, 0};
     }
-    if constexpr (BF16) {
-        const float f = pow2f(widen_exponent(*slot));
+    if constexpr (WIDEN) {
+        const int widen = widen_exponent(*slot);
 #pragma unroll
-        for (int p = 0; p < 8; ++p)
+        for (int p = 0; p < 8; ++p) {
+            const int64_t r = r0 + 8 * h + p;
+            const int x = widen + (g && r < rows ? RowScale(g[r], *gmax).s : 0);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                v[p][e] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(half_bits_to_f32(v[p][e], true) * f));
+                v[p][e] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(ldexpf(half_bits_to_f32(v[p][e], BF16), x)));
+        }
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -434,7 +458,7 @@ __global__ __launch_bounds__(C::NT) void k_dz(Operand H, Operand W, int64_t kbyt
     for (int x = 0; x < C::BL; ++x) {
         int64_t row = i0 + (wl * C::BL + x) * 16 + l16;
         row = row < H.rows ? row : H.rows - 1;
-        const float f = row_factor(g[row], gmax), l2 = lse[row] * kLog2e;
+        const float f = RowScale(g[row], gmax).f * kDzScale, l2 = lse[row] * kLog2e;
 #pragma unroll
         for (int y = 0; y < C::BR; ++y)
 #pragma unroll
@@ -462,7 +486,7 @@ __global__ __launch_bounds__(256) void k_dz_targets(const int64_t* __restrict__ 
     if (u >= n * top) return;
     const int64_t row = u / top, word = index[u];
     if (!entry_counts(word, teacher ? teacher[u] : 0.f, v) || word < v0 || word >= v0 + vc) return;
-    const float f = row_factor(g[row], slots[2]);
+    const float f = RowScale(g[row], slots[2]).f * kDzScale;
     const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(zt[u], c2, -lse[row] * kLog2e));
     dz[row * ldz + word - v0] = static_cast<_Float16>(f == 0.f ? 0.f : (p - weight[u]) * f);
 }
@@ -517,15 +541,20 @@ __global__ __launch_bounds__(C::NT) void k_grad_h(Operand Z, Operand W, int64_t 
         }
 }
 
+// dH from its parts.  A workgroup has 256 / quads rows of `quads` pieces of four
+// (at least one), or 256 pieces of one (blockIdx.y).
 template <class CT>
-__global__ __launch_bounds__(256) void k_finish_h(const float* __restrict__ sums, int parts, int64_t quads,
-                                                  const uint32_t* __restrict__ slots, CT* __restrict__ dh) {
+__global__ __launch_bounds__(256) void k_finish_h(const float* __restrict__ sums, int parts, int64_t n, uint32_t quads,
+                                                  const float* __restrict__ g, const uint32_t* __restrict__ slots,
+                                                  CT* __restrict__ dh) {
     typedef CT ct4 __attribute__((ext_vector_type(4)));
-    const int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (u >= quads) return;
+    const uint32_t t = threadIdx.x, rows = quads < 256 ? 256 / quads : 1, r = rows > 1 ? t / quads : 0;
+    const uint32_t q = rows > 1 ? t - r * quads : blockIdx.y * 256 + t;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * rows + r, u = row * quads + q;
+    if (r >= rows || q >= quads || row >= n) return;
     f32x4 s = reinterpret_cast<const f32x4*>(sums)[u];
-    for (int p = 1; p < parts; ++p) s += reinterpret_cast<const f32x4*>(sums)[p * quads + u];
-    const Unscale unscale(slots[2], slots[1]);
+    for (int p = 1; p < parts; ++p) s += reinterpret_cast<const f32x4*>(sums)[p * n * quads + u];
+    const Unscale unscale(slots[2], slots[1], RowScale(g[row], slots[2]).s);
     ct4 o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = static_cast<CT>(unscale(s[i]));
@@ -555,15 +584,13 @@ hipError_t by_rows(int64_t tile_rows, bool bf16, F f) {
     return bf16 ? by_rows_of<kBf16>(tile_rows, f) : by_rows_of<kF16>(tile_rows, f);
 }
 
+// slot: widened; g and gmax: rows times their 2^s.
 hipError_t transpose16(const void* in, int64_t ldin, int64_t rows, int64_t cols, uint16_t* out, int64_t ldout, bool bf16,
-                       const uint32_t* slot, const float* g, hipStream_t stream) {
+                       const uint32_t* slot, const float* g, const uint32_t* gmax, hipStream_t stream) {
     const int64_t tc = (cols + 127) / 128, tr = (rows + 127) / 128;
-    const dim3 grid(static_cast<unsigned>(tc * tr));
-    const auto* x = static_cast<const uint16_t*>(in);
-    if (bf16)
-        hipLaunchKernelGGL(k_transpose16<true>, grid, dim3(256), 0, stream, x, ldin, rows, cols, out, ldout, tc, slot, g);
-    else
-        hipLaunchKernelGGL(k_transpose16<false>, grid, dim3(256), 0, stream, x, ldin, rows, cols, out, ldout, tc, slot, g);
+    const auto kernel = bf16 ? k_transpose16<true, true> : slot ? k_transpose16<false, true> : k_transpose16<false, false>;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tc * tr)), dim3(256), 0, stream, static_cast<const uint16_t*>(in), ldin,
+                       rows, cols, out, ldout, tc, slot, g, gmax);
     return hipGetLastError();
 }
 
@@ -618,14 +645,14 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
     else
         hipLaunchKernelGGL(k_ce_prep, dim3(blocks_of(j.n, 256)), dim3(256), 0, stream, j.index, j.upstream, j.n, j.v, weight, g,
                            slots + 2);
-    if (j.bf16) {
-        const int64_t hp = j.dw ? j.n * j.k / 8 : 0, wp = j.dh ? j.v * j.k / 8 : 0, most = hp > wp ? hp : wp;
-        const unsigned grid = most > 1024 * 256 ? 1024u : blocks_of(most, 256);
-        hipLaunchKernelGGL(k_absmax, dim3(grid, 2), dim3(256), 0, stream, static_cast<const uint16_t*>(j.h), hp,
-                           static_cast<uint32_t>(j.k / 8), g, static_cast<const uint16_t*>(j.w), wp, slots);
+    const int64_t hp = j.dw ? j.n * j.k / 8 : 0, wp = j.dh && j.bf16 ? j.v * j.k / 8 : 0, most = hp > wp ? hp : wp;
+    if (most) {
+        const dim3 grid(most > 1024 * 256 ? 1024u : blocks_of(most, 256), wp ? 2 : 1);
+        hipLaunchKernelGGL(j.bf16 ? k_absmax<true> : k_absmax<false>, grid, dim3(256), 0, stream, static_cast<const uint16_t*>(j.h),
+                           hp, static_cast<uint32_t>(j.k / 8), g, static_cast<const uint16_t*>(j.w), wp, slots);
     }
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && j.dw) e = transpose16(j.h, j.k, j.n, j.k, ht, ldn, j.bf16, slots, g, stream);
+    if (e == hipSuccess && j.dw) e = transpose16(j.h, j.k, j.n, j.k, ht, ldn, j.bf16, slots, g, slots + 2, stream);
     for (int64_t v0 = 0; v0 < j.v && e == hipSuccess; v0 += p.piece) {
         const int64_t vc = j.v - v0 < p.piece ? j.v - v0 : p.piece, ldz = (vc + 7) / 8 * 8;
         const uint8_t* wp = static_cast<const uint8_t*>(j.w) + v0 * j.k * 2;
@@ -641,7 +668,7 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
         hipLaunchKernelGGL(k_dz_targets, dim3(blocks_of(j.n * j.top, 256)), dim3(256), 0, stream, j.index, weight, j.zt, j.lse, g,
                            slots, j.n, j.top, c2, v0, vc, j.v, j.teacher, dz, ldz);
         if (j.dw) {
-            e = transpose16(dz, ldz, j.n, vc, dzt, ldn, false, nullptr, nullptr, stream);
+            e = transpose16(dz, ldz, j.n, vc, dzt, ldn, false, nullptr, nullptr, nullptr, stream);
             if (e != hipSuccess) return e;
             const Operand Z{reinterpret_cast<const uint8_t*>(dzt), 2 * ldn, vc, nullptr, 0, 0};
             const Operand HT{reinterpret_cast<const uint8_t*>(ht), 2 * ldn, j.k, nullptr, 0, 0};
@@ -659,7 +686,7 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
             });
         }
         if (j.dh && e == hipSuccess) {
-            e = transpose16(wp, j.k, vc, j.k, wt, ldz, j.bf16, slots + 1, nullptr, stream);
+            e = transpose16(wp, j.k, vc, j.k, wt, ldz, j.bf16, j.bf16 ? slots + 1 : nullptr, nullptr, nullptr, stream);
             if (e != hipSuccess) return e;
             const Operand Z{reinterpret_cast<const uint8_t*>(dz), 2 * ldz, j.n, nullptr, 0, 0};
             const Operand WT{reinterpret_cast<const uint8_t*>(wt), 2 * ldz, j.k, nullptr, 0, 0};
@@ -676,13 +703,13 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
         }
     }
     if (e == hipSuccess && j.dh) {
-        const int64_t quads = j.n * j.k / 4;
-        const dim3 grid(blocks_of(quads, 256));
+        const uint32_t quads = static_cast<uint32_t>(j.k / 4), rows = quads < 256 ? 256 / quads : 1;
+        const dim3 grid(blocks_of(j.n, rows), (quads + 255) / 256);
         if (j.bf16)
-            hipLaunchKernelGGL(k_finish_h<__bf16>, grid, dim3(256), 0, stream, sums, static_cast<int>(p.parts), quads, slots,
+            hipLaunchKernelGGL(k_finish_h<__bf16>, grid, dim3(256), 0, stream, sums, static_cast<int>(p.parts), j.n, quads, g, slots,
                                static_cast<__bf16*>(j.dh));
         else
-            hipLaunchKernelGGL(k_finish_h<_Float16>, grid, dim3(256), 0, stream, sums, static_cast<int>(p.parts), quads, slots,
+            hipLaunchKernelGGL(k_finish_h<_Float16>, grid, dim3(256), 0, stream, sums, static_cast<int>(p.parts), j.n, quads, g, slots,
                                static_cast<_Float16*>(j.dh));
         e = hipGetLastError();
     }
