@@ -525,8 +525,9 @@ int swz_linear_loss_workspace(int64_t n, int64_t v, int64_t k, int32_t top, int3
  *              not count: its loss is 0 and it adds nothing to the gradients.
  *   d_loss, d_lse, d_zt : float [n]; zt is the logit at the target (0 for rows
  *              that do not count).  lse and zt are what the gradient call takes.
- * Products are exact in fp32 and summed in fp32.  A row with a logit that is
- * NaN or +infinity has a NaN lse.
+ * Products are exact in fp32 and summed in fp32; lse is never below zt, so a
+ * loss is never negative.  A row with a logit that is NaN or +infinity has a
+ * NaN lse.
  * Nothing written may overlap anything else.  n = 0 does nothing.
  * Errors: SWZ_EINVAL (sizes, alignment, NULL, overlap, x_type, a workspace
  * below swz_linear_loss_workspace), SWZ_EUNSUPPORTED (n or k of 2^22 and more,

@@ -1,4 +1,4 @@
-"""What one row of a loss call may not do to another."""
+"""What one row of a loss call may not do to another, and what a row's loss owes to its own logits."""
 
 import numpy as np
 import pytest
@@ -99,3 +99,48 @@ def test_upstreams_far_apart(n, v, k, top, tau, dt, decades):
     c.backward(d)
     torch.cuda.synchronize()
     check_rows(c, d)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("top,tau,z", [(0, 1.0, 90.0), (1, 1.0, 90.0), (1, 2.0, 180.0), (1, 0.7, 63.0)])
+@pytest.mark.parametrize("n,v,k", [(40, 600, 256), (300, 16500, 128), (600, 33000, 128), (33, 700, 1000)])
+def test_certain_rows_have_no_loss(n, v, k, top, tau, z, dt):
+    """The target's logit over tau is 90 and the others' are below 45 (asserted): their exponentials vanish beside one in
+    fp32, so lse is the target's own logit over tau, the loss zero and no gradient left; nothing is negative."""
+    announce("certain rows", n, v, k, top, tau, dt)
+    c = Case(n, v, k, dt, top=top, tau=tau, seed=24, absent=0.0, scale=0.1)
+    c.index[:, 0] = np.random.default_rng(25).permutation(v)[:n]
+    h = c.h.double()
+    w = c.w.double()
+    w[torch.from_numpy(c.index[:, 0])] = z * h / (h * h).sum(dim=1, keepdim=True)
+    c.w = w.to(c.w.dtype)
+    c.upstream = np.ones(n, np.float32)
+    zz = c.h.to(DEV).double() @ c.w.to(DEV).double().t() / tau
+    at = torch.from_numpy(c.index).to(DEV)
+    others = zz.scatter(1, at, -np.inf)
+    assert float(zz.gather(1, at).min()) > 88 and float(others.max()) < 45
+    d = c.device()
+    c.forward(d)
+    c.backward(d)
+    torch.cuda.synchronize()
+    for x in ("loss", "dh", "dw"):
+        assert bool((d[x] == 0).all()), (x, float(d[x].double().abs().max()))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("n,v,k", [(70, 900, 72), (300, 16500, 200), (600, 33000, 136), (5, 300, 4104)])
+def test_listed_logits_are_the_same_number_in_both_losses(n, v, k, dt):
+    """A logit is one number, whichever call reports it: cross entropy's at the target and distillation's at an entry."""
+    announce("logits", n, v, k, dt)
+    c = Case(n, v, k, dt, top=19, seed=26, absent=0.0)
+    c.teacher = np.random.default_rng(27).standard_normal(c.teacher.shape).astype(np.float32)
+    d = c.device()
+    c.forward(d)
+    for j in (0, 7, 18):
+        e = Case(1, 1, 8, dt)
+        e.n, e.v, e.k, e.h, e.w, e.index, e.upstream = n, v, k, c.h, c.w, c.index[:, j:j + 1].copy(), c.upstream
+        f = e.device()
+        e.forward(f)
+        torch.cuda.synchronize()
+        assert torch.equal(f["zt"][:, 0], d["zt"][:, j])
+        assert torch.equal(f["lse"], d["lse"])

@@ -73,7 +73,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_gemm_f8_few(Operand A, Operand 
             f32x4 p = E8M0 ? acc : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                p = mfma_bf16_pair(widen<RT == 1>(vb[u][j], E8M0 ? fb[u] : 1.f), widen<LT == 1>(va[u][j], E8M0 ? fa[u] : 1.f), p);
+                p = mfma_pair<kBf16>(widen<RT == 1>(vb[u][j], E8M0 ? fb[u] : 1.f), widen<LT == 1>(va[u][j], E8M0 ? fa[u] : 1.f), p);
             if constexpr (E8M0) {
                 acc = p;
             } else {  // the scales of the four rows of B in this lane's registers are other lanes'

@@ -12,8 +12,14 @@
 //
 // Forward: the logits of a 256 x 256 tile stay in accumulators, and a tile
 // leaves only each row's maximum and sum of exponentials (8 bytes per row and
-// 256 words); a second kernel joins them.  The few logits at listed words are
-// dot products of their own.  Bound by the bf16 / fp16 matrix rate.
+// 256 words); a second kernel joins them.  Bound by the bf16 / fp16 matrix rate.
+// A logit is one number wherever it enters: a tile writes cross entropy's at
+// the target, and distillation's at listed words are made by the same
+// instructions in the same order; and lse is the largest logit over tau plus a
+// logarithm of at least one.  So lse is never below a listed logit, cross
+// entropy's loss and the target's p - 1 have their signs, and a row that is
+// certain of its target has no loss and no gradient (with a sum of its own for
+// the target's logit: losses of +-2e-5 at logits of 90).
 //
 // Backward, a piece of the vocabulary at a time: the piece's logits again, dz
 // from them and the saved lse, then both gradient products.  Their operands
@@ -39,7 +45,7 @@ namespace {
 
 using namespace mma;
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kDzScale = 16384.f;
 constexpr int kSlots = 3;  // maxima, as bits: 0 |H|, 1 |W|, 2 |g tau|
 
@@ -51,11 +57,13 @@ __device__ __forceinline__ float half_bits_to_f32(uint16_t b, bool bf16) {
 }
 
 // ------------------------------------------------------------------ forward
-// Rows [i0, i0 + TL) against words [j0, j0 + TR): part[tile][row] = (maximum,
-// sum of 2^(t - maximum)) of t = z log2(e) / tau.
+// Rows [i0, i0 + TL) against words [j0, j0 + TR): part[tile][row] = (largest
+// logit m, sum of 2^((z - m) c2)), c2 = log2(e) / tau.  Cross entropy (index
+// given): zt of the rows whose target is in the tile.
 template <class C>
 __global__ __launch_bounds__(C::NT) void k_logit_stats(Operand H, Operand W, int64_t kbytes, float c2,
-                                                       float2* __restrict__ part, TileMap map) {
+                                                       float2* __restrict__ part, const int64_t* __restrict__ index,
+                                                       float* __restrict__ zt, TileMap map) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
     int64_t tm, tn;
@@ -70,15 +78,24 @@ __global__ __launch_bounds__(C::NT) void k_logit_stats(Operand H, Operand W, int
     const int64_t jw = j0 + wr * C::BR * 16 + 4 * g;
 #pragma unroll
     for (int x = 0; x < C::BL; ++x) {
+        if (index) {
+            const int64_t row = i0 + (wl * C::BL + x) * 16 + l16, word = row < H.rows ? index[row] : -1, at = word - jw;
+            const bool here = word < W.rows && at >= 0 && at < 16 * C::BR && at % 16 < 4;
+            if (__any(here)) {
+#pragma unroll
+                for (int y = 0; y < C::BR; ++y)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (here && at == 16 * y + i) zt[row] = acc[x][y][i];
+            }
+        }
         float m = -__builtin_inff();
 #pragma unroll
         for (int y = 0; y < C::BR; ++y)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float v = acc[x][y][i] * c2;
-                if (!whole && jw + 16 * y + i >= W.rows) v = -__builtin_inff();
-                acc[x][y][i] = v;
-                m = fmaxf(m, v);
+                if (!whole && jw + 16 * y + i >= W.rows) acc[x][y][i] = -__builtin_inff();
+                m = fmaxf(m, acc[x][y][i]);
             }
         m = fmaxf(m, __shfl_xor(m, 16));
         m = fmaxf(m, __shfl_xor(m, 32));
@@ -87,7 +104,7 @@ __global__ __launch_bounds__(C::NT) void k_logit_stats(Operand H, Operand W, int
 #pragma unroll
         for (int y = 0; y < C::BR; ++y)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s += __builtin_amdgcn_exp2f(acc[x][y][i] - mm);
+            for (int i = 0; i < 4; ++i) s += __builtin_amdgcn_exp2f((acc[x][y][i] - mm) * c2);
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
         if (g == 0) {
@@ -104,14 +121,17 @@ __global__ __launch_bounds__(C::NT) void k_logit_stats(Operand H, Operand W, int
         const float mm = m == -__builtin_inff() ? 0.f : m;
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < C::WR; ++w) s += red[(C::WR + w) * C::TL + r] * __builtin_amdgcn_exp2f(red[w * C::TL + r] - mm);
+        for (int w = 0; w < C::WR; ++w)
+            s += red[(C::WR + w) * C::TL + r] * __builtin_amdgcn_exp2f((red[w * C::TL + r] - mm) * c2);
         part[tn * H.rows + i0 + r] = make_float2(m, s);
     }
 }
 
-// lse from the pieces: 32 rows a workgroup, eight threads a row.
-__global__ __launch_bounds__(256) void k_join_stats(const float2* __restrict__ part, int64_t tiles, int64_t n,
-                                                    float* __restrict__ lse) {
+// lse from the pieces: 32 rows a workgroup, eight threads a row; and cross
+// entropy's loss (index given), with zt of the rows that do not count.
+__global__ __launch_bounds__(256) void k_join_stats(const float2* __restrict__ part, int64_t tiles, int64_t n, float c2,
+                                                    float tau, float* __restrict__ lse, const int64_t* __restrict__ index,
+                                                    int64_t v, float* __restrict__ zt, float* __restrict__ loss) {
     __shared__ float2 red[8][32];
     const int r = threadIdx.x % 32, sub = threadIdx.x / 32;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + r;
@@ -122,7 +142,7 @@ __global__ __launch_bounds__(256) void k_join_stats(const float2* __restrict__ p
             const float2 p = part[i * n + row];
             const float big = fmaxf(m, p.x);
             const float b = big == -__builtin_inff() ? 0.f : big;
-            s = s * __builtin_amdgcn_exp2f(m - b) + p.y * __builtin_amdgcn_exp2f(p.x - b);
+            s = s * __builtin_amdgcn_exp2f((m - b) * c2) + p.y * __builtin_amdgcn_exp2f((p.x - b) * c2);
             m = big;
         }
     }
@@ -132,8 +152,14 @@ __global__ __launch_bounds__(256) void k_join_stats(const float2* __restrict__ p
         for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i][r].x);
         const float b = m == -__builtin_inff() ? 0.f : m;
         float total = 0.f;
-        for (int i = 0; i < 8; ++i) total += red[i][r].y * __builtin_amdgcn_exp2f(red[i][r].x - b);
-        lse[row] = m * kLn2 + logf(total);
+        for (int i = 0; i < 8; ++i) total += red[i][r].y * __builtin_amdgcn_exp2f((red[i][r].x - b) * c2);
+        const float l = m / tau + logf(total);
+        lse[row] = l;
+        if (index) {
+            const bool counts = index[row] >= 0 && index[row] < v;
+            if (!counts) zt[row] = 0.f;
+            loss[row] = counts ? l - zt[row] : 0.f;
+        }
     }
 }
 
@@ -154,66 +180,91 @@ __device__ __forceinline__ bool entry_counts(int64_t word, float teacher, int64_
     return word >= 0 && word < v && teacher != -__builtin_inff();
 }
 
-// One workgroup a row: the logits at its listed words, then its loss.
-__global__ __launch_bounds__(256) void k_target_loss(const uint16_t* __restrict__ h, const uint16_t* __restrict__ w,
+// Distillation, one workgroup a row: the logits at its listed words, then its
+// loss.  A wave makes 16 logits with the instructions and the order of k of
+// tile_product, so they are its numbers: the words' rows feed the
+// instruction's rows, H's row all of its columns.  k is a multiple of 8, so
+// 16-byte chunks are inside or outside as a whole.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_listed_loss(const uint16_t* __restrict__ h, const uint16_t* __restrict__ w,
                                                      const int64_t* __restrict__ index,
                                                      const float* __restrict__ teacher, int64_t v, int64_t k, int top,
-                                                     float tau, int bf16, const float* __restrict__ lse,
-                                                     float* __restrict__ zt, float* __restrict__ loss) {
+                                                     float tau, const float* __restrict__ lse, float* __restrict__ zt,
+                                                     float* __restrict__ loss) {
     __shared__ float z[kMaxTop];
     const int64_t row = blockIdx.x;
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, waves = blockDim.x / 64;
-    const uint16_t* hr = h + row * k;
-    for (int j = wave; j < top; j += waves) {
-        const int64_t word = index[row * top + j];
-        float s = 0.f;
-        if (entry_counts(word, teacher ? teacher[row * top + j] : 0.f, v)) {
-            const uint16_t* wr = w + word * k;
-#pragma unroll 4
-            for (int64_t c = 8 * lane; c < k; c += 512) {
-                const u16x8 a = *reinterpret_cast<const u16x8*>(hr + c), b = *reinterpret_cast<const u16x8*>(wr + c);
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, waves = blockDim.x / 64, g = lane / 16, l16 = lane % 16;
+    const uint8_t* hr = reinterpret_cast<const uint8_t*>(h + row * k);
+    for (int j0 = 16 * wave; j0 < top; j0 += 16 * waves) {
+        // absent entries take word 0, and their result is dropped
+        const int mine = j0 + l16;
+        const int64_t word = mine < top ? index[row * top + mine] : -1;
+        const bool counts = mine < top && entry_counts(word, teacher[row * top + mine], v);
+        const uint8_t* wr = reinterpret_cast<const uint8_t*>(w + (counts ? word : 0) * k);
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        // U stages from byte `at` of the rows, all loads before the products
+        const int64_t kbytes = 2 * k, full = kbytes / 128 * 128;
+        auto stages = [&](int64_t at, auto un, bool lo_in, bool hi_in) {
+            constexpr int U = decltype(un)::value;
+            const i32x4 none = {0, 0, 0, 0};
+            i32x4 r[U][2], c[U][2];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s = fmaf(half_bits_to_f32(a[i], bf16), half_bits_to_f32(b[i], bf16), s);
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int64_t b = at + 128 * u + 64 * j + 16 * g;
+                    const bool in = j ? hi_in : lo_in;
+                    r[u][j] = in ? *reinterpret_cast<const i32x4*>(wr + b) : none;
+                    c[u][j] = in ? *reinterpret_cast<const i32x4*>(hr + b) : none;
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                acc = mfma_pair<BF16 ? kBf16 : kF16>(__builtin_shufflevector(r[u][0], r[u][1], 0, 1, 2, 3, 4, 5, 6, 7),
+                                                     __builtin_shufflevector(c[u][0], c[u][1], 0, 1, 2, 3, 4, 5, 6, 7), acc);
+        };
+        constexpr int U = 8;
+        int64_t at = 0;
+        for (; at + 128 * U <= full; at += 128 * U) stages(at, std::integral_constant<int, U>{}, true, true);
+        for (; at < full; at += 128) stages(at, std::integral_constant<int, 1>{}, true, true);
+        if (full < kbytes) stages(full, std::integral_constant<int, 1>{}, full + 16 * g < kbytes, full + 16 * g + 64 < kbytes);
+        // lane 16 g holds words 4 g .. 4 g + 3 (all columns are the same)
+        const unsigned long long here = __ballot(counts);
+        if (l16 == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = j0 + 4 * g + i;
+                if (j >= top) continue;
+                z[j] = (here >> (4 * g + i)) & 1 ? acc[i] : 0.f;
+                zt[row * top + j] = z[j];
             }
-            s = wave_sum(s);
-        }
-        if (lane == 0) {
-            z[j] = s;
-            zt[row * top + j] = s;
         }
     }
     __syncthreads();
     if (wave != 0) return;
     const float l = lse[row];
-    float out = 0.f;
-    if (!teacher) {
-        const int64_t word = index[row];
-        out = word >= 0 && word < v ? l - z[0] : 0.f;
-    } else {
-        float m = -__builtin_inff();
-        bool any = false;
+    float out = 0.f, m = -__builtin_inff();
+    bool any = false;
+    for (int j = lane; j < top; j += 64) {
+        const float t = teacher[row * top + j];
+        if (entry_counts(index[row * top + j], t, v)) m = fmaxf(m, t), any = true;
+    }
+    // (t - m) / tau, not t / tau - m / tau: the lowest float over a tau below
+    // one would overflow
+    if (__any(any)) {
+        m = wave_max(m);
+        float s = 0.f;
         for (int j = lane; j < top; j += 64) {
             const float t = teacher[row * top + j];
-            if (entry_counts(index[row * top + j], t, v)) m = fmaxf(m, t), any = true;
+            if (entry_counts(index[row * top + j], t, v)) s += expf((t - m) / tau);
         }
-        // (t - m) / tau, not t / tau - m / tau: the lowest float over a tau below
-        // one would overflow
-        if (__any(any)) {
-            m = wave_max(m);
-            float s = 0.f;
-            for (int j = lane; j < top; j += 64) {
-                const float t = teacher[row * top + j];
-                if (entry_counts(index[row * top + j], t, v)) s += expf((t - m) / tau);
-            }
-            const float ls = logf(wave_sum(s));
-            for (int j = lane; j < top; j += 64) {
-                const float t = teacher[row * top + j];
-                if (!entry_counts(index[row * top + j], t, v)) continue;
-                const float lp = (t - m) / tau - ls, p = expf(lp);
-                out += p > 0.f || p != p ? p * (lp - (z[j] / tau - l)) : 0.f;
-            }
-            out = tau * tau * wave_sum(out);
+        const float ls = logf(wave_sum(s));
+        for (int j = lane; j < top; j += 64) {
+            const float t = teacher[row * top + j];
+            if (!entry_counts(index[row * top + j], t, v)) continue;
+            const float lp = (t - m) / tau - ls, p = expf(lp);
+            out += p > 0.f || p != p ? p * (lp - (z[j] / tau - l)) : 0.f;
         }
+        out = tau * tau * wave_sum(out);
     }
     if (lane == 0) loss[row] = out;
 }
@@ -479,7 +530,7 @@ __global__ __launch_bounds__(C::NT) void k_dz(Operand H, Operand W, int64_t kbyt
 __global__ __launch_bounds__(256) void k_dz_targets(const int64_t* __restrict__ index, const float* __restrict__ weight,
                                                     const float* __restrict__ zt, const float* __restrict__ lse,
                                                     const float* __restrict__ g, const uint32_t* __restrict__ slots,
-                                                    int64_t n, int top, float c2, int64_t v0, int64_t vc, int64_t v,
+                                                    int64_t n, int top, float tau, int64_t v0, int64_t vc, int64_t v,
                                                     const float* __restrict__ teacher, _Float16* __restrict__ dz,
                                                     int64_t ldz) {
     const int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -487,7 +538,7 @@ __global__ __launch_bounds__(256) void k_dz_targets(const int64_t* __restrict__ 
     const int64_t row = u / top, word = index[u];
     if (!entry_counts(word, teacher ? teacher[u] : 0.f, v) || word < v0 || word >= v0 + vc) return;
     const float f = RowScale(g[row], slots[2]).f * kDzScale;
-    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(zt[u], c2, -lse[row] * kLog2e));
+    const float p = __builtin_amdgcn_exp2f((zt[u] / tau - lse[row]) * kLog2e);  // at most one
     dz[row * ldz + word - v0] = static_cast<_Float16>(f == 0.f ? 0.f : (p - weight[u]) * f);
 }
 
@@ -608,14 +659,19 @@ hipError_t launch_loss(const LossJob& j, hipStream_t stream) {
         const int64_t tm = (j.n + C::TL - 1) / C::TL;
         tiles = (j.v + C::TR - 1) / C::TR;
         const TileMap map = TileMap::make(tm, tiles);
-        hipLaunchKernelGGL(k_logit_stats<C>, dim3(map.grid), dim3(C::NT), 0, stream, H, W, 2 * j.k, c2, part, map);
+        hipLaunchKernelGGL(k_logit_stats<C>, dim3(map.grid), dim3(C::NT), 0, stream, H, W, 2 * j.k, c2, part,
+                           j.teacher ? nullptr : j.index, j.zt, map);
         return hipGetLastError();
     });
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_join_stats, dim3(blocks_of(j.n, 32)), dim3(256), 0, stream, part, tiles, j.n, j.lse);
-    hipLaunchKernelGGL(k_target_loss, dim3(static_cast<unsigned>(j.n)), dim3(64 * (j.top < 4 ? j.top : 4)), 0, stream,
-                       static_cast<const uint16_t*>(j.h), static_cast<const uint16_t*>(j.w), j.index, j.teacher, j.v, j.k,
-                       j.top, j.tau, j.bf16 ? 1 : 0, j.lse, j.zt, j.loss);
+    hipLaunchKernelGGL(k_join_stats, dim3(blocks_of(j.n, 32)), dim3(256), 0, stream, part, tiles, j.n, c2, j.tau, j.lse,
+                       j.teacher ? nullptr : j.index, j.v, j.zt, j.loss);
+    if (j.teacher) {
+        const int waves = (j.top + 15) / 16;
+        hipLaunchKernelGGL(j.bf16 ? k_listed_loss<true> : k_listed_loss<false>, dim3(static_cast<unsigned>(j.n)),
+                           dim3(64 * (waves < 4 ? waves : 4)), 0, stream, static_cast<const uint16_t*>(j.h),
+                           static_cast<const uint16_t*>(j.w), j.index, j.teacher, j.v, j.k, j.top, j.tau, j.lse, j.zt, j.loss);
+    }
     return hipGetLastError();
 }
 
@@ -666,7 +722,7 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
         });
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(k_dz_targets, dim3(blocks_of(j.n * j.top, 256)), dim3(256), 0, stream, j.index, weight, j.zt, j.lse, g,
-                           slots, j.n, j.top, c2, v0, vc, j.v, j.teacher, dz, ldz);
+                           slots, j.n, j.top, j.tau, v0, vc, j.v, j.teacher, dz, ldz);
         if (j.dw) {
             e = transpose16(dz, ldz, j.n, vc, dzt, ldn, false, nullptr, nullptr, nullptr, stream);
             if (e != hipSuccess) return e;

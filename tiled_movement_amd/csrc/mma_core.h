@@ -291,14 +291,18 @@ __device__ __forceinline__ f32x4 mfma_e8m0_r(i32x8 r, i32x8 l, f32x4 c, int sr, 
     }
 }
 
-// The stage's two 16x16x32 products of bf16 fragments.
-__device__ __forceinline__ f32x4 mfma_bf16_pair(i32x8 r, i32x8 l, f32x4 acc) {
+// The stage's two 16x16x32 products of two-byte fragments.
+template <int ELEM>
+__device__ __forceinline__ f32x4 mfma_pair(i32x8 r, i32x8 l, f32x4 acc) {
     const i32x4 r0 = __builtin_shufflevector(r, r, 0, 1, 2, 3), r1 = __builtin_shufflevector(r, r, 4, 5, 6, 7);
     const i32x4 l0 = __builtin_shufflevector(l, l, 0, 1, 2, 3), l1 = __builtin_shufflevector(l, l, 4, 5, 6, 7);
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r0), __builtin_bit_cast(bf16x8, l0), acc, 0,
-                                                  0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r1), __builtin_bit_cast(bf16x8, l1), acc, 0,
-                                                   0, 0);
+    if constexpr (ELEM == kF16) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, r0), __builtin_bit_cast(f16x8, l0), acc, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, r1), __builtin_bit_cast(f16x8, l1), acc, 0, 0, 0);
+    } else {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r0), __builtin_bit_cast(bf16x8, l0), acc, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, r1), __builtin_bit_cast(bf16x8, l1), acc, 0, 0, 0);
+    }
 }
 
 // Adds one stage's product of block fragments: r rows (registers), l columns
@@ -327,16 +331,7 @@ __device__ __forceinline__ void mma_stage(f32x4& acc, i32x8 r, i32x8 l, int sr, 
             }
         }
     } else {
-        if constexpr (C::ELEM == kBf16) {
-            acc = mfma_bf16_pair(r, l, acc);
-        } else {
-            const i32x4 r0 = __builtin_shufflevector(r, r, 0, 1, 2, 3), r1 = __builtin_shufflevector(r, r, 4, 5, 6, 7);
-            const i32x4 l0 = __builtin_shufflevector(l, l, 0, 1, 2, 3), l1 = __builtin_shufflevector(l, l, 4, 5, 6, 7);
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, r0), __builtin_bit_cast(f16x8, l0), acc,
-                                                         0, 0, 0);
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, r1), __builtin_bit_cast(f16x8, l1), acc,
-                                                         0, 0, 0);
-        }
+        acc = mfma_pair<C::ELEM>(r, l, acc);
     }
 }
 
@@ -463,7 +458,7 @@ __device__ __forceinline__ void stage_products_wide(f32x4 (&acc)[C::BL][C::BR], 
 #pragma unroll
             for (int x = 0; x < C::BL; ++x) {
                 f32x4 p = C::SC == kE8M0 ? acc[x][y] : f32x4{0.f, 0.f, 0.f, 0.f};
-                p = mfma_bf16_pair(rf, lf[x], p);
+                p = mfma_pair<kBf16>(rf, lf[x], p);
                 if constexpr (C::SC == kE8M0) {
                     acc[x][y] = p;
                 } else {
