@@ -563,7 +563,9 @@ int swz_linear_ce_grad(const void* d_h, const void* d_w, int32_t x_type, const i
  *               -infinity are absent; a row without entries has loss 0 and adds
  *               nothing to the gradients.  Equal indices add up.
  *   d_zt      : float [n][top], the student's logits (before tau) at the entries.
- *   tau       : > 0 and finite.
+ *   tau       : > 0, finite and a normal number.  The loss is tau^2 times a
+ *               difference of fp32 numbers of the size of lse, and z / tau has
+ *               to stay within fp32.
  * The rest, and the errors, as swz_linear_ce (SWZ_EUNSUPPORTED also for top
  * above 256). */
 int swz_linear_distill(const void* d_h, const void* d_w, int32_t x_type, const int64_t* d_index,

@@ -144,3 +144,43 @@ def test_listed_logits_are_the_same_number_in_both_losses(n, v, k, dt):
         torch.cuda.synchronize()
         assert torch.equal(f["zt"][:, 0], d["zt"][:, j])
         assert torch.equal(f["lse"], d["lse"])
+
+
+@pytest.mark.parametrize("tau", [1e-25, 1e-8, 1e-5])
+@pytest.mark.parametrize("n,v,k", [(50, 700, 64), (300, 16500, 64)])
+def test_temperatures_that_leave_one_word(n, v, k, tau):
+    """H rows pick one feature and W holds multiples of 1/16: the row's largest logit is 1/16 or more above the others,
+    hundreds and more over tau, so both softmaxes are one word each.  Then lse is the largest logit over tau, the loss
+    tau times the distance of the two words' logits, and a row of dH the difference of two rows of W (multiples of 1/16
+    up to 32: a difference is exact in fp32, so one rounding to bf16, 2^-8)."""
+    announce("temperature", n, v, k, tau)
+    rng = np.random.default_rng(28)
+    c = Case(n, v, k, "bf16", top=8, tau=float(np.float32(tau)), seed=28, absent=0.0)
+    feature = rng.integers(0, k, n)
+    h = np.zeros((n, k))
+    h[np.arange(n), feature] = 1.0
+    w = rng.integers(-256, 240, size=(v, k)) / 16.0
+    best = rng.permutation(v)[:k]
+    w[best, np.arange(k)] = 15.0 + 1.0 / 16  # the largest of its column
+    c.h, c.w = torch.from_numpy(h).bfloat16(), torch.from_numpy(w).bfloat16()
+    w = c.w.double().numpy()
+    z = h @ w.T
+    two = np.sort(z, axis=1)[:, -2:]
+    assert np.all(two[:, 1] - two[:, 0] >= 1 / 16)
+    c.index = np.stack([rng.permutation(v)[:8] for _ in range(n)])
+    c.teacher = np.stack([rng.permutation(8) for _ in range(n)]).astype(np.float32)
+    c.upstream = np.full(n, 1 / c.tau, np.float32)
+    d = c.device()
+    c.forward(d)
+    c.backward(d)
+    torch.cuda.synchronize()
+    top = z.argmax(axis=1)
+    word = c.index[np.arange(n), c.teacher.argmax(axis=1)]
+    # two roundings of z / tau and one of the sum, and their differences scaled back
+    m = z.max(axis=1) / c.tau
+    assert np.all(np.abs(d["lse"].double().cpu().numpy() - m) <= 3 * U * np.abs(m))
+    loss = c.tau * (z[np.arange(n), top] - z[np.arange(n), word])
+    assert np.all(np.abs(d["loss"].double().cpu().numpy() - loss) <= c.tau * 8 * U * np.abs(z).max(axis=1))
+    # the two 1 / tau of upstream and of 1 / tau times tau: one within 2 U
+    ref = np.where((top == word)[:, None], 0.0, w[top] - w[word])
+    assert np.all(np.abs(d["dh"].double().cpu().numpy() - ref) <= (2.0 ** -8 + 2.0 ** -11 + 4 * U) * np.abs(ref) + 2.0 ** -20)

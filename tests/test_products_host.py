@@ -165,6 +165,17 @@ def test_loss_sizes_of_any_magnitude_are_refused(big):
             assert losses(which, wsb=1 << 45, **kw) == EUNSUP, (which, kw)
 
 
+@pytest.mark.parametrize("which", ["distill", "distill_grad"])
+def test_temperatures_at_the_ends_of_the_range(which):
+    """Every finite normal temperature is taken (checked with nothing to do), a subnormal one, whose inverse is not, refused."""
+    tiny = float(np.finfo(np.float32).tiny)
+    nothing = dict(n=0, dw=None) if "grad" in which else dict(n=0)
+    for tau in (tiny, 1e-30, 3.4e38, float(np.finfo(np.float32).max)):
+        assert losses(which, tau=tau, **nothing) == OK, tau
+    for tau in (tiny / 2, 1e-40, float(np.finfo(np.float32).smallest_subnormal)):
+        assert losses(which, tau=tau, **nothing) == EINVAL, tau
+
+
 class FakeCuda:
     is_cuda = True
 

@@ -1,6 +1,7 @@
 // C ABI of libswz.so: argument checks, parameter choice and launches.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -139,7 +140,7 @@ int loss_forward(const void* d_h, const void* d_w, int32_t x_type, const int64_t
                  float tau, float* loss, float* lse, float* zt, int64_t n, int64_t v, int64_t k, void* ws, int64_t ws_bytes,
                  void* stream) {
     if (x_type != SWZ_X_BF16 && x_type != SWZ_X_F16) return SWZ_EINVAL;
-    if (!(tau > 0.f) || tau > 3.4e38f) return SWZ_EINVAL;
+    if (!(tau >= FLT_MIN && tau <= FLT_MAX)) return SWZ_EINVAL;  // 1 / tau and log2(e) / tau are finite then
     const int st = check_loss_sizes(n, v, k, top);
     if (st != SWZ_OK) return st;
     if (n == 0) return SWZ_OK;
@@ -160,7 +161,7 @@ int loss_backward(const void* d_h, const void* d_w, int32_t x_type, const int64_
                   float tau, const float* lse, const float* zt, const float* upstream, void* dh, void* dw, int64_t n,
                   int64_t v, int64_t k, void* ws, int64_t ws_bytes, void* stream) {
     if (x_type != SWZ_X_BF16 && x_type != SWZ_X_F16) return SWZ_EINVAL;
-    if (!(tau > 0.f) || tau > 3.4e38f) return SWZ_EINVAL;
+    if (!(tau >= FLT_MIN && tau <= FLT_MAX)) return SWZ_EINVAL;  // 1 / tau and log2(e) / tau are finite then
     const int st = check_loss_sizes(n, v, k, top);
     if (st != SWZ_OK) return st;
     if (!dh && !dw) return SWZ_EINVAL;

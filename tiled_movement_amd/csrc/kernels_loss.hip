@@ -16,7 +16,8 @@
 // A logit is one number wherever it enters: a tile writes cross entropy's at
 // the target, and distillation's at listed words are made by the same
 // instructions in the same order; and lse is the largest logit over tau plus a
-// logarithm of at least one.  So lse is never below a listed logit, cross
+// logarithm of at least one, with the same product by 1/tau (over_tau) wherever
+// a logit meets lse.  So lse is never below a listed logit, cross
 // entropy's loss and the target's p - 1 have their signs, and a row that is
 // certain of its target has no loss and no gradient (with a sum of its own for
 // the target's logit: losses of +-2e-5 at logits of 90).
@@ -54,6 +55,19 @@ typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ float half_bits_to_f32(uint16_t b, bool bf16) {
     return bf16 ? __uint_as_float(static_cast<uint32_t>(b) << 16)
                 : static_cast<float>(__builtin_bit_cast(_Float16, b));
+}
+
+// z / tau as one product by inv = 1 / tau, rounded by itself (a fused
+// multiply-add with what it meets would round elsewhere): rounding keeps the
+// order, so no logit comes out above its row's largest, however far over tau.
+__device__ __forceinline__ float over_tau(float z, float inv) {
+#pragma clang fp contract(off)
+    return z * inv;
+}
+// exp(z / tau - lse): at most one.
+__device__ __forceinline__ float probability(float z, float inv, float lse) {
+#pragma clang fp contract(off)
+    return __builtin_amdgcn_exp2f((over_tau(z, inv) - lse) * kLog2e);
 }
 
 // ------------------------------------------------------------------ forward
@@ -130,7 +144,7 @@ __global__ __launch_bounds__(C::NT) void k_logit_stats(Operand H, Operand W, int
 // lse from the pieces: 32 rows a workgroup, eight threads a row; and cross
 // entropy's loss (index given), with zt of the rows that do not count.
 __global__ __launch_bounds__(256) void k_join_stats(const float2* __restrict__ part, int64_t tiles, int64_t n, float c2,
-                                                    float tau, float* __restrict__ lse, const int64_t* __restrict__ index,
+                                                    float inv, float* __restrict__ lse, const int64_t* __restrict__ index,
                                                     int64_t v, float* __restrict__ zt, float* __restrict__ loss) {
     __shared__ float2 red[8][32];
     const int r = threadIdx.x % 32, sub = threadIdx.x / 32;
@@ -153,7 +167,7 @@ __global__ __launch_bounds__(256) void k_join_stats(const float2* __restrict__ p
         const float b = m == -__builtin_inff() ? 0.f : m;
         float total = 0.f;
         for (int i = 0; i < 8; ++i) total += red[i][r].y * __builtin_amdgcn_exp2f((red[i][r].x - b) * c2);
-        const float l = m / tau + logf(total);
+        const float l = over_tau(m, inv) + logf(total);
         lse[row] = l;
         if (index) {
             const bool counts = index[row] >= 0 && index[row] < v;
@@ -262,9 +276,9 @@ __global__ __launch_bounds__(256) void k_listed_loss(const uint16_t* __restrict_
             const float t = teacher[row * top + j];
             if (!entry_counts(index[row * top + j], t, v)) continue;
             const float lp = (t - m) / tau - ls, p = expf(lp);
-            out += p > 0.f || p != p ? p * (lp - (z[j] / tau - l)) : 0.f;
+            out += p > 0.f || p != p ? p * (lp - (over_tau(z[j], 1.f / tau) - l)) : 0.f;
         }
-        out = tau * tau * wave_sum(out);
+        out = tau * (tau * wave_sum(out));  // tau^2 alone may leave fp32's range
     }
     if (lane == 0) loss[row] = out;
 }
@@ -491,7 +505,7 @@ __global__ __launch_bounds__(256) void k_transpose16(const uint16_t* __restrict_
 
 // dz of words [j0, ...) of a piece (W starts at the piece): fp16 [rows][ldz].
 template <class C>
-__global__ __launch_bounds__(C::NT) void k_dz(Operand H, Operand W, int64_t kbytes, float c2,
+__global__ __launch_bounds__(C::NT) void k_dz(Operand H, Operand W, int64_t kbytes, float inv,
                                               const float* __restrict__ lse, const float* __restrict__ g,
                                               const uint32_t* __restrict__ slots, _Float16* __restrict__ dz, int64_t ldz,
                                               TileMap map) {
@@ -509,12 +523,12 @@ __global__ __launch_bounds__(C::NT) void k_dz(Operand H, Operand W, int64_t kbyt
     for (int x = 0; x < C::BL; ++x) {
         int64_t row = i0 + (wl * C::BL + x) * 16 + l16;
         row = row < H.rows ? row : H.rows - 1;
-        const float f = RowScale(g[row], gmax).f * kDzScale, l2 = lse[row] * kLog2e;
+        const float f = RowScale(g[row], gmax).f * kDzScale, l = lse[row];
 #pragma unroll
         for (int y = 0; y < C::BR; ++y)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[x][y][i], c2, -l2));
+                const float p = probability(acc[x][y][i], inv, l);
                 acc[x][y][i] = f == 0.f ? 0.f : p * f;
             }
     }
@@ -530,7 +544,7 @@ __global__ __launch_bounds__(C::NT) void k_dz(Operand H, Operand W, int64_t kbyt
 __global__ __launch_bounds__(256) void k_dz_targets(const int64_t* __restrict__ index, const float* __restrict__ weight,
                                                     const float* __restrict__ zt, const float* __restrict__ lse,
                                                     const float* __restrict__ g, const uint32_t* __restrict__ slots,
-                                                    int64_t n, int top, float tau, int64_t v0, int64_t vc, int64_t v,
+                                                    int64_t n, int top, float inv, int64_t v0, int64_t vc, int64_t v,
                                                     const float* __restrict__ teacher, _Float16* __restrict__ dz,
                                                     int64_t ldz) {
     const int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -538,7 +552,7 @@ __global__ __launch_bounds__(256) void k_dz_targets(const int64_t* __restrict__ 
     const int64_t row = u / top, word = index[u];
     if (!entry_counts(word, teacher ? teacher[u] : 0.f, v) || word < v0 || word >= v0 + vc) return;
     const float f = RowScale(g[row], slots[2]).f * kDzScale;
-    const float p = __builtin_amdgcn_exp2f((zt[u] / tau - lse[row]) * kLog2e);  // at most one
+    const float p = probability(zt[u], inv, lse[row]);
     dz[row * ldz + word - v0] = static_cast<_Float16>(f == 0.f ? 0.f : (p - weight[u]) * f);
 }
 
@@ -664,7 +678,7 @@ hipError_t launch_loss(const LossJob& j, hipStream_t stream) {
         return hipGetLastError();
     });
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_join_stats, dim3(blocks_of(j.n, 32)), dim3(256), 0, stream, part, tiles, j.n, c2, j.tau, j.lse,
+    hipLaunchKernelGGL(k_join_stats, dim3(blocks_of(j.n, 32)), dim3(256), 0, stream, part, tiles, j.n, c2, 1.f / j.tau, j.lse,
                        j.teacher ? nullptr : j.index, j.v, j.zt, j.loss);
     if (j.teacher) {
         const int waves = (j.top + 15) / 16;
@@ -692,7 +706,7 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
     auto* ht = reinterpret_cast<uint16_t*>(ws + p.ht);
     auto* wt = reinterpret_cast<uint16_t*>(ws + p.wt);
     auto* sums = reinterpret_cast<float*>(ws + p.sums);
-    const float c2 = kLog2e / j.tau;
+    const float inv = 1.f / j.tau;
     const int64_t ldn = (j.n + 7) / 8 * 8;
     hipLaunchKernelGGL(k_clear_slots, dim3(1), dim3(64), 0, stream, slots);
     if (j.teacher)
@@ -717,12 +731,12 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
             using C = decltype(cfg);
             const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (vc + C::TR - 1) / C::TR;
             const TileMap map = TileMap::make(tm, tn);
-            hipLaunchKernelGGL(k_dz<C>, dim3(map.grid), dim3(C::NT), 0, stream, H, W, 2 * j.k, c2, j.lse, g, slots, dz, ldz, map);
+            hipLaunchKernelGGL(k_dz<C>, dim3(map.grid), dim3(C::NT), 0, stream, H, W, 2 * j.k, inv, j.lse, g, slots, dz, ldz, map);
             return hipGetLastError();
         });
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(k_dz_targets, dim3(blocks_of(j.n * j.top, 256)), dim3(256), 0, stream, j.index, weight, j.zt, j.lse, g,
-                           slots, j.n, j.top, j.tau, v0, vc, j.v, j.teacher, dz, ldz);
+                           slots, j.n, j.top, inv, v0, vc, j.v, j.teacher, dz, ldz);
         if (j.dw) {
             e = transpose16(dz, ldz, j.n, vc, dzt, ldn, false, nullptr, nullptr, nullptr, stream);
             if (e != hipSuccess) return e;
