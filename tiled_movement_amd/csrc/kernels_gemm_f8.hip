@@ -39,16 +39,24 @@ __global__ __launch_bounds__(C::NT) void k_gemm_f8(Operand A, Operand B, CT* __r
     store_tile<C>(acc, slice, c, ldc, wi, wj, A.rows, B.rows, vec, lane, [](float v) { return v; });
 }
 
+// A launch's threads stay below 2^32 along x, so more than 2^22 tiles (the
+// entry point's bound is in tiles of 256 x 256) go by ranges of rows.
 template <class C, class CT>
 hipError_t launch_tiles(const GemmF8Job& j, bool by_xcd, hipStream_t stream) {
-    const Operand A{static_cast<const uint8_t*>(j.a), j.lda, j.m, j.scale_a, (j.k + 127) / 128, j.a_square ? 7 : 0};
-    const Operand B{static_cast<const uint8_t*>(j.b), j.ldb, j.n, j.scale_b, (j.k + 127) / 128, j.b_square ? 7 : 0};
-    const int64_t tm = (j.m + C::TL - 1) / C::TL, tn = (j.n + C::TR - 1) / C::TR;
-    if (tm > 0x7fffffff / C::NT / tn) return hipErrorInvalidValue;
+    constexpr int ES = C::SC == kE8M0 ? 1 : 4;
+    const int64_t tn = (j.n + C::TR - 1) / C::TR, kb = (j.k + 127) / 128, most = (int64_t(1) << 22) / tn * C::TL;
     const int vec = j.n * static_cast<int64_t>(sizeof(CT)) % 16 == 0 && reinterpret_cast<uintptr_t>(j.c) % 16 == 0;
-    const TileMap map = TileMap::make(tm, tn);
-    hipLaunchKernelGGL((k_gemm_f8<C, CT>), dim3(by_xcd ? static_cast<unsigned>(tm * tn) : map.grid), dim3(C::NT), 0, stream, A, B,
-                       static_cast<CT*>(j.c), j.n, j.k, map, vec, by_xcd ? 1 : 0);
+    const Operand B{static_cast<const uint8_t*>(j.b), j.ldb, j.n, j.scale_b, kb, j.b_square ? 7 : 0};
+    static_assert(C::TL % 128 == 0 || C::TL == 64, "ranges of rows are whole squares (64 rows: a single range)");
+    for (int64_t i0 = 0; i0 < j.m; i0 += most) {
+        const int64_t rows = j.m - i0 < most ? j.m - i0 : most, tm = (rows + C::TL - 1) / C::TL;
+        const int64_t scale0 = (j.a_square ? i0 / 128 : i0) * kb * ES;
+        const Operand A{static_cast<const uint8_t*>(j.a) + i0 * j.lda, j.lda, rows,
+                        static_cast<const uint8_t*>(j.scale_a) + scale0, kb, j.a_square ? 7 : 0};
+        const TileMap map = TileMap::make(tm, tn);
+        hipLaunchKernelGGL((k_gemm_f8<C, CT>), dim3(by_xcd ? static_cast<unsigned>(tm * tn) : map.grid), dim3(C::NT), 0, stream, A,
+                           B, static_cast<CT*>(j.c) + i0 * j.n, j.n, j.k, map, vec, by_xcd ? 1 : 0);
+    }
     return hipGetLastError();
 }
 
