@@ -626,9 +626,9 @@ __global__ __launch_bounds__(256) void k_finish_h(const float* __restrict__ sums
     reinterpret_cast<ct4*>(dh)[u] = o;
 }
 
-__global__ __launch_bounds__(256) void k_zero16(uint32_t* __restrict__ p, int64_t words) {
-    const int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (u < words) p[u] = 0;
+__global__ __launch_bounds__(256) void k_zero16(i32x4* __restrict__ p, int64_t pieces) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; u < pieces; u += step) p[u] = i32x4{0, 0, 0, 0};
 }
 
 unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); }
@@ -693,8 +693,9 @@ hipError_t launch_loss_grad(const LossJob& j, const LossPlan& p, hipStream_t str
     auto* ws = static_cast<uint8_t*>(j.ws);
     if (j.n == 0) {  // no rows: the weights' gradient is zero (v k is a multiple of 8)
         if (j.dw) {
-            const int64_t words = j.v * j.k / 2;
-            hipLaunchKernelGGL(k_zero16, dim3(blocks_of(words, 256)), dim3(256), 0, stream, static_cast<uint32_t*>(j.dw), words);
+            const int64_t pieces = j.v * j.k / 8;  // may be more than one launch has threads
+            const unsigned grid = pieces > 65536 * 256 ? 65536u : blocks_of(pieces, 256);
+            hipLaunchKernelGGL(k_zero16, dim3(grid), dim3(256), 0, stream, static_cast<i32x4*>(j.dw), pieces);
         }
         return hipGetLastError();
     }
