@@ -221,6 +221,89 @@ def test_binding_checks_its_buffers(monkeypatch):
         T.swz_linear_ce(big, big, i64, f32, f32, f32, 50, 700, 60, big)
 
 
+class Typed(FakeCuda):
+    """A FakeCuda with an element type."""
+
+    def __init__(self, dtype, nbytes=1 << 24):
+        super().__init__(nbytes, dtype.itemsize)
+        self.dtype = dtype
+
+
+BF, HF, FL, F64, BYTE, I16, I32, I64 = (torch.bfloat16, torch.float16, torch.float32, torch.float64, torch.uint8, torch.int16,
+                                        torch.int32, torch.int64)
+E4, E5, E8 = torch.float8_e4m3fn, torch.float8_e5m2, torch.float8_e8m0fnu
+
+
+def _call(name, dtypes, **kw):
+    """One call of a binding with buffers of the given types, which have to be right but for one."""
+    b = {k: None if d is None else Typed(d) for k, d in dtypes.items()}
+    if name == "quant":
+        T.swz_quant_f8(b["x"], b["q"], b["scale"], 100, 200, qt=b["qt"], scale_t=b["scale_t"], **kw)
+    elif name == "gemm":
+        T.swz_gemm_f8(b["a"], b["scale_a"], b["b"], b["scale_b"], b["c"], 100, 200, 300, **kw)
+    else:
+        grad, distill = "grad" in name, "distill" in name
+        args = [b["h"], b["w"], b["index" if distill else "target"]] + ([b["teacher"]] if distill else [])
+        args += [b["lse"], b["zt"], b["upstream"], b["dh"], b["dw"]] if grad else [b["loss"], b["lse"], b["zt"]]
+        args += [50, 700, 64] + ([3, 1.0] if distill else [])
+        getattr(T, "swz_linear_" + name)(*args, b["ws"], **kw)
+
+
+QUANT_T = dict(x=BF, q=BYTE, scale=BYTE, qt=BYTE, scale_t=BYTE)
+GEMM_T = dict(a=BYTE, scale_a=BYTE, b=BYTE, scale_b=BYTE, c=BF)
+CE_T = dict(h=BF, w=BF, target=I64, loss=FL, lse=FL, zt=FL, ws=BYTE)
+CEG_T = dict(h=BF, w=BF, target=I64, lse=FL, zt=FL, upstream=FL, dh=BF, dw=BF, ws=BYTE)
+DI_T = dict(h=BF, w=BF, index=I64, teacher=FL, loss=FL, lse=FL, zt=FL, ws=BYTE)
+DIG_T = dict(h=BF, w=BF, index=I64, teacher=FL, lse=FL, zt=FL, upstream=FL, dh=BF, dw=BF, ws=BYTE)
+WRONG = [("quant", QUANT_T, {}, dict(x=[HF, FL, F64], q=[E5, FL, I16], scale=[FL, HF, I32], qt=[E5, BF], scale_t=[FL, E4])),
+         ("quant", QUANT_T, dict(x_type=T.X_F32), dict(x=[BF, HF, F64])),
+         ("quant", {**QUANT_T, "x": HF}, dict(x_type=T.X_F16, f8_type=T.F8_E5M2), dict(x=[BF, FL], q=[E4], qt=[E4])),
+         ("quant", QUANT_T, dict(scale_type=T.SCALE_F32), dict(scale=[BYTE, HF, F64, E8])),
+         ("gemm", GEMM_T, {}, dict(a=[E5, BF, I32], b=[E5, FL], scale_a=[FL, E4, I16], scale_b=[FL], c=[FL, HF, F64])),
+         ("gemm", {**GEMM_T, "c": FL}, dict(a_type=T.F8_E5M2, c_type=T.C_F32), dict(a=[E4], c=[BF, F64])),
+         ("gemm", {**GEMM_T, "scale_a": FL, "scale_b": FL}, dict(scale_type=T.SCALE_F32), dict(scale_a=[BYTE, F64], scale_b=[E8, HF])),
+         ("ce", CE_T, {}, dict(h=[HF, FL, F64], w=[HF, FL], target=[I32, F64, FL], loss=[F64, BF, I64], lse=[F64, HF], zt=[F64])),
+         ("ce_grad", CEG_T, {}, dict(h=[HF], w=[HF], target=[I32, F64], lse=[F64], zt=[F64, BF], upstream=[F64, BF, HF], dh=[HF, FL],
+                                     dw=[HF, FL])),
+         ("ce_grad", {**CEG_T, "h": HF, "w": HF, "dh": HF, "dw": HF}, dict(x_type=T.X_F16), dict(h=[BF], w=[BF], dh=[BF], dw=[BF])),
+         ("distill", DI_T, {}, dict(h=[HF], w=[HF], index=[I32, F64], teacher=[F64, BF], loss=[F64], lse=[F64], zt=[F64])),
+         ("distill_grad", DIG_T, {}, dict(h=[HF], index=[I32], teacher=[F64], lse=[F64], zt=[F64], upstream=[F64], dh=[HF], dw=[HF]))]
+
+
+@pytest.mark.parametrize("name,right,kw,wrong", WRONG)
+def test_binding_refuses_tensors_of_other_types(monkeypatch, name, right, kw, wrong):
+    """A tensor of another type than the call reads there is named, not read as what it is not."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for buf, dtypes in wrong.items():
+        for dtype in dtypes:
+            types = {**right, buf: dtype}
+            if kw.get("scale_type") == T.SCALE_F32:
+                types = {**{k: FL for k in right if "scale" in k}, **{k: v for k, v in types.items() if "scale" not in k}, buf: dtype}
+            with pytest.raises(ValueError, match=f": {buf} "):
+                _call(name, types, **kw)
+
+
+@pytest.mark.parametrize("name,right,kw,wrong", WRONG)
+def test_binding_takes_tensors_of_the_right_types_and_raw_bits(monkeypatch, name, right, kw, wrong):
+    """Right types, and integers of their size as raw bits, pass the checks (what comes next, the address, is not asked for)."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    types = {**right}
+    if kw.get("scale_type") == T.SCALE_F32:
+        types.update({k: FL for k in right if "scale" in k})
+    if name == "quant" and kw.get("x_type") == T.X_F32:
+        types["x"] = FL
+    raw = {1: BYTE, 2: I16, 4: I32, 8: I64}
+    f8 = {"q": E4, "qt": E4, "a": E4, "b": E4, "scale": E8, "scale_t": E8, "scale_a": E8, "scale_b": E8}
+    named = {k: f8[k] if k in f8 and d == BYTE else d for k, d in types.items()}
+    if kw.get("f8_type") == T.F8_E5M2:
+        named.update(q=E5, qt=E5)
+    if kw.get("a_type") == T.F8_E5M2:
+        named["a"] = E5
+    for given in (types, {k: raw[d.itemsize] for k, d in types.items()}, named):
+        with pytest.raises(AssertionError, match="reached the library"):
+            _call(name, given, **kw)
+
+
 # ---------------------------------------------------------- 64-bit definitions
 @pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
 def test_rounding_picks_the_nearest_value_and_even_on_ties(kind):

@@ -339,6 +339,35 @@ def swz_gemm_ex(a, bt, c, m: int, n: int, k: int, layout: str = "swizzle", param
                            _stream(stream, a, bt, c)), "swz_gemm_ex")
 
 
+# What the calls below read, by their enums: (bytes per element, torch type).
+_X = {X_BF16: (2, "bfloat16"), X_F16: (2, "float16"), X_F32: (4, "float32")}
+_F8 = {F8_E4M3: (1, "float8_e4m3fn"), F8_E5M2: (1, "float8_e5m2")}
+_SCALE = {SCALE_F32: (4, "float32"), SCALE_E8M0: (1, "float8_e8m0fnu")}
+_C = {C_F32: (4, "float32"), C_BF16: (2, "bfloat16")}
+_FLOAT, _INDEX = (4, "float32"), (8, "int64")
+_TYPES_SEEN = set()  # (torch type, what the call reads) that fit: looked up instead of compared, a call's own time counts
+
+
+def _typed(call: str, **bufs) -> None:
+    """Raise ValueError for a tensor that is not of the type the call reads (name=(tensor, (bytes per element, type))).
+
+    Whole numbers of the element's size pass as its raw bits.  An enum that the library does not know leaves its
+    buffers to the library, which refuses it."""
+    for name, (t, kind) in bufs.items():
+        if t is None or kind is None or isinstance(t, int):
+            continue
+        dtype = getattr(t, "dtype", None)
+        if (dtype, kind) in _TYPES_SEEN:
+            continue
+        size, want = kind
+        if t.element_size() != size:
+            raise ValueError(f"{call}: {name} has {t.element_size()}-byte elements, the call reads {size}-byte ones")
+        if dtype is not None:
+            if (dtype.is_floating_point or dtype.is_complex) and str(dtype) != f"torch.{want}":
+                raise ValueError(f"{call}: {name} holds {dtype}, the call reads {want}")
+            _TYPES_SEEN.add((dtype, kind))
+
+
 def _f8_scale_bytes(rows: int, cols: int, block: int, scale_type: int) -> int:
     return (-(-rows // 128) if block == BLOCK_128X128 else rows) * -(-cols // 128) * (1 if scale_type == SCALE_E8M0 else 4)
 
@@ -355,6 +384,8 @@ def swz_quant_f8(x, q, scale, rows: int, cols: int, x_type: int = X_BF16, f8_typ
     _buf("swz_quant_f8", x=(x, rows * ld_x * (4 if x_type == X_F32 else 2)), q=(q, rows * ld_q),
          scale=(scale, _f8_scale_bytes(rows, cols, block, scale_type)), qt=(qt, cols * ld_qt),
          scale_t=(scale_t, _f8_scale_bytes(cols, rows, block, scale_type)))
+    f8, sc = _F8.get(f8_type), _SCALE.get(scale_type)
+    _typed("swz_quant_f8", x=(x, _X.get(x_type)), q=(q, f8), scale=(scale, sc), qt=(qt, f8), scale_t=(scale_t, sc))
     _check(lib.swz_quant_f8(_ptr(x), x_type, rows, cols, ld_x, f8_type, block, scale_type, _ptr(q), _ptr(scale), ld_q,
                             _ptr(qt), _ptr(scale_t), ld_qt, _stream(stream, x, q, qt)), "swz_quant_f8")
 
@@ -367,6 +398,9 @@ def swz_gemm_f8(a, scale_a, b, scale_b, c, m: int, n: int, k: int, lda: Optional
     ldb = -(-k // 16) * 16 if ldb is None else ldb
     _buf("swz_gemm_f8", a=(a, m * lda), scale_a=(scale_a, _f8_scale_bytes(m, k, a_block, scale_type)), b=(b, n * ldb),
          scale_b=(scale_b, _f8_scale_bytes(n, k, b_block, scale_type)), c=(c, (2 if c_type == C_BF16 else 4) * m * n))
+    sc = _SCALE.get(scale_type)
+    _typed("swz_gemm_f8", a=(a, _F8.get(a_type)), scale_a=(scale_a, sc), b=(b, _F8.get(b_type)), scale_b=(scale_b, sc),
+           c=(c, _C.get(c_type)))
     _check(lib.swz_gemm_f8(_ptr(a), _ptr(scale_a), _ptr(b), _ptr(scale_b), _ptr(c), m, n, k, lda, ldb, a_type, b_type,
                            a_block, b_block, scale_type, c_type, _stream(stream, a, b, c)), "swz_gemm_f8")
 
@@ -383,19 +417,13 @@ def _ws_bytes(ws, need: int) -> int:
     return need if ws is None or isinstance(ws, int) else ws.numel() * ws.element_size()
 
 
-def _typed(call: str, **bufs) -> None:
-    """Raise ValueError for a tensor whose element size is not the one the call reads (name=(tensor, bytes per element))."""
-    for name, (t, size) in bufs.items():
-        if t is not None and not isinstance(t, int) and t.element_size() != size:
-            raise ValueError(f"{call}: {name} has {t.element_size()}-byte elements, the call reads {size}-byte ones")
-
-
 def swz_linear_ce(h, w, target, loss, lse, zt, n: int, v: int, k: int, ws, x_type: int = X_BF16, stream=None) -> None:
     """loss[i] = lse[i] - zt[i] of the logits h w^T, which are not kept (target: int64)."""
     need = swz_linear_loss_workspace(n, v, k)
     _buf("swz_linear_ce", h=(h, 2 * n * k), w=(w, 2 * v * k), target=(target, 8 * n), loss=(loss, 4 * n), lse=(lse, 4 * n),
          zt=(zt, 4 * n), ws=(ws, need))
-    _typed("swz_linear_ce", h=(h, 2), w=(w, 2), target=(target, 8))
+    xt = _X.get(x_type)
+    _typed("swz_linear_ce", h=(h, xt), w=(w, xt), target=(target, _INDEX), loss=(loss, _FLOAT), lse=(lse, _FLOAT), zt=(zt, _FLOAT))
     _check(lib.swz_linear_ce(_ptr(h), _ptr(w), x_type, _ptr(target), _ptr(loss), _ptr(lse), _ptr(zt), n, v, k, _ptr(ws),
                              _ws_bytes(ws, need), _stream(stream, h, w)), "swz_linear_ce")
 
@@ -406,7 +434,9 @@ def swz_linear_ce_grad(h, w, target, lse, zt, upstream, dh, dw, n: int, v: int, 
     need = swz_linear_loss_workspace(n, v, k, grad=True)
     _buf("swz_linear_ce_grad", h=(h, 2 * n * k), w=(w, 2 * v * k), target=(target, 8 * n), lse=(lse, 4 * n), zt=(zt, 4 * n),
          upstream=(upstream, 4 * n), dh=(dh, 2 * n * k), dw=(dw, 2 * v * k), ws=(ws, need))
-    _typed("swz_linear_ce_grad", h=(h, 2), w=(w, 2), target=(target, 8), dh=(dh, 2), dw=(dw, 2))
+    xt = _X.get(x_type)
+    _typed("swz_linear_ce_grad", h=(h, xt), w=(w, xt), target=(target, _INDEX), lse=(lse, _FLOAT), zt=(zt, _FLOAT),
+           upstream=(upstream, _FLOAT), dh=(dh, xt), dw=(dw, xt))
     _check(lib.swz_linear_ce_grad(_ptr(h), _ptr(w), x_type, _ptr(target), _ptr(lse), _ptr(zt), _ptr(upstream), _ptr(dh),
                                   _ptr(dw), n, v, k, _ptr(ws), _ws_bytes(ws, need), _stream(stream, h, w)),
            "swz_linear_ce_grad")
@@ -418,7 +448,9 @@ def swz_linear_distill(h, w, index, teacher, loss, lse, zt, n: int, v: int, k: i
     need = swz_linear_loss_workspace(n, v, k, top)
     _buf("swz_linear_distill", h=(h, 2 * n * k), w=(w, 2 * v * k), index=(index, 8 * n * top), teacher=(teacher, 4 * n * top),
          loss=(loss, 4 * n), lse=(lse, 4 * n), zt=(zt, 4 * n * top), ws=(ws, need))
-    _typed("swz_linear_distill", h=(h, 2), w=(w, 2), index=(index, 8), teacher=(teacher, 4))
+    xt = _X.get(x_type)
+    _typed("swz_linear_distill", h=(h, xt), w=(w, xt), index=(index, _INDEX), teacher=(teacher, _FLOAT), loss=(loss, _FLOAT),
+           lse=(lse, _FLOAT), zt=(zt, _FLOAT))
     _check(lib.swz_linear_distill(_ptr(h), _ptr(w), x_type, _ptr(index), _ptr(teacher), top, tau, _ptr(loss), _ptr(lse),
                                   _ptr(zt), n, v, k, _ptr(ws), _ws_bytes(ws, need), _stream(stream, h, w)),
            "swz_linear_distill")
@@ -431,7 +463,9 @@ def swz_linear_distill_grad(h, w, index, teacher, lse, zt, upstream, dh, dw, n: 
     _buf("swz_linear_distill_grad", h=(h, 2 * n * k), w=(w, 2 * v * k), index=(index, 8 * n * top),
          teacher=(teacher, 4 * n * top), lse=(lse, 4 * n), zt=(zt, 4 * n * top), upstream=(upstream, 4 * n),
          dh=(dh, 2 * n * k), dw=(dw, 2 * v * k), ws=(ws, need))
-    _typed("swz_linear_distill_grad", h=(h, 2), w=(w, 2), index=(index, 8), teacher=(teacher, 4), dh=(dh, 2), dw=(dw, 2))
+    xt = _X.get(x_type)
+    _typed("swz_linear_distill_grad", h=(h, xt), w=(w, xt), index=(index, _INDEX), teacher=(teacher, _FLOAT), lse=(lse, _FLOAT),
+           zt=(zt, _FLOAT), upstream=(upstream, _FLOAT), dh=(dh, xt), dw=(dw, xt))
     _check(lib.swz_linear_distill_grad(_ptr(h), _ptr(w), x_type, _ptr(index), _ptr(teacher), top, tau, _ptr(lse), _ptr(zt),
                                        _ptr(upstream), _ptr(dh), _ptr(dw), n, v, k, _ptr(ws), _ws_bytes(ws, need),
                                        _stream(stream, h, w)), "swz_linear_distill_grad")
