@@ -452,7 +452,8 @@ enum swz_scale_type { SWZ_SCALE_F32 = 0, SWZ_SCALE_E8M0 = 1 };
 
 /* A matrix to 8-bit floating point with a power-of-two scale per block, and
  * on request its transpose, which the gradient products contract over.
- *   d_x       : x_type [rows][ld_x], ld_x >= cols elements.
+ *   d_x       : x_type [rows][ld_x], ld_x >= cols elements; the last row ends
+ *               behind its cols, here and below (columns of a wider matrix).
  *   d_q       : 8-bit [rows][ld_q]; columns cols .. ld_q - 1 stay as they were.
  *   d_scale   : SWZ_BLOCK_1X128   [rows][ceil(cols / 128)],
  *               SWZ_BLOCK_128X128 [ceil(rows / 128)][ceil(cols / 128)].
@@ -479,7 +480,8 @@ int swz_quant_f8(const void* d_x, int32_t x_type, int64_t rows, int64_t cols, in
  *   C[i][j] = sum over blocks b of sA[i][b] sB[j][b] sum over k in b of A[i][k] B[j][k].
  *   d_a       : a_type [m][lda]; d_b : b_type [n][ldb]; lda, ldb >= k bytes,
  *               multiples of 16 and below 2^23; bytes behind column k are not
- *               used, whatever they hold.
+ *               used, whatever they hold, and the last row ends behind k rounded
+ *               up to 16 (a part of k of a wider operand is one too).
  *   d_scale_a : scale_type, laid out as swz_quant_f8 writes it for a_block;
  *   d_scale_b : the same for b_block.
  *   d_c       : float or bf16 (c_type, enum swz_c_type) [m][n], written

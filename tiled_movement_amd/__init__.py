@@ -368,6 +368,11 @@ def _typed(call: str, **bufs) -> None:
             _TYPES_SEEN.add((dtype, kind))
 
 
+def _span(rows: int, cols: int, ld: int) -> int:
+    """Elements from the first of [rows][ld] to the last row's last of `cols`."""
+    return (rows - 1) * ld + cols if rows > 0 and cols > 0 else 0
+
+
 def _f8_scale_bytes(rows: int, cols: int, block: int, scale_type: int) -> int:
     return (-(-rows // 128) if block == BLOCK_128X128 else rows) * -(-cols // 128) * (1 if scale_type == SCALE_E8M0 else 4)
 
@@ -381,8 +386,8 @@ def swz_quant_f8(x, q, scale, rows: int, cols: int, x_type: int = X_BF16, f8_typ
     ld_x = cols if ld_x is None else ld_x
     ld_q = -(-cols // 16) * 16 if ld_q is None else ld_q
     ld_qt = -(-rows // 16) * 16 if ld_qt is None else ld_qt
-    _buf("swz_quant_f8", x=(x, rows * ld_x * (4 if x_type == X_F32 else 2)), q=(q, rows * ld_q),
-         scale=(scale, _f8_scale_bytes(rows, cols, block, scale_type)), qt=(qt, cols * ld_qt),
+    _buf("swz_quant_f8", x=(x, _span(rows, cols, ld_x) * (4 if x_type == X_F32 else 2)), q=(q, _span(rows, cols, ld_q)),
+         scale=(scale, _f8_scale_bytes(rows, cols, block, scale_type)), qt=(qt, _span(cols, rows, ld_qt)),
          scale_t=(scale_t, _f8_scale_bytes(cols, rows, block, scale_type)))
     f8, sc = _F8.get(f8_type), _SCALE.get(scale_type)
     _typed("swz_quant_f8", x=(x, _X.get(x_type)), q=(q, f8), scale=(scale, sc), qt=(qt, f8), scale_t=(scale_t, sc))
@@ -396,7 +401,8 @@ def swz_gemm_f8(a, scale_a, b, scale_b, c, m: int, n: int, k: int, lda: Optional
     """C [m][n] = A B^T of 8-bit operands with scales (pitches default to k rounded up to 16 bytes)."""
     lda = -(-k // 16) * 16 if lda is None else lda
     ldb = -(-k // 16) * 16 if ldb is None else ldb
-    _buf("swz_gemm_f8", a=(a, m * lda), scale_a=(scale_a, _f8_scale_bytes(m, k, a_block, scale_type)), b=(b, n * ldb),
+    k16 = -(-k // 16) * 16
+    _buf("swz_gemm_f8", a=(a, _span(m, k16, lda)), scale_a=(scale_a, _f8_scale_bytes(m, k, a_block, scale_type)), b=(b, _span(n, k16, ldb)),
          scale_b=(scale_b, _f8_scale_bytes(n, k, b_block, scale_type)), c=(c, (2 if c_type == C_BF16 else 4) * m * n))
     sc = _SCALE.get(scale_type)
     _typed("swz_gemm_f8", a=(a, _F8.get(a_type)), scale_a=(scale_a, sc), b=(b, _F8.get(b_type)), scale_b=(scale_b, sc),

@@ -39,12 +39,23 @@ int hip_status(hipError_t e) { return e == hipSuccess ? SWZ_OK : SWZ_EHIP; }
 // the rows of a tile lie within 31-bit offsets (mma_core.h).
 constexpr int64_t kMaxPitch = int64_t(1) << 23;
 
-// Bytes of an 8-bit operand [rows][ld] and of its scales.
-bool f8_operand_bytes(int64_t rows, int64_t cols, int64_t ld, bool square, int32_t scale_type, int64_t* data,
+// Elements from the first of [rows][ld] to the last of `cols` used in the last
+// row: what lies behind them is not the matrix's (it may be a part of a wider
+// one).  False where rows ld leaves 64 bits; ld >= cols >= 0.
+bool span_elems(int64_t rows, int64_t cols, int64_t ld, int64_t* elems) {
+    if (!mul_ok(rows, ld, elems)) return false;
+    *elems = rows && cols ? *elems - ld + cols : 0;
+    return true;
+}
+
+// Bytes of an 8-bit operand [rows][ld], of which rows use `used` bytes, and of
+// its scales.
+bool f8_operand_bytes(int64_t rows, int64_t cols, int64_t used, int64_t ld, bool square, int32_t scale_type, int64_t* data,
                       int64_t* scales) {
     int64_t n;
     const int64_t srows = square ? rows / 128 + (rows % 128 != 0) : rows, scols = cols / 128 + (cols % 128 != 0);
-    return mul_ok(rows, ld, data) && mul_ok(srows, scols, &n) && mul_ok(n, scale_type == SWZ_SCALE_F32 ? 4 : 1, scales);
+    return span_elems(rows, used, ld, data) && mul_ok(srows, scols, &n) &&
+           mul_ok(n, scale_type == SWZ_SCALE_F32 ? 4 : 1, scales);
 }
 
 // Sizes of an output-layer loss that the kernels' grids and offsets take:
@@ -704,15 +715,15 @@ SWZ_API int swz_quant_f8(const void* d_x, int32_t x_type, int64_t rows, int64_t 
     const int64_t esz = x_type == SWZ_X_F32 ? 4 : 2;
     const bool square = block == SWZ_BLOCK_128X128;
     int64_t n, x_bytes, q_bytes = 0, s_bytes = 0, qt_bytes = 0, st_bytes = 0;
-    if (!mul_ok(rows, ld_x, &n) || !mul_ok(n, esz, &x_bytes)) return SWZ_EINVAL;
+    if (!span_elems(rows, cols, ld_x, &n) || !mul_ok(n, esz, &x_bytes)) return SWZ_EINVAL;
     if (d_q) {
-        if (!d_scale || ld_q < cols || ld_q % 16 || !f8_operand_bytes(rows, cols, ld_q, square, scale_type, &q_bytes, &s_bytes))
+        if (!d_scale || ld_q < cols || ld_q % 16 || !f8_operand_bytes(rows, cols, cols, ld_q, square, scale_type, &q_bytes, &s_bytes))
             return SWZ_EINVAL;
         if (reinterpret_cast<uintptr_t>(d_q) % 16) return SWZ_EINVAL;
     }
     if (d_qt) {
         if (!d_scale_t || ld_qt < rows || ld_qt % 16 ||
-            !f8_operand_bytes(cols, rows, ld_qt, square, scale_type, &qt_bytes, &st_bytes))
+            !f8_operand_bytes(cols, rows, rows, ld_qt, square, scale_type, &qt_bytes, &st_bytes))
             return SWZ_EINVAL;
         if (reinterpret_cast<uintptr_t>(d_qt) % 16) return SWZ_EINVAL;
     }
@@ -747,8 +758,9 @@ SWZ_API int swz_gemm_f8(const void* d_a, const void* d_scale_a, const void* d_b,
     const bool sqa = a_block == SWZ_BLOCK_128X128, sqb = b_block == SWZ_BLOCK_128X128;
     const int64_t esz = c_type == SWZ_C_BF16 ? 2 : 4;
     int64_t a_bytes, sa_bytes, b_bytes, sb_bytes, c_elems, c_bytes;
-    if (!f8_operand_bytes(m, k, lda, sqa, scale_type, &a_bytes, &sa_bytes) ||
-        !f8_operand_bytes(n, k, ldb, sqb, scale_type, &b_bytes, &sb_bytes) || !mul_ok(m, n, &c_elems) ||
+    const int64_t k16 = k + (16 - k % 16) % 16;  // rows are read in pieces of 16 bytes; k <= lda, a multiple of 16
+    if (!f8_operand_bytes(m, k, k16, lda, sqa, scale_type, &a_bytes, &sa_bytes) ||
+        !f8_operand_bytes(n, k, k16, ldb, sqb, scale_type, &b_bytes, &sb_bytes) || !mul_ok(m, n, &c_elems) ||
         !mul_ok(c_elems, esz, &c_bytes))
         return SWZ_EINVAL;
     if (m == 0 || n == 0) return SWZ_OK;
