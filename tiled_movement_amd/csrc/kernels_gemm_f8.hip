@@ -60,26 +60,16 @@ hipError_t launch_tiles(const GemmF8Job& j, bool by_xcd, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Tile by the number of workgroups it leaves, 256 being one a compute unit.
-// A stage costs a workgroup at least its barrier, loads and fragment reads,
-// some 0.3 us for 64 x 64 and 0.8 us for 128 x 128, however few workgroups
-// run; so small tiles where all of them run at once (m x 4096 x 4096: m = 128,
-// 64 x 64 tiles 12 us, 64 x 128 16, 128 x 128 23, 256 x 256 45; m = 512: 16,
-// 17, 24, 48; 256 x 8192 x 8192: 43, 35, 46, 114), and 256 x 256, which reads
-// the least per product, where there is work for all units anyway (m = 2048:
-// 62, 61, 47, 49).  In the small grids the workgroups of an XCD take
-// neighbouring tiles, which share B's rows in its cache (512 x 8192 x 8192,
-// 128 x 128 tiles: 73 -> 47 us); 256 x 256 tiles lose by it (8192 x 8192 x
-// 4096: 237 -> 267 us).
 // fp32 scales of both operands' rows on widened operands need more registers
 // than a 64 x 128 wave tile leaves (145 spilled): half the rows.
 template <int ELEM, int LT, int RT, int SC, class CT>
 hipError_t launch_sized(const GemmF8Job& j, hipStream_t stream) {
-    auto tiles = [&](int64_t tm, int64_t tn) { return ((j.m + tm - 1) / tm) * ((j.n + tn - 1) / tn); };
-    if (tiles(64, 64) <= 256) return launch_tiles<Config<ELEM, LT, RT, SC, 2, 2, 2, 2>, CT>(j, true, stream);
-    if (tiles(64, 128) <= 256) return launch_tiles<Config<ELEM, LT, RT, SC, 2, 4, 2, 2>, CT>(j, true, stream);
-    if (tiles(128, 128) <= 256) return launch_tiles<Config<ELEM, LT, RT, SC, 2, 4, 4, 2>, CT>(j, true, stream);
-    return launch_tiles<Config<ELEM, LT, RT, SC, 4, 2, ELEM == kF8Wide && SC == kF32Rows ? 2 : 4, 8>, CT>(j, false, stream);
+    switch (gemm_f8_tile(j.m, j.n)) {
+        case GemmF8Tile::k64x64: return launch_tiles<Config<ELEM, LT, RT, SC, 2, 2, 2, 2>, CT>(j, true, stream);
+        case GemmF8Tile::k64x128: return launch_tiles<Config<ELEM, LT, RT, SC, 2, 4, 2, 2>, CT>(j, true, stream);
+        case GemmF8Tile::k128x128: return launch_tiles<Config<ELEM, LT, RT, SC, 2, 4, 4, 2>, CT>(j, true, stream);
+        default: return launch_tiles<Config<ELEM, LT, RT, SC, 4, 2, ELEM == kF8Wide && SC == kF32Rows ? 2 : 4, 8>, CT>(j, false, stream);
+    }
 }
 
 // A bf16 result takes the one-byte instruction, whose dropped bits are a

@@ -83,6 +83,25 @@ struct GemmF8Job {
 hipError_t launch_gemm_f8(const GemmF8Job& job, hipStream_t stream);
 hipError_t launch_gemm_f8_few(const GemmF8Job& job, hipStream_t stream);  // m <= kFewRows
 constexpr int64_t kFewRows = 16;
+// Tile of swz_gemm_f8 by the number of workgroups it leaves, 256 being one a compute unit.
+// A stage costs a workgroup at least its barrier, loads and fragment reads,
+// some 0.3 us for 64 x 64 and 0.8 us for 128 x 128, however few workgroups
+// run; so small tiles where all of them run at once (m x 4096 x 4096: m = 128,
+// 64 x 64 tiles 12 us, 64 x 128 16, 128 x 128 23, 256 x 256 45; m = 512: 16,
+// 17, 24, 48; 256 x 8192 x 8192: 43, 35, 46, 114), and 256 x 256, which reads
+// the least per product, where there is work for all units anyway (m = 2048:
+// 62, 61, 47, 49).  In the small grids the workgroups of an XCD take
+// neighbouring tiles, which share B's rows in its cache (512 x 8192 x 8192,
+// 128 x 128 tiles: 73 -> 47 us); 256 x 256 tiles lose by it (8192 x 8192 x
+// 4096: 237 -> 267 us).
+enum class GemmF8Tile { k64x64, k64x128, k128x128, k256x256 };
+inline GemmF8Tile gemm_f8_tile(int64_t m, int64_t n) {
+    auto tiles = [&](int64_t rows, int64_t cols) { return ((m + rows - 1) / rows) * ((n + cols - 1) / cols); };
+    if (tiles(64, 64) <= 256) return GemmF8Tile::k64x64;
+    if (tiles(64, 128) <= 256) return GemmF8Tile::k64x128;
+    if (tiles(128, 128) <= 256) return GemmF8Tile::k128x128;
+    return GemmF8Tile::k256x256;
+}
 
 // swz_linear_ce, swz_linear_distill and their gradients.  teacher ==
 // nullptr: cross entropy (top 1, tau 1).
