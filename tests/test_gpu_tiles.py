@@ -93,3 +93,19 @@ def test_losses_in_every_tile(shape, top, tau, dt):
     c.backward(d)
     torch.cuda.synchronize()
     check_rows(c, d)
+
+
+@pytest.mark.parametrize("ea,eb", [(1, 200), (253, 60), (30, 200), (0, 254), (127, 127), (254, 4)])
+@pytest.mark.parametrize("m,n", [(90, 140), (2100, 2200)])
+def test_gemm_far_scales_with_a_rounded_result(m, n, ea, eb):
+    """E8M0 scales at the ends of their range, through the 8-bit instruction: exact up to the one rounding to bf16."""
+    announce("gemm far scales, bf16", m, n, ea, eb)
+    k = 256
+    a, b = operand(m, k, "e4m3", False, T.SCALE_E8M0, 13), operand(n, k, "e4m3", True, T.SCALE_E8M0, 14)
+    va, vb = (t[0][:, :k].view(torch.float8_e4m3fn).double() for t in (a, b))
+    a[1].fill_(ea)
+    b[1].fill_(eb)
+    ref = (va @ vb.t()) * 2.0 ** (ea + eb - 254)
+    c = torch.full((m, n), float("nan"), dtype=torch.bfloat16, device=DEV)
+    T.swz_gemm_f8(a[0], a[1], b[0], b[1], c, m, n, k, lda=a[0].shape[1], ldb=b[0].shape[1])
+    assert torch.equal(c, ref.to(torch.bfloat16))
