@@ -500,7 +500,8 @@ int swz_quant_f8(const void* d_x, int32_t x_type, int64_t rows, int64_t cols, in
  * dropping what lies more than 13 bits below the largest of them (1.5e-5 of
  * the norm of a product of normal operands, a hundredth of the rounding to
  * bf16), sums those in fp32 and is rounded once, to nearest even.  fp32 scales
- * multiply fp32 sums within their block.
+ * multiply fp32 sums within their block, by the product of a block's two
+ * scales, which has to be a normal fp32 number.
  * NaN and infinities in the used elements and scales propagate.
  * Errors: SWZ_EINVAL (sizes, pitches, alignment, NULL, overlap, enum values),
  * SWZ_EUNSUPPORTED (lda or ldb of 2^23 and more; n of 2^26 and more; over 2^22
@@ -514,7 +515,13 @@ int swz_gemm_f8(const void* d_a, const void* d_scale_a, const void* d_b, const v
  * the forward calls; 1, enough for the forward and the gradient calls.  A
  * workspace is 256-byte aligned device memory that carries nothing from one
  * call to the next; calls that may run at the same time (on two streams, in
- * two graphs) need one each.
+ * two graphs) need one each.  The forward calls take 8 bytes a row and 256
+ * words, a 64th of bf16 logits.  The gradient calls hold dz of a piece of up
+ * to 32768 words twice, that piece of W once and H once (2 bytes each), and
+ * dH's sums (4 bytes, up to 32 times where there are few rows): less than bf16
+ * logits where the vocabulary is many pieces long (4096 x 262144 x 4096: 906 MB,
+ * logits 2147), more where it is not or the rows are few (4096 x 65536 x 4096:
+ * 906 and 537; 64 x 128256 x 4096: 290 and 16).
  * Errors: SWZ_EINVAL, SWZ_EUNSUPPORTED (sizes, as the calls). */
 int swz_linear_loss_workspace(int64_t n, int64_t v, int64_t k, int32_t top, int32_t grad, int64_t* bytes);
 

@@ -35,10 +35,6 @@ bool pitch16(int64_t n, int32_t esz) { return (static_cast<uint64_t>(n) * static
 
 int hip_status(hipError_t e) { return e == hipSuccess ? SWZ_OK : SWZ_EHIP; }
 
-// Row pitches of the products' operands stay below this many bytes, so that
-// the rows of a tile lie within 31-bit offsets (mma_core.h).
-constexpr int64_t kMaxPitch = int64_t(1) << 23;
-
 // Elements from the first of [rows][ld] to the last of `cols` used in the last
 // row: what lies behind them is not the matrix's (it may be a part of a wider
 // one).  False where rows ld leaves 64 bits; ld >= cols >= 0.
@@ -63,7 +59,7 @@ bool f8_operand_bytes(int64_t rows, int64_t cols, int64_t used, int64_t ld, bool
 // product.
 int check_loss_sizes(int64_t n, int64_t v, int64_t k, int32_t top) {
     if (n < 0 || v < 1 || k < 8 || k % 8 || top < 1) return SWZ_EINVAL;
-    if (top > swz::kMaxTop || k >= kMaxPitch / 2 || n >= kMaxPitch / 2 - 8 || v >= int64_t(1) << 31) return SWZ_EUNSUPPORTED;
+    if (top > swz::kMaxTop || k >= swz::kMaxPitch / 2 || n >= swz::kMaxPitch / 2 - 8 || v >= int64_t(1) << 31) return SWZ_EUNSUPPORTED;
     if ((n / 256 + 1) * (v / 256 + 1) > int64_t(1) << 22) return SWZ_EUNSUPPORTED;  // tiles of one launch
     return SWZ_OK;
 }
@@ -775,7 +771,7 @@ SWZ_API int swz_gemm_f8(const void* d_a, const void* d_scale_a, const void* d_b,
             overlaps(d_c, c_bytes, d_scale_a, sa_bytes) || overlaps(d_c, c_bytes, d_scale_b, sb_bytes))
             return SWZ_EINVAL;
     }
-    if (lda >= kMaxPitch || ldb >= kMaxPitch) return SWZ_EUNSUPPORTED;
+    if (lda >= swz::kMaxPitch || ldb >= swz::kMaxPitch) return SWZ_EUNSUPPORTED;
     if (n >= int64_t(1) << 26 || (m - 1) / 256 + 1 > ((int64_t(1) << 22) - 1) / ((n - 1) / 256 + 1)) return SWZ_EUNSUPPORTED;
     const swz::GemmF8Job job{d_a, d_scale_a, d_b, d_scale_b, d_c, m, n, k, lda, ldb, a_type == SWZ_F8_E5M2,
                              b_type == SWZ_F8_E5M2, sqa, sqb, scale_type == SWZ_SCALE_E8M0, c_type == SWZ_C_BF16};

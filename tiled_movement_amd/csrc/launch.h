@@ -73,6 +73,10 @@ struct QuantJob {
 };
 hipError_t launch_quant(const QuantJob& job, hipStream_t stream);
 
+// Row pitches of the products' operands stay below this many bytes, so that
+// the 256 rows of a tile lie within 31-bit offsets from its first (mma_core.h).
+constexpr int64_t kMaxPitch = int64_t(1) << 23;
+
 // swz_gemm_f8: C [m][n] = A B^T of 8-bit operands with scales.
 struct GemmF8Job {
     const void *a, *scale_a, *b, *scale_b;

@@ -49,7 +49,6 @@ typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
 // keep about 13 bits below it: 1.5e-5 of the result's norm on normal
 // operands (16x16x32 and 16x16x128 alike), against 4e-8 for bf16.
 enum Elem { kBf16, kF16, kF8, kF8Wide };
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 // Scales of one-byte operands, one per row (or 128 rows) and stage: none;
 // powers of two as exponent bytes, applied by the matrix instruction; fp32,
 // applied to the stage's product (kF32Square: R's scale is the same for all
@@ -58,14 +57,12 @@ enum Scale { kNoScale, kE8M0, kF32Rows, kF32Square };
 
 struct Operand {
     const uint8_t* data;  // [rows][ld] bytes
-    int64_t ld;           // row pitch in bytes, a multiple of 16, below kMaxLd
+    int64_t ld;           // row pitch in bytes, a multiple of 16, below kMaxPitch
     int64_t rows;
     const void* scale;    // [rows >> scale_shift][scale_ld]
     int64_t scale_ld;
     int scale_shift;      // 0: a scale per row, 7: per 128 rows
 };
-// 256 rows of this pitch stay within 31-bit offsets from a tile's first row.
-constexpr int64_t kMaxLd = int64_t(1) << 23;
 
 template <int ELEM_, int LT_, int RT_, int SC_, int WL_, int WR_, int BL_, int BR_>
 struct Config {
