@@ -195,11 +195,13 @@ def _ptr(x) -> Optional[int]:
 def _buf(call: str, **bufs) -> None:
     """Check the device buffers of one call before it reaches the library:
     every tensor is a contiguous CUDA tensor, all on the current device, and
-    holds at least the bytes the call reads or writes there (name=(tensor, bytes)).
+    holds at least the bytes the call reads or writes there, in elements of the
+    type it reads (name=(tensor, bytes) or name=(tensor, bytes, type)).
     Raw integer addresses and None pass unchecked (the library checks what
     it can: NULL, alignment, overlap).  Raises ValueError."""
-    device = None
-    for name, (t, need) in bufs.items():
+    device, other = None, None
+    for name, spec in bufs.items():
+        t = spec[0]
         if t is None or isinstance(t, int):
             continue
         if not getattr(t, "is_cuda", False):
@@ -207,13 +209,19 @@ def _buf(call: str, **bufs) -> None:
                              f"{getattr(t, 'device', 'the host')})")
         if not t.is_contiguous():
             raise ValueError(f"{call}: {name} must be contiguous (a strided view is not its own bytes)")
+        here = t.device
         if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{call}: {name} is on {t.device}, the other buffers on {device}")
+            device = here
+        elif here != device:
+            raise ValueError(f"{call}: {name} is on {here}, the other buffers on {device}")
         have = t.numel() * t.element_size()
-        if have < max(int(need), 0):
-            raise ValueError(f"{call}: {name} holds {have} bytes, the call needs {int(need)}")
+        if have < spec[1]:
+            raise ValueError(f"{call}: {name} holds {have} bytes, the call needs {int(spec[1])}")
+        if len(spec) == 3 and spec[2] is not None and getattr(t, "dtype", None) not in spec[2].seen:
+            other = other or []
+            other.append((name, t, spec[2]))
+    for name, t, kind in other or ():
+        kind.check(call, name, t)
     if device is not None and device.index is not None:
         import torch
 
@@ -339,33 +347,31 @@ def swz_gemm_ex(a, bt, c, m: int, n: int, k: int, layout: str = "swizzle", param
                            _stream(stream, a, bt, c)), "swz_gemm_ex")
 
 
-# What the calls below read, by their enums: (bytes per element, torch type).
-_X = {X_BF16: (2, "bfloat16"), X_F16: (2, "float16"), X_F32: (4, "float32")}
-_F8 = {F8_E4M3: (1, "float8_e4m3fn"), F8_E5M2: (1, "float8_e5m2")}
-_SCALE = {SCALE_F32: (4, "float32"), SCALE_E8M0: (1, "float8_e8m0fnu")}
-_C = {C_F32: (4, "float32"), C_BF16: (2, "bfloat16")}
-_FLOAT, _INDEX = (4, "float32"), (8, "int64")
-_TYPES_SEEN = set()  # (torch type, what the call reads) that fit: looked up instead of compared, a call's own time counts
+class _Type:
+    """An element type that a call reads.  Whole numbers of its size pass as its raw bits."""
 
+    def __init__(self, size: int, name: str):
+        self.size, self.name = size, name
+        self.seen = set()  # torch types found right: a call's own time counts
 
-def _typed(call: str, **bufs) -> None:
-    """Raise ValueError for a tensor that is not of the type the call reads (name=(tensor, (bytes per element, type))).
-
-    Whole numbers of the element's size pass as its raw bits.  An enum that the library does not know leaves its
-    buffers to the library, which refuses it."""
-    for name, (t, kind) in bufs.items():
-        if t is None or kind is None or isinstance(t, int):
-            continue
+    def check(self, call: str, name: str, t) -> None:
+        if t.element_size() != self.size:
+            raise ValueError(f"{call}: {name} has {t.element_size()}-byte elements, the call reads {self.size}-byte ones")
         dtype = getattr(t, "dtype", None)
-        if (dtype, kind) in _TYPES_SEEN:
-            continue
-        size, want = kind
-        if t.element_size() != size:
-            raise ValueError(f"{call}: {name} has {t.element_size()}-byte elements, the call reads {size}-byte ones")
-        if dtype is not None:
-            if (dtype.is_floating_point or dtype.is_complex) and str(dtype) != f"torch.{want}":
-                raise ValueError(f"{call}: {name} holds {dtype}, the call reads {want}")
-            _TYPES_SEEN.add((dtype, kind))
+        if dtype is None:
+            return
+        if (dtype.is_floating_point or dtype.is_complex) and str(dtype) != f"torch.{self.name}":
+            raise ValueError(f"{call}: {name} holds {dtype}, the call reads {self.name}")
+        self.seen.add(dtype)
+
+
+# By the calls' enums; a value that the library does not know leaves its
+# buffers to the library, which refuses it.
+_FLOAT, _BF16, _BYTE_SCALE, _INDEX = _Type(4, "float32"), _Type(2, "bfloat16"), _Type(1, "float8_e8m0fnu"), _Type(8, "int64")
+_X = {X_BF16: _BF16, X_F16: _Type(2, "float16"), X_F32: _FLOAT}
+_F8 = {F8_E4M3: _Type(1, "float8_e4m3fn"), F8_E5M2: _Type(1, "float8_e5m2")}
+_SCALE = {SCALE_F32: _FLOAT, SCALE_E8M0: _BYTE_SCALE}
+_C = {C_F32: _FLOAT, C_BF16: _BF16}
 
 
 def _span(rows: int, cols: int, ld: int) -> int:
@@ -386,11 +392,10 @@ def swz_quant_f8(x, q, scale, rows: int, cols: int, x_type: int = X_BF16, f8_typ
     ld_x = cols if ld_x is None else ld_x
     ld_q = -(-cols // 16) * 16 if ld_q is None else ld_q
     ld_qt = -(-rows // 16) * 16 if ld_qt is None else ld_qt
-    _buf("swz_quant_f8", x=(x, _span(rows, cols, ld_x) * (4 if x_type == X_F32 else 2)), q=(q, _span(rows, cols, ld_q)),
-         scale=(scale, _f8_scale_bytes(rows, cols, block, scale_type)), qt=(qt, _span(cols, rows, ld_qt)),
-         scale_t=(scale_t, _f8_scale_bytes(cols, rows, block, scale_type)))
     f8, sc = _F8.get(f8_type), _SCALE.get(scale_type)
-    _typed("swz_quant_f8", x=(x, _X.get(x_type)), q=(q, f8), scale=(scale, sc), qt=(qt, f8), scale_t=(scale_t, sc))
+    _buf("swz_quant_f8", x=(x, _span(rows, cols, ld_x) * (4 if x_type == X_F32 else 2), _X.get(x_type)),
+         q=(q, _span(rows, cols, ld_q), f8), scale=(scale, _f8_scale_bytes(rows, cols, block, scale_type), sc),
+         qt=(qt, _span(cols, rows, ld_qt), f8), scale_t=(scale_t, _f8_scale_bytes(cols, rows, block, scale_type), sc))
     _check(lib.swz_quant_f8(_ptr(x), x_type, rows, cols, ld_x, f8_type, block, scale_type, _ptr(q), _ptr(scale), ld_q,
                             _ptr(qt), _ptr(scale_t), ld_qt, _stream(stream, x, q, qt)), "swz_quant_f8")
 
@@ -401,12 +406,11 @@ def swz_gemm_f8(a, scale_a, b, scale_b, c, m: int, n: int, k: int, lda: Optional
     """C [m][n] = A B^T of 8-bit operands with scales (pitches default to k rounded up to 16 bytes)."""
     lda = -(-k // 16) * 16 if lda is None else lda
     ldb = -(-k // 16) * 16 if ldb is None else ldb
-    k16 = -(-k // 16) * 16
-    _buf("swz_gemm_f8", a=(a, _span(m, k16, lda)), scale_a=(scale_a, _f8_scale_bytes(m, k, a_block, scale_type)), b=(b, _span(n, k16, ldb)),
-         scale_b=(scale_b, _f8_scale_bytes(n, k, b_block, scale_type)), c=(c, (2 if c_type == C_BF16 else 4) * m * n))
-    sc = _SCALE.get(scale_type)
-    _typed("swz_gemm_f8", a=(a, _F8.get(a_type)), scale_a=(scale_a, sc), b=(b, _F8.get(b_type)), scale_b=(scale_b, sc),
-           c=(c, _C.get(c_type)))
+    k16, sc = -(-k // 16) * 16, _SCALE.get(scale_type)
+    _buf("swz_gemm_f8", a=(a, _span(m, k16, lda), _F8.get(a_type)),
+         scale_a=(scale_a, _f8_scale_bytes(m, k, a_block, scale_type), sc),
+         b=(b, _span(n, k16, ldb), _F8.get(b_type)), scale_b=(scale_b, _f8_scale_bytes(n, k, b_block, scale_type), sc),
+         c=(c, (2 if c_type == C_BF16 else 4) * m * n, _C.get(c_type)))
     _check(lib.swz_gemm_f8(_ptr(a), _ptr(scale_a), _ptr(b), _ptr(scale_b), _ptr(c), m, n, k, lda, ldb, a_type, b_type,
                            a_block, b_block, scale_type, c_type, _stream(stream, a, b, c)), "swz_gemm_f8")
 
@@ -426,10 +430,9 @@ def _ws_bytes(ws, need: int) -> int:
 def swz_linear_ce(h, w, target, loss, lse, zt, n: int, v: int, k: int, ws, x_type: int = X_BF16, stream=None) -> None:
     """loss[i] = lse[i] - zt[i] of the logits h w^T, which are not kept (target: int64)."""
     need = swz_linear_loss_workspace(n, v, k)
-    _buf("swz_linear_ce", h=(h, 2 * n * k), w=(w, 2 * v * k), target=(target, 8 * n), loss=(loss, 4 * n), lse=(lse, 4 * n),
-         zt=(zt, 4 * n), ws=(ws, need))
     xt = _X.get(x_type)
-    _typed("swz_linear_ce", h=(h, xt), w=(w, xt), target=(target, _INDEX), loss=(loss, _FLOAT), lse=(lse, _FLOAT), zt=(zt, _FLOAT))
+    _buf("swz_linear_ce", h=(h, 2 * n * k, xt), w=(w, 2 * v * k, xt), target=(target, 8 * n, _INDEX),
+         loss=(loss, 4 * n, _FLOAT), lse=(lse, 4 * n, _FLOAT), zt=(zt, 4 * n, _FLOAT), ws=(ws, need))
     _check(lib.swz_linear_ce(_ptr(h), _ptr(w), x_type, _ptr(target), _ptr(loss), _ptr(lse), _ptr(zt), n, v, k, _ptr(ws),
                              _ws_bytes(ws, need), _stream(stream, h, w)), "swz_linear_ce")
 
@@ -438,11 +441,10 @@ def swz_linear_ce_grad(h, w, target, lse, zt, upstream, dh, dw, n: int, v: int, 
                        stream=None) -> None:
     """dh [n][k] and dw [v][k] of sum(upstream * loss); either may be None."""
     need = swz_linear_loss_workspace(n, v, k, grad=True)
-    _buf("swz_linear_ce_grad", h=(h, 2 * n * k), w=(w, 2 * v * k), target=(target, 8 * n), lse=(lse, 4 * n), zt=(zt, 4 * n),
-         upstream=(upstream, 4 * n), dh=(dh, 2 * n * k), dw=(dw, 2 * v * k), ws=(ws, need))
     xt = _X.get(x_type)
-    _typed("swz_linear_ce_grad", h=(h, xt), w=(w, xt), target=(target, _INDEX), lse=(lse, _FLOAT), zt=(zt, _FLOAT),
-           upstream=(upstream, _FLOAT), dh=(dh, xt), dw=(dw, xt))
+    _buf("swz_linear_ce_grad", h=(h, 2 * n * k, xt), w=(w, 2 * v * k, xt), target=(target, 8 * n, _INDEX),
+         lse=(lse, 4 * n, _FLOAT), zt=(zt, 4 * n, _FLOAT), upstream=(upstream, 4 * n, _FLOAT), dh=(dh, 2 * n * k, xt),
+         dw=(dw, 2 * v * k, xt), ws=(ws, need))
     _check(lib.swz_linear_ce_grad(_ptr(h), _ptr(w), x_type, _ptr(target), _ptr(lse), _ptr(zt), _ptr(upstream), _ptr(dh),
                                   _ptr(dw), n, v, k, _ptr(ws), _ws_bytes(ws, need), _stream(stream, h, w)),
            "swz_linear_ce_grad")
@@ -452,11 +454,10 @@ def swz_linear_distill(h, w, index, teacher, loss, lse, zt, n: int, v: int, k: i
                        x_type: int = X_BF16, stream=None) -> None:
     """tau^2 KL(teacher's top logits || softmax(h w^T / tau)) per row (index: int64 [n][top], teacher: fp32)."""
     need = swz_linear_loss_workspace(n, v, k, top)
-    _buf("swz_linear_distill", h=(h, 2 * n * k), w=(w, 2 * v * k), index=(index, 8 * n * top), teacher=(teacher, 4 * n * top),
-         loss=(loss, 4 * n), lse=(lse, 4 * n), zt=(zt, 4 * n * top), ws=(ws, need))
     xt = _X.get(x_type)
-    _typed("swz_linear_distill", h=(h, xt), w=(w, xt), index=(index, _INDEX), teacher=(teacher, _FLOAT), loss=(loss, _FLOAT),
-           lse=(lse, _FLOAT), zt=(zt, _FLOAT))
+    _buf("swz_linear_distill", h=(h, 2 * n * k, xt), w=(w, 2 * v * k, xt), index=(index, 8 * n * top, _INDEX),
+         teacher=(teacher, 4 * n * top, _FLOAT), loss=(loss, 4 * n, _FLOAT), lse=(lse, 4 * n, _FLOAT),
+         zt=(zt, 4 * n * top, _FLOAT), ws=(ws, need))
     _check(lib.swz_linear_distill(_ptr(h), _ptr(w), x_type, _ptr(index), _ptr(teacher), top, tau, _ptr(loss), _ptr(lse),
                                   _ptr(zt), n, v, k, _ptr(ws), _ws_bytes(ws, need), _stream(stream, h, w)),
            "swz_linear_distill")
@@ -466,12 +467,10 @@ def swz_linear_distill_grad(h, w, index, teacher, lse, zt, upstream, dh, dw, n: 
                             ws, x_type: int = X_BF16, stream=None) -> None:
     """dh [n][k] and dw [v][k] of sum(upstream * loss); either may be None."""
     need = swz_linear_loss_workspace(n, v, k, top, grad=True)
-    _buf("swz_linear_distill_grad", h=(h, 2 * n * k), w=(w, 2 * v * k), index=(index, 8 * n * top),
-         teacher=(teacher, 4 * n * top), lse=(lse, 4 * n), zt=(zt, 4 * n * top), upstream=(upstream, 4 * n),
-         dh=(dh, 2 * n * k), dw=(dw, 2 * v * k), ws=(ws, need))
     xt = _X.get(x_type)
-    _typed("swz_linear_distill_grad", h=(h, xt), w=(w, xt), index=(index, _INDEX), teacher=(teacher, _FLOAT), lse=(lse, _FLOAT),
-           zt=(zt, _FLOAT), upstream=(upstream, _FLOAT), dh=(dh, xt), dw=(dw, xt))
+    _buf("swz_linear_distill_grad", h=(h, 2 * n * k, xt), w=(w, 2 * v * k, xt), index=(index, 8 * n * top, _INDEX),
+         teacher=(teacher, 4 * n * top, _FLOAT), lse=(lse, 4 * n, _FLOAT), zt=(zt, 4 * n * top, _FLOAT),
+         upstream=(upstream, 4 * n, _FLOAT), dh=(dh, 2 * n * k, xt), dw=(dw, 2 * v * k, xt), ws=(ws, need))
     _check(lib.swz_linear_distill_grad(_ptr(h), _ptr(w), x_type, _ptr(index), _ptr(teacher), top, tau, _ptr(lse), _ptr(zt),
                                        _ptr(upstream), _ptr(dh), _ptr(dw), n, v, k, _ptr(ws), _ws_bytes(ws, need),
                                        _stream(stream, h, w)), "swz_linear_distill_grad")
