@@ -496,15 +496,14 @@ __device__ __forceinline__ void stage_products(f32x4 (&acc)[C::BL][C::BR], const
 // reads its next fragments.  A stage is four quadrants of 2 x 4 blocks in the
 // order (L0 R0) (L1 R0) (L1 R1) (L0 R1), each with one new operand half, which
 // the slot before it reads: L0, L1, R1, and R0 of the next stage.
-// Measured at 8192 x 8192 x 4096 with one-byte operands, in turn on one box:
-// 229 us (2.40 PFLOP/s), 240 with all of a stage's loads in one slot; before
-// that 236 with all waves in step (reads, then products, one barrier a stage).
-// No better: the halves in the order L0 R0, L0 R1, L1 R1, L1 R0 (12, 8, 4 and 0
+// At 8192 x 8192 x 4096 with one-byte operands 217 us (2.54 PFLOP/s); against
+// all waves in step (reads, then products, one barrier a stage) 221 to 236, in
+// turn on one box, before the loads were split (below).  No better: the halves in the order L0 R0, L0 R1, L1 R1, L1 R0 (12, 8, 4 and 0
 // reads a slot), a pipelined loop with one barrier a stage whose reads run one
 // quadrant ahead (267 us, 21 registers spilled), and L's loads two slots before
-// R's (269 us).  What bounds it, from builds that leave one thing out: without
-// the loads into LDS 161 us, with half of them 175, without waiting for them
-// 219, without the fragment reads 222, without barriers 209.  So it is the rate
+// R's (269 us).  What bounds it, from builds that leave one thing out (of one
+// at 229 us): without the loads into LDS 161 us, with half of them 175, without
+// waiting for them 219, without the fragment reads 222, without barriers 209.  So it is the rate
 // of the loads into LDS, 64 KiB a stage and workgroup; the matrix units are
 // busy 53% of the cycles at 2.1 GHz.
 // Slots of stage s, counted from the leading waves' first (8 s; the second half
