@@ -184,3 +184,25 @@ def test_temperatures_that_leave_one_word(n, v, k, tau):
     # the two 1 / tau of upstream and of 1 / tau times tau: one within 2 U
     ref = np.where((top == word)[:, None], 0.0, w[top] - w[word])
     assert np.all(np.abs(d["dh"].double().cpu().numpy() - ref) <= (2.0 ** -8 + 2.0 ** -11 + 4 * U) * np.abs(ref) + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("tau", [0.1, 0.3, 0.77, 1.3, 3.0, 7.1, 11.0])
+def test_certain_rows_at_any_temperature(tau):
+    """Whatever the inverse of tau rounds to, lse and a listed logit take the same product (the rows of
+    test_certain_rows_have_no_loss, logits of 90 and below 45 over tau)."""
+    announce("certain rows at", tau)
+    n, v, k = 60, 900, 256
+    c = Case(n, v, k, "bf16", top=1, tau=tau, seed=29, absent=0.0, scale=0.1 * tau)
+    c.index[:, 0] = np.random.default_rng(30).permutation(v)[:n]
+    h, w = c.h.double(), c.w.double()
+    w[torch.from_numpy(c.index[:, 0])] = 90.0 * tau * h / (h * h).sum(dim=1, keepdim=True)
+    c.w = w.to(c.w.dtype)
+    zz = c.h.to(DEV).double() @ c.w.to(DEV).double().t() / tau
+    at = torch.from_numpy(c.index).to(DEV)
+    assert float(zz.gather(1, at).min()) > 88 and float(zz.scatter(1, at, -np.inf).max()) < 45
+    d = c.device()
+    c.forward(d)
+    c.backward(d)
+    torch.cuda.synchronize()
+    for x in ("loss", "dh", "dw"):
+        assert bool((d[x] == 0).all()), (x, float(d[x].double().abs().max()))

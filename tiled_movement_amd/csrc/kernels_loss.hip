@@ -203,8 +203,8 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void k_listed_loss(const uint16_t* __restrict__ h, const uint16_t* __restrict__ w,
                                                      const int64_t* __restrict__ index,
                                                      const float* __restrict__ teacher, int64_t v, int64_t k, int top,
-                                                     float tau, const float* __restrict__ lse, float* __restrict__ zt,
-                                                     float* __restrict__ loss) {
+                                                     float tau, float inv, const float* __restrict__ lse,
+                                                     float* __restrict__ zt, float* __restrict__ loss) {
     __shared__ float z[kMaxTop];
     const int64_t row = blockIdx.x;
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, waves = blockDim.x / 64, g = lane / 16, l16 = lane % 16;
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(256) void k_listed_loss(const uint16_t* __restrict_
             const float t = teacher[row * top + j];
             if (!entry_counts(index[row * top + j], t, v)) continue;
             const float lp = (t - m) / tau - ls, p = expf(lp);
-            out += p > 0.f || p != p ? p * (lp - (over_tau(z[j], 1.f / tau) - l)) : 0.f;
+            out += p > 0.f || p != p ? p * (lp - (over_tau(z[j], inv) - l)) : 0.f;
         }
         out = tau * (tau * wave_sum(out));  // tau^2 alone may leave fp32's range
     }
@@ -666,7 +666,7 @@ hipError_t launch_loss(const LossJob& j, hipStream_t stream) {
     const auto* w = static_cast<const uint8_t*>(j.w);
     auto* part = reinterpret_cast<float2*>(static_cast<uint8_t*>(j.ws));
     const Operand H{h, 2 * j.k, j.n, nullptr, 0, 0}, W{w, 2 * j.k, j.v, nullptr, 0, 0};
-    const float c2 = kLog2e / j.tau;
+    const float c2 = kLog2e / j.tau, inv = 1.f / j.tau;
     int64_t tiles = 0;
     const hipError_t e = by_rows(loss_tile_rows(j.n, (j.v + 255) / 256), j.bf16, [&](auto cfg) {
         using C = decltype(cfg);
@@ -678,13 +678,14 @@ hipError_t launch_loss(const LossJob& j, hipStream_t stream) {
         return hipGetLastError();
     });
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_join_stats, dim3(blocks_of(j.n, 32)), dim3(256), 0, stream, part, tiles, j.n, c2, 1.f / j.tau, j.lse,
+    hipLaunchKernelGGL(k_join_stats, dim3(blocks_of(j.n, 32)), dim3(256), 0, stream, part, tiles, j.n, c2, inv, j.lse,
                        j.teacher ? nullptr : j.index, j.v, j.zt, j.loss);
     if (j.teacher) {
         const int waves = (j.top + 15) / 16;
         hipLaunchKernelGGL(j.bf16 ? k_listed_loss<true> : k_listed_loss<false>, dim3(static_cast<unsigned>(j.n)),
                            dim3(64 * (waves < 4 ? waves : 4)), 0, stream, static_cast<const uint16_t*>(j.h),
-                           static_cast<const uint16_t*>(j.w), j.index, j.teacher, j.v, j.k, j.top, j.tau, j.lse, j.zt, j.loss);
+                           static_cast<const uint16_t*>(j.w), j.index, j.teacher, j.v, j.k, j.top, j.tau, inv, j.lse,
+                           j.zt, j.loss);
     }
     return hipGetLastError();
 }
