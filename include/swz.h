@@ -20,7 +20,10 @@
  * tiles (swz_gemm, swz_gemm_ex for a bf16 result); 8-bit floating-point
  * operands with a scale per block of 128 (swz_quant_f8) and their product
  * (swz_gemm_f8); the losses of an output layer whose logits are not kept, with
- * their gradients (swz_linear_ce, swz_linear_distill); host-only planning, bank-conflict prediction and layout
+ * their gradients (swz_linear_ce, swz_linear_distill); a gated feed-forward
+ * block with its gradients (swz_gated), weights of 4 bits and products of a few
+ * rows with them (swz_quant_w4, swz_gemm_w4, swz_gated_w4), and the norm of
+ * many tensors together (swz_grad_norm, swz_clip_grads); host-only planning, bank-conflict prediction and layout
  * algebra (swz_choose, swz_plan, swz_predict_conflicts, swz_kernel_accesses,
  * swz_bank_model_get, swz_fold); and two diagnostics (swz_copy,
  * swz_lds_probe).
@@ -587,6 +590,133 @@ int swz_linear_distill_grad(const void* d_h, const void* d_w, int32_t x_type, co
                             const float* d_teacher, int32_t top, float tau, const float* d_lse, const float* d_zt,
                             const float* d_upstream, void* d_dh, void* d_dw, int64_t n, int64_t v, int64_t k,
                             void* d_ws, int64_t ws_bytes, void* stream);
+
+/* Activations of the gated calls: z / (1 + e^-z); z Phi(z) with the normal
+ * distribution's Phi; and z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. */
+enum swz_act { SWZ_ACT_SILU = 0, SWZ_ACT_GELU = 1, SWZ_ACT_GELU_TANH = 2 };
+
+/* A gated feed-forward block's two projections, its activation and the
+ * product:
+ *   g = x Wg^T,  u = x Wu^T,  y = act(g) u.
+ *   d_x      : x_type (SWZ_X_BF16 or SWZ_X_F16) [n][k]; d_wg, d_wu : the same
+ *              type [f][k]; k a multiple of 8, all 16-byte aligned.
+ *   d_y      : x_type [n][f], aligned to its element (16-byte pieces where f is a
+ *              multiple of 8 and d_y, d_pre are 16-byte aligned).
+ *   d_pre    : NULL, or float [2][n][f]: g, then u, for the gradient call.
+ * g and u are exact products summed in fp32; y is rounded once.  Calls of up to
+ * 16 rows go to a kernel that streams both weights once.  Nothing written may
+ * overlap anything else.  n = 0 does nothing.
+ * Errors: SWZ_EINVAL (sizes, alignment, NULL, overlap, enum values),
+ * SWZ_EUNSUPPORTED (n, f or k of 2^22 - 8 and more, over 2^21 tiles of
+ * 256 x 128 of y, 256 x 256 of a gradient). */
+int swz_gated(const void* d_x, const void* d_wg, const void* d_wu, int32_t x_type, int32_t act, void* d_y, float* d_pre,
+              int64_t n, int64_t f, int64_t k, void* stream);
+
+/* Host only.  Bytes of workspace of the gradient call: 256-byte aligned device
+ * memory that carries nothing from one call to the next; calls that may run at
+ * the same time (on two streams, in two graphs) need one each.  It holds dg and
+ * du (2 bytes each a place of y) and, where a gradient has few tiles, fp32 sums
+ * of its parts.
+ * Errors: as swz_gated. */
+int swz_gated_workspace(int64_t n, int64_t f, int64_t k, int64_t* bytes);
+
+/* Its gradients, for dy = d(total) / dy (x_type [n][f]):
+ *   dg = dy u act'(g),  du = dy act(g),
+ *   dx = dg Wg + du Wu ([n][k]),  dwg = dg^T x,  dwu = du^T x ([f][k]),
+ * all x_type, overwritten, 16-byte aligned; each may be NULL (not all).
+ *   d_pre    : what swz_gated wrote there, or NULL: g and u are made again, for
+ *              4 n f k operations more.
+ * dg and du are rounded to x_type once (as they are where a program holds them;
+ * with fp16, values beyond its range are infinite or lose digits, as gradients
+ * of that type do); sums are fp32 and rounded to x_type at the end.  n = 0
+ * writes zero dwg and dwu.  Results do not depend on the order of anything:
+ * the same call gives the same bits.
+ * Errors: as swz_gated, and SWZ_EINVAL for a workspace below
+ * swz_gated_workspace. */
+int swz_gated_grad(const void* d_x, const void* d_wg, const void* d_wu, int32_t x_type, int32_t act, const void* d_dy,
+                   const float* d_pre, void* d_dx, void* d_dwg, void* d_dwu, int64_t n, int64_t f, int64_t k, void* d_ws,
+                   int64_t ws_bytes, void* stream);
+
+/* Weights of 4 bits: w = (code - zero) scale, with a scale, and on request a
+ * zero point, per `group` consecutive values of a row (32, 64 or 128; a row's
+ * last group may be shorter).
+ *   d_w     : w_type (enum swz_x_type) [n][k], k a multiple of 32.
+ *   d_q     : [n][k / 2] bytes: the even column's code in the low half.
+ *   d_scale : x_type (SWZ_X_BF16 or SWZ_X_F16) [n][ceil(k / group)].
+ *   d_zero  : NULL (every zero point is 8), or one byte per group, the same
+ *             shape.
+ * Without zero points scale is the group's largest magnitude times 1/7, with them
+ * its range, widened to hold zero, times 1/15 (as fp32 numbers), in fp32 and
+ * rounded to x_type; zero = -lowest / scale and code = w / scale + zero, quotients
+ * in fp32 rounded to the nearest whole number, ties to even, and both cut to
+ * 0 .. 15.  A group
+ * whose scale comes out 0 is zero; one with a NaN or an infinity, or whose scale
+ * leaves x_type, has a NaN scale.
+ *   d_w and d_q 16-byte aligned, d_scale to its element.
+ * Nothing written may overlap anything else.
+ * Errors: SWZ_EINVAL (sizes, alignment, NULL, overlap, enum values, group),
+ * SWZ_EUNSUPPORTED (n k of 2^34 and more). */
+int swz_quant_w4(const void* d_w, int32_t w_type, int64_t n, int64_t k, int32_t group, int32_t x_type, void* d_q,
+                 void* d_scale, uint8_t* d_zero, void* stream);
+
+/* And back: d_w x_type [n][k] = (code - zero) scale, rounded once; any scales
+ * and zero points (0 .. 255).  Buffers and errors as swz_quant_w4.  For many rows of x
+ * the product of this (swz_gemm_ex, swz_gated) is the faster one. */
+int swz_dequant_w4(const void* d_q, const void* d_scale, const uint8_t* d_zero, int64_t n, int64_t k, int32_t group,
+                   int32_t x_type, void* d_w, void* stream);
+
+/* C = X W^T of such weights, for few rows of X:
+ *   d_x : x_type [m][k]; d_c : x_type [m][n], written whatever it held, aligned
+ *   to its element; d_x and d_q 16-byte aligned.
+ * Products are exact in fp32 (x times 16 + code) and summed in fp32, a group's
+ * sum less (16 + zero) times the group's sum of x, and that times its scale in
+ * fp32; the result is rounded once.  |x| has to stay below the type's largest
+ * value over 2^9 k; a row of X that holds an infinity or NaN comes out NaN.
+ * Meant for up to some 64 rows: 16 rows of X read the weights once.  m = 0 does
+ * nothing; any n.
+ * Errors: SWZ_EINVAL (sizes, alignment, NULL, overlap, enum values, group),
+ * SWZ_EUNSUPPORTED (m or k of 2^22 and more, n of 2^26 and more, n k of 2^34
+ * and more). */
+int swz_gemm_w4(const void* d_x, int32_t x_type, const void* d_q, const void* d_scale, const uint8_t* d_zero, int32_t group,
+                void* d_c, int64_t m, int64_t n, int64_t k, void* stream);
+
+/* The gated block of two such weights, C = act(X Wg^T) (X Wu^T): both with zero
+ * points or both without.  The rest, and the errors, as swz_gemm_w4. */
+int swz_gated_w4(const void* d_x, int32_t x_type, int32_t act, const void* d_qg, const void* d_scale_g,
+                 const uint8_t* d_zero_g, const void* d_qu, const void* d_scale_u, const uint8_t* d_zero_u, int32_t group,
+                 void* d_c, int64_t m, int64_t n, int64_t k, void* stream);
+
+/* Host only.  Bytes of workspace (8-byte aligned device memory) of the two
+ * calls below for a list of tensors; it carries nothing from one call to the
+ * next, and calls that may run at the same time need one each.
+ *   d_t, numel, type : host arrays of `count` device addresses, sizes in
+ *                      elements (0 allowed, then with any address) and types
+ *                      (enum swz_x_type).  They are read during the call only.
+ * Errors: as swz_grad_norm. */
+int swz_grad_norm_workspace(const void* const* d_t, const int64_t* numel, const int32_t* type, int32_t count,
+                            int64_t* bytes);
+
+/* d_norm[0] = sqrt(sum over all tensors of the sum of their squares), squares
+ * and sums in fp64; the same call gives the same bits.  Tensors aligned to
+ * their element; 16-byte aligned ones are read in whole pieces.
+ * Errors: SWZ_EINVAL (NULL, sizes, types, alignment, overlap of what is written
+ * with anything, a workspace below swz_grad_norm_workspace), SWZ_EUNSUPPORTED
+ * (over 2^20 tensors, or one of 2^38 elements and more). */
+int swz_grad_norm(const void* const* d_t, const int64_t* numel, const int32_t* type, int32_t count, float* d_norm,
+                  void* d_ws, int64_t ws_bytes, void* stream);
+
+/* The tensors scaled so that their norm together is at most max_norm (>= 0; may
+ * be infinite): out = x factor, in fp32 and rounded once, with factor =
+ * max_norm / norm where the norm is over max_norm and finite, else 1 (tensors as
+ * they were: what to do about infinities and NaN is the caller's to say, from
+ * the norm).  d_norm[0] is the norm before, d_norm[1] the factor.
+ *   d_out : NULL, in place (then a factor of 1 writes nothing); or a host array
+ *           of `count` device addresses, each its tensor's own or apart from
+ *           everything.
+ * The same memory may not stand in the list twice.
+ * Errors: as swz_grad_norm; SWZ_EINVAL for a max_norm that is negative or NaN. */
+int swz_clip_grads(const void* const* d_t, void* const* d_out, const int64_t* numel, const int32_t* type, int32_t count,
+                   float max_norm, float* d_norm, void* d_ws, int64_t ws_bytes, void* stream);
 
 /* Host only.  The swizzle the library uses for a tile of tile_rows x
  * tile_cols elements of elem_bytes, staged by vec_bytes-wide stores and read

@@ -37,6 +37,7 @@ X_BF16, X_F16, X_F32 = 0, 1, 2
 F8_E4M3, F8_E5M2 = 0, 1
 BLOCK_1X128, BLOCK_128X128 = 0, 1
 SCALE_F32, SCALE_E8M0 = 0, 1
+ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2
 LAYOUTS = {"swizzle": LAYOUT_SWIZZLE, "pad": LAYOUT_PAD, "plain": LAYOUT_PLAIN, "direct": LAYOUT_SWIZZLE_DIRECT}
 
 EXPORTS = (
@@ -59,6 +60,16 @@ EXPORTS = (
     "swz_linear_ce_grad",
     "swz_linear_distill",
     "swz_linear_distill_grad",
+    "swz_gated",
+    "swz_gated_workspace",
+    "swz_gated_grad",
+    "swz_quant_w4",
+    "swz_dequant_w4",
+    "swz_gemm_w4",
+    "swz_gated_w4",
+    "swz_grad_norm_workspace",
+    "swz_grad_norm",
+    "swz_clip_grads",
     "swz_fold",
     "swz_choose",
     "swz_predict_conflicts",
@@ -166,6 +177,20 @@ def _load() -> ctypes.CDLL:
     lib.swz_linear_ce_grad.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, i64, vp]
     lib.swz_linear_distill.argtypes = [vp, vp, i32, vp, vp, i32, f32, vp, vp, vp, i64, i64, i64, vp, i64, vp]
     lib.swz_linear_distill_grad.argtypes = [vp, vp, i32, vp, vp, i32, f32, vp, vp, vp, vp, vp, i64, i64, i64, vp, i64, vp]
+    feed_forward = {
+        "swz_gated": [vp, vp, vp, i32, i32, vp, vp, i64, i64, i64, vp],
+        "swz_gated_workspace": [i64, i64, i64, P(i64)],
+        "swz_gated_grad": [vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, i64, i64, i64, vp, i64, vp],
+        "swz_quant_w4": [vp, i32, i64, i64, i32, i32, vp, vp, vp, vp],
+        "swz_dequant_w4": [vp, vp, vp, i64, i64, i32, i32, vp, vp],
+        "swz_gemm_w4": [vp, i32, vp, vp, vp, i32, vp, i64, i64, i64, vp],
+        "swz_gated_w4": [vp, i32, i32, vp, vp, vp, vp, vp, vp, i32, vp, i64, i64, i64, vp],
+        "swz_grad_norm_workspace": [vp, vp, vp, i32, P(i64)],
+        "swz_grad_norm": [vp, vp, vp, i32, vp, vp, i64, vp],
+        "swz_clip_grads": [vp, vp, vp, vp, i32, f32, vp, vp, i64, vp],
+    }
+    for name, types in feed_forward.items():
+        getattr(lib, name).argtypes = types
     for name in EXPORTS:
         if name != "swz_strerror":
             getattr(lib, name).restype = ctypes.c_int
@@ -474,6 +499,158 @@ def swz_linear_distill_grad(h, w, index, teacher, lse, zt, upstream, dh, dw, n: 
     _check(lib.swz_linear_distill_grad(_ptr(h), _ptr(w), x_type, _ptr(index), _ptr(teacher), top, tau, _ptr(lse), _ptr(zt),
                                        _ptr(upstream), _ptr(dh), _ptr(dw), n, v, k, _ptr(ws), _ws_bytes(ws, need),
                                        _stream(stream, h, w)), "swz_linear_distill_grad")
+
+
+def swz_gated(x, wg, wu, y, n: int, f: int, k: int, x_type: int = X_BF16, act: int = ACT_SILU, pre=None, stream=None) -> None:
+    """y [n][f] = act(x wg^T) * (x wu^T); pre (fp32 [2][n][f]), if given, keeps both products for the gradients."""
+    xt = _X.get(x_type)
+    _buf("swz_gated", x=(x, 2 * n * k, xt), wg=(wg, 2 * f * k, xt), wu=(wu, 2 * f * k, xt), y=(y, 2 * n * f, xt),
+         pre=(pre, 8 * n * f, _FLOAT))
+    _check(lib.swz_gated(_ptr(x), _ptr(wg), _ptr(wu), x_type, act, _ptr(y), _ptr(pre), n, f, k, _stream(stream, x, wg)),
+           "swz_gated")
+
+
+def swz_gated_workspace(n: int, f: int, k: int) -> int:
+    """Bytes of workspace for swz_gated_grad."""
+    out = ctypes.c_int64()
+    _check(lib.swz_gated_workspace(n, f, k, ctypes.byref(out)), "swz_gated_workspace")
+    return out.value
+
+
+def swz_gated_grad(x, wg, wu, dy, dx, dwg, dwu, n: int, f: int, k: int, ws, x_type: int = X_BF16, act: int = ACT_SILU,
+                   pre=None, stream=None) -> None:
+    """dx [n][k], dwg and dwu [f][k] of sum(dy * y); each may be None (not all).  Without pre the products are made again."""
+    need = swz_gated_workspace(n, f, k)
+    xt = _X.get(x_type)
+    _buf("swz_gated_grad", x=(x, 2 * n * k, xt), wg=(wg, 2 * f * k, xt), wu=(wu, 2 * f * k, xt), dy=(dy, 2 * n * f, xt),
+         pre=(pre, 8 * n * f, _FLOAT), dx=(dx, 2 * n * k, xt), dwg=(dwg, 2 * f * k, xt), dwu=(dwu, 2 * f * k, xt), ws=(ws, need))
+    _check(lib.swz_gated_grad(_ptr(x), _ptr(wg), _ptr(wu), x_type, act, _ptr(dy), _ptr(pre), _ptr(dx), _ptr(dwg), _ptr(dwu), n,
+                              f, k, _ptr(ws), _ws_bytes(ws, need), _stream(stream, x, wg)), "swz_gated_grad")
+
+
+_CODES = _Type(1, "uint8")
+
+
+def _w4(n: int, k: int, group: int, q, scale, zero, st, suffix: str = "") -> dict:
+    """The buffers of 4-bit weights for _buf."""
+    groups = n * -(-k // group) if group > 0 else 0
+    return {"q" + suffix: (q, n * (k // 2), _CODES), "scale" + suffix: (scale, 2 * groups, st),
+            "zero" + suffix: (zero, groups, _CODES)}
+
+
+def swz_quant_w4(w, q, scale, n: int, k: int, group: int = 128, w_type: int = X_BF16, x_type: int = X_BF16, zero=None,
+                 stream=None) -> None:
+    """w [n][k] to 4-bit codes q [n][k / 2] with scales of x_type per group (and zero points, uint8, if zero is given)."""
+    _buf("swz_quant_w4", w=(w, n * k * (4 if w_type == X_F32 else 2), _X.get(w_type)),
+         **_w4(n, k, group, q, scale, zero, _X.get(x_type)))
+    _check(lib.swz_quant_w4(_ptr(w), w_type, n, k, group, x_type, _ptr(q), _ptr(scale), _ptr(zero), _stream(stream, w, q)),
+           "swz_quant_w4")
+
+
+def swz_dequant_w4(q, scale, w, n: int, k: int, group: int = 128, x_type: int = X_BF16, zero=None, stream=None) -> None:
+    """w [n][k] (x_type) = (code - zero) * scale."""
+    xt = _X.get(x_type)
+    _buf("swz_dequant_w4", w=(w, 2 * n * k, xt), **_w4(n, k, group, q, scale, zero, xt))
+    _check(lib.swz_dequant_w4(_ptr(q), _ptr(scale), _ptr(zero), n, k, group, x_type, _ptr(w), _stream(stream, q, w)),
+           "swz_dequant_w4")
+
+
+def swz_gemm_w4(x, q, scale, c, m: int, n: int, k: int, group: int = 128, x_type: int = X_BF16, zero=None, stream=None) -> None:
+    """c [m][n] = x [m][k] W^T of 4-bit weights, for few rows of x."""
+    xt = _X.get(x_type)
+    _buf("swz_gemm_w4", x=(x, 2 * m * k, xt), c=(c, 2 * m * n, xt), **_w4(n, k, group, q, scale, zero, xt))
+    _check(lib.swz_gemm_w4(_ptr(x), x_type, _ptr(q), _ptr(scale), _ptr(zero), group, _ptr(c), m, n, k, _stream(stream, x, q)),
+           "swz_gemm_w4")
+
+
+def swz_gated_w4(x, qg, scale_g, qu, scale_u, c, m: int, n: int, k: int, group: int = 128, x_type: int = X_BF16,
+                 act: int = ACT_SILU, zero_g=None, zero_u=None, stream=None) -> None:
+    """c [m][n] = act(x Wg^T) * (x Wu^T) of 4-bit weights, for few rows of x."""
+    xt = _X.get(x_type)
+    _buf("swz_gated_w4", x=(x, 2 * m * k, xt), c=(c, 2 * m * n, xt), **_w4(n, k, group, qg, scale_g, zero_g, xt, "_g"),
+         **_w4(n, k, group, qu, scale_u, zero_u, xt, "_u"))
+    _check(lib.swz_gated_w4(_ptr(x), x_type, act, _ptr(qg), _ptr(scale_g), _ptr(zero_g), _ptr(qu), _ptr(scale_u), _ptr(zero_u),
+                            group, _ptr(c), m, n, k, _stream(stream, x, qg)), "swz_gated_w4")
+
+
+_X_OF = {}  # torch element types of the norm calls, filled by their first call
+
+
+def _tensors(call: str, tensors, like=None):
+    """A list of tensors as the host arrays that the norm calls read: (addresses, sizes, types, count).  like: the list
+    that these tensors have to match in size and type."""
+    import torch
+
+    if not _X_OF:
+        _X_OF.update({torch.bfloat16: X_BF16, torch.float16: X_F16, torch.float32: X_F32})
+    n = len(tensors)
+    if like is not None and n != len(like):
+        raise ValueError(f"{call}: {n} tensors to write, {len(like)} to read")
+    at, numel, kinds = [0] * n, [0] * n, [0] * n
+    device = None
+    for i, t in enumerate(tensors):
+        kind = _X_OF.get(getattr(t, "dtype", None))
+        if kind is None:
+            raise ValueError(f"{call}: tensor {i} is not a bfloat16, float16 or float32 tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{call}: tensor {i} must be a CUDA tensor")
+        if not t.is_contiguous():
+            raise ValueError(f"{call}: tensor {i} must be contiguous (a strided view is not its own bytes)")
+        here = t.device
+        if device is None:
+            device = here
+            if here.index != torch.cuda.current_device():
+                raise ValueError(f"{call}: tensor {i} is on {here}, the current device is cuda:{torch.cuda.current_device()} "
+                                 f"(call inside torch.cuda.device({here.index}))")
+        elif here != device:
+            raise ValueError(f"{call}: tensor {i} is on {here}, the other tensors on {device}")
+        at[i], numel[i], kinds[i] = t.data_ptr(), t.numel(), kind
+        if like is not None and (t.dtype != like[i].dtype or numel[i] != like[i].numel()):
+            raise ValueError(f"{call}: tensor {i} to write differs from the one to read in size or type")
+    return (ctypes.c_void_p * n)(*at), (ctypes.c_int64 * n)(*numel), (ctypes.c_int32 * n)(*kinds), n, device
+
+
+def _norm_workspace(call: str, arrays) -> int:
+    out = ctypes.c_int64()
+    _check(lib.swz_grad_norm_workspace(*arrays[:4], ctypes.byref(out)), call)
+    return out.value
+
+
+def swz_grad_norm_workspace(tensors) -> int:
+    """Bytes of workspace for the norm of these tensors."""
+    return _norm_workspace("swz_grad_norm_workspace", _tensors("swz_grad_norm_workspace", tensors))
+
+
+def swz_grad_norm(tensors, norm, ws, stream=None) -> None:
+    """norm[0] (fp32) = sqrt of the sum of all the tensors' squares."""
+    a = _tensors("swz_grad_norm", tensors)
+    need = _norm_workspace("swz_grad_norm", a)
+    _same_device("swz_grad_norm", a[4], norm)
+    _buf("swz_grad_norm", norm=(norm, 4, _FLOAT), ws=(ws, need))
+    _check(lib.swz_grad_norm(*a[:4], _ptr(norm), _ptr(ws), _ws_bytes(ws, need), _stream(stream, norm, ws)), "swz_grad_norm")
+
+
+def swz_clip_grads(tensors, max_norm: float, norm, ws, out=None, stream=None) -> None:
+    """The tensors scaled so that their norm together is at most max_norm, in place or into the tensors of `out`;
+    norm (fp32 [2]): the norm before, and the factor."""
+    a = _tensors("swz_clip_grads", tensors)
+    to = None
+    if out is not None:
+        b = _tensors("swz_clip_grads", out, tensors)
+        to = b[0]
+        if b[4] != a[4]:
+            raise ValueError(f"swz_clip_grads: the tensors to write are on {b[4]}, those to read on {a[4]}")
+    need = _norm_workspace("swz_clip_grads", a)
+    _same_device("swz_clip_grads", a[4], norm)
+    _buf("swz_clip_grads", norm=(norm, 8, _FLOAT), ws=(ws, need))
+    _check(lib.swz_clip_grads(a[0], to, *a[1:4], max_norm, _ptr(norm), _ptr(ws), _ws_bytes(ws, need), _stream(stream, norm, ws)),
+           "swz_clip_grads")
+
+
+def _same_device(call: str, device, t) -> None:
+    here = getattr(t, "device", None)
+    if device is not None and here is not None and here != device:
+        raise ValueError(f"{call}: norm is on {here}, the tensors on {device}")
 
 
 def swz_fold(params, base: int, active: int):

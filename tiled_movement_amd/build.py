@@ -31,6 +31,9 @@ SOURCES = [
     "kernels_gemm_f8_few.hip",
     "kernels_quant.hip",
     "kernels_loss.hip",
+    "kernels_gated.hip",
+    "kernels_w4.hip",
+    "kernels_norm.hip",
     "kernels_map.hip",
     "kernels_rows.hip",
     "kernels_copy.hip",

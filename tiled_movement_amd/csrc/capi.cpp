@@ -1,14 +1,19 @@
 // C ABI of libswz.so: argument checks, parameter choice and launches.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cfloat>
+#include <cmath>
 #include <cstring>
 #include <map>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <tuple>
 
 #include "chooser.h"
 #include "launch.h"
+#include "launch_ffn.h"
 #include "swz.h"
 
 #define SWZ_API extern "C" __attribute__((visibility("default")))
@@ -141,6 +146,131 @@ bool spans_ok(const Span* s, int count) {
             if ((s[i].written || s[j].written) && s[j].bytes && overlaps(s[i].p, s[i].bytes, s[j].p, s[j].bytes)) return false;
     }
     return true;
+}
+
+// Sizes of a gated block that the kernels' grids and offsets take.
+int check_gated_sizes(int64_t n, int64_t f, int64_t k) {
+    if (n < 0 || f < 1 || k < 8 || k % 8) return SWZ_EINVAL;
+    for (const int64_t v : {n, f, k})
+        if (v >= swz::kMaxPitch / 2 - 8) return SWZ_EUNSUPPORTED;
+    const int64_t tiles = int64_t(1) << 21;
+    if ((n / 256 + 1) * (f / 128 + 1) > tiles || (n / 256 + 1) * (k / 256 + 1) > tiles || (f / 256 + 1) * (k / 256 + 1) > tiles)
+        return SWZ_EUNSUPPORTED;
+    return SWZ_OK;
+}
+
+bool half_type(int32_t x_type) { return x_type == SWZ_X_BF16 || x_type == SWZ_X_F16; }
+bool act_known(int32_t act) { return act == SWZ_ACT_SILU || act == SWZ_ACT_GELU || act == SWZ_ACT_GELU_TANH; }
+
+// Rows of a gradient product's tiles and the parts that its sum is split into:
+// where there are fewer tiles than the 256 compute units, parts of at least 8
+// stages with fp32 sums of their own.
+void plan_product(int64_t rows, int64_t cols, int64_t products, int64_t stages, int64_t* tile_rows, int64_t* parts) {
+    *tile_rows = rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    const int64_t tiles = (rows + *tile_rows - 1) / *tile_rows * ((cols + 255) / 256) * products;
+    *parts = tiles >= 256 || tiles == 0 ? 1 : 256 / tiles;
+    if (*parts > 32) *parts = 32;
+    if (*parts > stages / 8) *parts = stages / 8 ? stages / 8 : 1;
+}
+
+swz::GatedPlan plan_gated(int64_t n, int64_t f, int64_t k) {
+    swz::GatedPlan p{};
+    p.ldz = up(f, 8);
+    plan_product(n, k, 1, 2 * ((f + 63) / 64), &p.dx_rows, &p.dx_parts);
+    plan_product(f, k, 2, (n + 63) / 64, &p.dw_rows, &p.dw_parts);
+    const int64_t dx = p.dx_parts > 1 ? 4 * p.dx_parts * n * k : 0, dw = p.dw_parts > 1 ? 8 * p.dw_parts * f * k : 0;
+    p.dg = 0;
+    p.du = up(2 * n * p.ldz, 256);
+    p.sums = 2 * p.du;
+    p.bytes = p.sums + up(dx > dw ? dx : dw, 256);
+    return p;
+}
+
+int check_w4_sizes(int64_t n, int64_t k, int32_t group) {
+    if (n < 0 || k < 32 || k % 32 || (group != 32 && group != 64 && group != 128)) return SWZ_EINVAL;
+    if (n > 0 && k >= (int64_t(1) << 34) / n) return SWZ_EUNSUPPORTED;
+    return SWZ_OK;
+}
+
+int gemm_w4(const void* d_x, int32_t x_type, int32_t act, const swz::WeightsW4* w, int mats, int32_t group, void* d_c, int64_t m,
+            int64_t n, int64_t k, void* stream) {
+    if (!half_type(x_type) || m < 0) return SWZ_EINVAL;
+    const int st = check_w4_sizes(n, k, group);
+    if (st != SWZ_OK) return st;
+    if (m >= int64_t(1) << 22 || k >= int64_t(1) << 22 || n >= int64_t(1) << 26) return SWZ_EUNSUPPORTED;
+    if (m == 0 || n == 0) return SWZ_OK;
+    const int64_t groups = (k + group - 1) / group;
+    Span s[8] = {{d_x, 2 * m * k, 16, false}, {d_c, 2 * m * n, 2, true}};
+    int count = 2;
+    for (int i = 0; i < mats; ++i) {
+        s[count++] = {w[i].q, n * (k / 2), 16, false};
+        s[count++] = {w[i].scale, 2 * n * groups, 2, false};
+        if (w[i].zero) s[count++] = {w[i].zero, n * groups, 1, false};
+    }
+    if (!spans_ok(s, count)) return SWZ_EINVAL;
+    swz::GemmW4Job j{d_x, x_type == SWZ_X_BF16, m, n, k, group, mats == 2 ? act : -1, {w[0], w[mats - 1]}, d_c};
+    return hip_status(swz::launch_gemm_w4(j, static_cast<hipStream_t>(stream)));
+}
+
+// The list of a norm call: SWZ_OK and its partial sums' bytes, or why not.
+int check_norm_list(const void* const* d_t, const int64_t* numel, const int32_t* type, int32_t count, int64_t* ws_bytes) {
+    if (count < 0 || (count > 0 && (!d_t || !numel || !type))) return SWZ_EINVAL;
+    if (count > 1 << 20) return SWZ_EUNSUPPORTED;
+    int64_t partials = 0, chunks = 0;
+    int here = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        if (numel[i] < 0 || (type[i] != SWZ_X_BF16 && type[i] != SWZ_X_F16 && type[i] != SWZ_X_F32)) return SWZ_EINVAL;
+        if (numel[i] >= int64_t(1) << 38) return SWZ_EUNSUPPORTED;
+        if (numel[i] == 0) continue;
+        if (!d_t[i] || reinterpret_cast<uintptr_t>(d_t[i]) % (type[i] == SWZ_X_F32 ? 4 : 2)) return SWZ_EINVAL;
+        chunks += swz::norm_chunks(d_t[i], numel[i], type[i]);
+        if (++here == swz::kNormTensors) {
+            partials += std::min(chunks, swz::kNormBlocks);
+            chunks = here = 0;
+        }
+    }
+    *ws_bytes = 8 * (partials + std::min(chunks, swz::kNormBlocks));
+    return SWZ_OK;
+}
+
+// Whether nothing written overlaps anything else, in time linear but for a sort.
+bool apart(Span* s, int64_t count) {
+    std::sort(s, s + count, [](const Span& a, const Span& b) {
+        return reinterpret_cast<uintptr_t>(a.p) < reinterpret_cast<uintptr_t>(b.p);
+    });
+    uintptr_t read_end = 0, written_end = 0;  // of those before
+    for (int64_t i = 0; i < count; ++i) {
+        const auto at = reinterpret_cast<uintptr_t>(s[i].p);
+        if (at < written_end || (s[i].written && at < read_end)) return false;
+        uintptr_t& end = s[i].written ? written_end : read_end;
+        end = std::max(end, at + static_cast<uintptr_t>(s[i].bytes));
+    }
+    return true;
+}
+
+int norm_call(const void* const* d_t, void* const* d_out, const int64_t* numel, const int32_t* type, int32_t count, bool clip,
+              float max_norm, float* d_norm, void* d_ws, int64_t ws_bytes, void* stream) {
+    int64_t need;
+    const int st = check_norm_list(d_t, numel, type, count, &need);
+    if (st != SWZ_OK) return st;
+    if (!d_norm || reinterpret_cast<uintptr_t>(d_norm) % 4) return SWZ_EINVAL;
+    if (need > 0 && (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 8 || ws_bytes < need)) return SWZ_EINVAL;
+    const std::unique_ptr<Span[]> s(new (std::nothrow) Span[2 * static_cast<size_t>(count) + 2]);
+    if (!s) return SWZ_EUNSUPPORTED;
+    int64_t spans = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        if (numel[i] == 0) continue;
+        const int64_t es = type[i] == SWZ_X_F32 ? 4 : 2, bytes = es * numel[i];
+        const void* out = clip && d_out ? d_out[i] : d_t[i];
+        if (!out || reinterpret_cast<uintptr_t>(out) % static_cast<uintptr_t>(es)) return SWZ_EINVAL;
+        s[spans++] = {out, bytes, 1, clip};
+        if (out != d_t[i]) s[spans++] = {d_t[i], bytes, 1, false};
+    }
+    s[spans++] = {d_norm, clip ? 8 : 4, 1, true};
+    if (need > 0) s[spans++] = {d_ws, need, 1, true};
+    if (!apart(s.get(), spans)) return SWZ_EINVAL;
+    const swz::NormJob j{d_t, d_out, numel, type, count, clip, max_norm, d_norm, static_cast<double*>(d_ws)};
+    return hip_status(swz::launch_norm(j, static_cast<hipStream_t>(stream)));
 }
 
 int loss_forward(const void* d_h, const void* d_w, int32_t x_type, const int64_t* index, const float* teacher, int32_t top,
@@ -817,6 +947,110 @@ SWZ_API int swz_linear_distill_grad(const void* d_h, const void* d_w, int32_t x_
     if (n > 0 && !d_teacher) return SWZ_EINVAL;
     return loss_backward(d_h, d_w, x_type, d_index, d_teacher, top, tau, d_lse, d_zt, d_upstream, d_dh, d_dw, n, v, k, d_ws,
                          ws_bytes, stream);
+}
+
+SWZ_API int swz_gated(const void* d_x, const void* d_wg, const void* d_wu, int32_t x_type, int32_t act, void* d_y, float* d_pre,
+                      int64_t n, int64_t f, int64_t k, void* stream) {
+    if (!half_type(x_type) || !act_known(act)) return SWZ_EINVAL;
+    const int st = check_gated_sizes(n, f, k);
+    if (st != SWZ_OK) return st;
+    if (n == 0) return SWZ_OK;
+    const Span s[] = {{d_x, 2 * n * k, 16, false}, {d_wg, 2 * f * k, 16, false}, {d_wu, 2 * f * k, 16, false},
+                      {d_y, 2 * n * f, 2, true}, {d_pre, d_pre ? 8 * n * f : 0, 4, true}};
+    if (!spans_ok(s, 5)) return SWZ_EINVAL;
+    swz::GatedJob j{};
+    j.x = d_x, j.wg = d_wg, j.wu = d_wu, j.bf16 = x_type == SWZ_X_BF16, j.act = act, j.n = n, j.f = f, j.k = k, j.y = d_y;
+    j.pre = d_pre;
+    return hip_status(swz::launch_gated(j, static_cast<hipStream_t>(stream)));
+}
+
+SWZ_API int swz_gated_workspace(int64_t n, int64_t f, int64_t k, int64_t* bytes) {
+    if (!bytes) return SWZ_EINVAL;
+    const int st = check_gated_sizes(n, f, k);
+    if (st != SWZ_OK) return st;
+    *bytes = plan_gated(n, f, k).bytes;
+    return SWZ_OK;
+}
+
+SWZ_API int swz_gated_grad(const void* d_x, const void* d_wg, const void* d_wu, int32_t x_type, int32_t act, const void* d_dy,
+                           const float* d_pre, void* d_dx, void* d_dwg, void* d_dwu, int64_t n, int64_t f, int64_t k, void* d_ws,
+                           int64_t ws_bytes, void* stream) {
+    if (!half_type(x_type) || !act_known(act)) return SWZ_EINVAL;
+    const int st = check_gated_sizes(n, f, k);
+    if (st != SWZ_OK) return st;
+    if (!d_dx && !d_dwg && !d_dwu) return SWZ_EINVAL;
+    const swz::GatedPlan p = plan_gated(n, f, k);
+    const bool any = n > 0;
+    if (ws_bytes < p.bytes) return SWZ_EINVAL;
+    const Span s[] = {{d_x, 2 * n * k, 16, false}, {d_wg, any ? 2 * f * k : 0, 16, false}, {d_wu, any ? 2 * f * k : 0, 16, false},
+                      {d_dy, 2 * n * f, 2, false}, {d_pre, d_pre ? 8 * n * f : 0, 4, false}, {d_dx, d_dx ? 2 * n * k : 0, 16, true},
+                      {d_dwg, d_dwg ? 2 * f * k : 0, 16, true}, {d_dwu, d_dwu ? 2 * f * k : 0, 16, true},
+                      {d_ws, p.bytes, 256, true}};
+    if (!spans_ok(s, 9)) return SWZ_EINVAL;
+    swz::GatedJob j{};
+    j.x = d_x, j.wg = d_wg, j.wu = d_wu, j.bf16 = x_type == SWZ_X_BF16, j.act = act, j.n = n, j.f = f, j.k = k, j.dy = d_dy;
+    j.pre = const_cast<float*>(d_pre), j.dx = d_dx, j.dwg = d_dwg, j.dwu = d_dwu, j.ws = d_ws;
+    return hip_status(swz::launch_gated_grad(j, p, static_cast<hipStream_t>(stream)));
+}
+
+SWZ_API int swz_quant_w4(const void* d_w, int32_t w_type, int64_t n, int64_t k, int32_t group, int32_t x_type, void* d_q,
+                         void* d_scale, uint8_t* d_zero, void* stream) {
+    if ((!half_type(w_type) && w_type != SWZ_X_F32) || !half_type(x_type)) return SWZ_EINVAL;
+    const int st = check_w4_sizes(n, k, group);
+    if (st != SWZ_OK) return st;
+    const int64_t groups = (k + group - 1) / group;
+    const Span s[] = {{d_w, n * k * (w_type == SWZ_X_F32 ? 4 : 2), 16, false}, {d_q, n * (k / 2), 16, true},
+                      {d_scale, 2 * n * groups, 2, true}, {d_zero, d_zero ? n * groups : 0, 1, true}};
+    if (n == 0) return SWZ_OK;
+    if (!spans_ok(s, 4)) return SWZ_EINVAL;
+    const swz::QuantW4Job j{d_w, w_type, x_type == SWZ_X_BF16, n, k, group, d_q, d_scale, d_zero};
+    return hip_status(swz::launch_quant_w4(j, static_cast<hipStream_t>(stream)));
+}
+
+SWZ_API int swz_dequant_w4(const void* d_q, const void* d_scale, const uint8_t* d_zero, int64_t n, int64_t k, int32_t group,
+                           int32_t x_type, void* d_w, void* stream) {
+    if (!half_type(x_type)) return SWZ_EINVAL;
+    const int st = check_w4_sizes(n, k, group);
+    if (st != SWZ_OK) return st;
+    const int64_t groups = (k + group - 1) / group;
+    const Span s[] = {{d_q, n * (k / 2), 16, false}, {d_scale, 2 * n * groups, 2, false}, {d_zero, d_zero ? n * groups : 0, 1, false},
+                      {d_w, 2 * n * k, 16, true}};
+    if (n == 0) return SWZ_OK;
+    if (!spans_ok(s, 4)) return SWZ_EINVAL;
+    const swz::WeightsW4 w{static_cast<const uint8_t*>(d_q), d_scale, d_zero};
+    return hip_status(swz::launch_dequant_w4(w, x_type == SWZ_X_BF16, n, k, group, d_w, static_cast<hipStream_t>(stream)));
+}
+
+SWZ_API int swz_gemm_w4(const void* d_x, int32_t x_type, const void* d_q, const void* d_scale, const uint8_t* d_zero, int32_t group,
+                        void* d_c, int64_t m, int64_t n, int64_t k, void* stream) {
+    const swz::WeightsW4 w{static_cast<const uint8_t*>(d_q), d_scale, d_zero};
+    return gemm_w4(d_x, x_type, 0, &w, 1, group, d_c, m, n, k, stream);
+}
+
+SWZ_API int swz_gated_w4(const void* d_x, int32_t x_type, int32_t act, const void* d_qg, const void* d_scale_g,
+                         const uint8_t* d_zero_g, const void* d_qu, const void* d_scale_u, const uint8_t* d_zero_u, int32_t group,
+                         void* d_c, int64_t m, int64_t n, int64_t k, void* stream) {
+    if (!act_known(act) || !d_zero_g != !d_zero_u) return SWZ_EINVAL;
+    const swz::WeightsW4 w[2] = {{static_cast<const uint8_t*>(d_qg), d_scale_g, d_zero_g},
+                                 {static_cast<const uint8_t*>(d_qu), d_scale_u, d_zero_u}};
+    return gemm_w4(d_x, x_type, act, w, 2, group, d_c, m, n, k, stream);
+}
+
+SWZ_API int swz_grad_norm_workspace(const void* const* d_t, const int64_t* numel, const int32_t* type, int32_t count,
+                                    int64_t* bytes) {
+    if (!bytes) return SWZ_EINVAL;
+    return check_norm_list(d_t, numel, type, count, bytes);
+}
+
+SWZ_API int swz_grad_norm(const void* const* d_t, const int64_t* numel, const int32_t* type, int32_t count, float* d_norm,
+                          void* d_ws, int64_t ws_bytes, void* stream) {
+    return norm_call(d_t, nullptr, numel, type, count, false, 0.f, d_norm, d_ws, ws_bytes, stream);
+}
+
+SWZ_API int swz_clip_grads(const void* const* d_t, void* const* d_out, const int64_t* numel, const int32_t* type, int32_t count,
+                           float max_norm, float* d_norm, void* d_ws, int64_t ws_bytes, void* stream) {
+    if (!(max_norm >= 0.f)) return SWZ_EINVAL;
+    return norm_call(d_t, d_out, numel, type, count, true, max_norm, d_norm, d_ws, ws_bytes, stream);
 }
 
 SWZ_API int swz_fold(const swz_params* p, uint32_t base, uint32_t active, uint32_t* collision,

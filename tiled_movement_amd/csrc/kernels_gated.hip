@@ -1,0 +1,412 @@
+// A gated feed-forward block's two projections, its activation and the
+// product, y = act(g) u with g = x Wg^T and u = x Wu^T, and its gradients
+//   dg = dy u act'(g),  du = dy act(g),
+//   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x.
+//
+// Forward: a tile of x against rows of both weights in turn (Gated in
+// mma_core.h), so that a lane holds g and u of its places; y is their only
+// rounding.  On request g and u are kept in fp32 for the backward pass (8 bytes a
+// place against 4 k operations to make them again).
+//
+// Backward: dg and du are made once, in x's type, by elements from the kept g
+// and u or by the forward products over again.  The products that follow sum over
+// f (dx) and over the rows of x (dW), where the weights, dg, du and x
+// lie across the sum; they are read as they lie, by transposing reads out of
+// LDS (Across in mma_core.h), so nothing is transposed through memory.
+#include "activation.h"
+#include "launch_ffn.h"
+#include "mma_core.h"
+
+namespace swz {
+namespace {
+
+using namespace mma;
+
+// A configuration's half along R: what the epilogue of a Gated one stores.
+template <class C>
+struct HalfR {
+    static constexpr int BL = C::BL, BR = C::BR / 2, kPitch = 16 * BR + 4;
+};
+
+template <int ELEM>
+using Value = std::conditional_t<ELEM == kBf16, __bf16, _Float16>;
+
+// What a workgroup of a tile kernel works on.
+template <class C>
+struct Place {
+    int lane, g, l16, wave, wl, wr;
+    int64_t i0, f0;  // the wave's first row and feature
+    __device__ __forceinline__ Place(int64_t tm, int64_t tn) {
+        const int t = threadIdx.x;
+        lane = t % 64, g = lane / 16, l16 = lane % 16;
+        wave = __builtin_amdgcn_readfirstlane(t / 64), wl = wave / C::WR, wr = wave % C::WR;
+        i0 = tm * C::TL + wl * C::BL * 16;
+        f0 = tn * (C::TR / 2) + wr * C::BR * 8;
+    }
+};
+
+template <class C, int ACT>
+__global__ __launch_bounds__(C::NT) void k_gated(Operand X, PairOperand W, int64_t kbytes, Value<C::ELEM>* __restrict__ y,
+                                                 float* __restrict__ pre, int vec, TileMap map) {
+    __shared__ i32x4 lds_v[C::kLds / 16];
+    lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
+    int64_t tm, tn;
+    if (!map.at(blockIdx.x, &tm, &tn)) return;
+    f32x4 acc[C::BL][C::BR];
+    tile_product<C>(acc, X, W, tm * C::TL, tn * (C::TR / 2), kbytes, lds);
+    const Place<C> at(tm, tn);
+    using H = HalfR<C>;
+    lds_f32* slice = (lds_f32*)(lds + at.wave * C::kSlice);
+    const int64_t n = X.rows, f = W.rows;
+    f32x4 part[H::BL][H::BR];
+    if (pre) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+#pragma unroll
+            for (int x = 0; x < H::BL; ++x)
+#pragma unroll
+                for (int b = 0; b < H::BR; ++b) part[x][b] = acc[x][p * H::BR + b];
+            store_tile<H>(part, slice, pre + p * n * f, f, at.i0, at.f0, n, f, vec, at.lane, [](float v) { return v; });
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < H::BL; ++x)
+#pragma unroll
+        for (int b = 0; b < H::BR; ++b) {
+            __builtin_amdgcn_sched_barrier(0);  // all places' activations at once would not fit in registers
+#pragma unroll
+            for (int i = 0; i < 4; ++i) part[x][b][i] = act::both<ACT, false>(acc[x][b][i]).x * acc[x][H::BR + b][i];
+        }
+    store_tile<H>(part, slice, y, f, at.i0, at.f0, n, f, vec, at.lane, [](float v) { return v; });
+}
+
+// Up to 16 rows of x: the time is the weights' bytes.  A workgroup owns 16
+// features of both weights; its waves split k, wave w taking the blocks of 64
+// w, w + kFewWaves, ..., and the weights go from HBM straight into matrix
+// fragments; the waves' sums are joined through LDS in their order.
+constexpr int kFewWaves = 8;
+template <int ELEM, int ACT>
+__global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(const uint8_t* __restrict__ x, const uint8_t* __restrict__ wg,
+                                                              const uint8_t* __restrict__ wu, int64_t n, int64_t f, int64_t k,
+                                                              Value<ELEM>* __restrict__ y, float* __restrict__ pre) {
+    __shared__ f32x4 red[2][kFewWaves][64];
+    const int t = threadIdx.x, lane = t % 64, g = lane / 16, l16 = lane % 16;
+    const int wave = __builtin_amdgcn_readfirstlane(t / 64);
+    const int64_t f0 = static_cast<int64_t>(blockIdx.x) * 16;
+    // this lane's rows; the last stands in for rows behind it, whose results are not stored
+    const int64_t rx = l16 < n ? l16 : n - 1, rw = f0 + l16 < f ? f0 + l16 : f - 1;
+    const uint8_t* row[3] = {x + 2 * rx * k, wg + 2 * rw * k, wu + 2 * rw * k};
+    const int64_t kbytes = 2 * k, full = kbytes / 128;
+    f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    // U blocks of this wave from b on, all loads before the products
+    auto step = [&](int64_t b, auto un, bool lo_in, bool hi_in) {
+        constexpr int U = decltype(un)::value;
+        const i32x4 none = {0, 0, 0, 0};
+        i32x8 v[U][3];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int o = 2; o >= 0; --o) {
+                const uint8_t* p = row[o] + (b + u * kFewWaves) * 128 + 16 * g;
+                const i32x4 lo = lo_in ? *reinterpret_cast<const i32x4*>(p) : none;
+                const i32x4 hi = hi_in ? *reinterpret_cast<const i32x4*>(p + 64) : none;
+                v[u][o] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) acc[o] = mfma_pair<ELEM>(v[u][o + 1], v[u][0], acc[o]);
+    };
+    constexpr int U = 4;
+    int64_t b = wave;
+    for (; b + (U - 1) * kFewWaves < full; b += U * kFewWaves) step(b, std::integral_constant<int, U>{}, true, true);
+    for (; b < full; b += kFewWaves) step(b, std::integral_constant<int, 1>{}, true, true);
+    // k is a multiple of 8: 16-byte chunks are inside or outside as a whole
+    if (full * 128 < kbytes && full % kFewWaves == wave)
+        step(full, std::integral_constant<int, 1>{}, full * 128 + 16 * g < kbytes, full * 128 + 16 * g + 64 < kbytes);
+
+    // lane (g, l16): row l16 of x, features 4g .. 4g+3
+#pragma unroll
+    for (int o = 0; o < 2; ++o) red[o][wave][l16 * 4 + g] = acc[o];
+    __syncthreads();
+    if (t >= 256) return;
+    const float* rf = reinterpret_cast<const float*>(red);
+    float z[2] = {0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) z[0] += rf[w * 256 + t], z[1] += rf[(kFewWaves + w) * 256 + t];
+    const int64_t i = t / 16, j = f0 + t % 16;
+    if (i >= n || j >= f) return;
+    if (pre) pre[i * f + j] = z[0], pre[(n + i) * f + j] = z[1];
+    y[i * f + j] = static_cast<Value<ELEM>>(act::both<ACT, false>(z[0]).x * z[1]);
+}
+
+// dg and du ([n][ldz], x's type) from the kept g and u.  Rows by blockIdx.y.
+template <class CT, int ACT>
+__global__ __launch_bounds__(256) void k_gated_dz(const float* __restrict__ pre, const CT* __restrict__ dy, int64_t n, int64_t f,
+                                                  int64_t ldz, CT* __restrict__ dg, CT* __restrict__ du) {
+    const int64_t j = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (j >= f) return;
+    for (int64_t i = blockIdx.y; i < n; i += gridDim.y) {
+        const float g = pre[i * f + j], u = pre[(n + i) * f + j], d = static_cast<float>(dy[i * f + j]);
+        const float2 a = act::both<ACT, true>(g);
+        dg[i * ldz + j] = static_cast<CT>(d * u * a.y);
+        du[i * ldz + j] = static_cast<CT>(d * a.x);
+    }
+}
+
+// The same with g and u made again.
+template <class C, int ACT>
+__global__ __launch_bounds__(C::NT) void k_gated_again_dz(Operand X, PairOperand W, int64_t kbytes,
+                                                          const Value<C::ELEM>* __restrict__ dy, int64_t ldz,
+                                                          Value<C::ELEM>* __restrict__ dg, Value<C::ELEM>* __restrict__ du,
+                                                          TileMap map) {
+    __shared__ i32x4 lds_v[C::kLds / 16];
+    lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
+    int64_t tm, tn;
+    if (!map.at(blockIdx.x, &tm, &tn)) return;
+    f32x4 acc[C::BL][C::BR];
+    tile_product<C>(acc, X, W, tm * C::TL, tn * (C::TR / 2), kbytes, lds);
+    const Place<C> at(tm, tn);
+    using H = HalfR<C>;
+    lds_f32* slice = (lds_f32*)(lds + at.wave * C::kSlice);
+    const int64_t n = X.rows, f = W.rows;
+    f32x4 z[H::BL][H::BR];
+#pragma unroll
+    for (int x = 0; x < H::BL; ++x)
+#pragma unroll
+        for (int b = 0; b < H::BR; ++b) {
+            __builtin_amdgcn_sched_barrier(0);  // all places' activations at once would not fit in registers
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t r = at.i0 + 16 * x + at.l16, j = at.f0 + 16 * b + 4 * at.g + i;
+                const float d = r < n && j < f ? static_cast<float>(dy[r * f + j]) : 0.f;
+                const float2 a = act::both<ACT, true>(acc[x][b][i]);
+                z[x][b][i] = d * acc[x][H::BR + b][i] * a.y;
+                acc[x][b][i] = d * a.x;
+            }
+        }
+    // whole pieces: ldz is a multiple of 8, and what lies behind f is not used
+    const auto same = [](float v) { return v; };
+    store_tile<H>(z, slice, dg, ldz, at.i0, at.f0, n, ldz, true, at.lane, same);
+#pragma unroll
+    for (int x = 0; x < H::BL; ++x)
+#pragma unroll
+        for (int b = 0; b < H::BR; ++b) z[x][b] = acc[x][b];
+    store_tile<H>(z, slice, du, ldz, at.i0, at.f0, n, ldz, true, at.lane, same);
+}
+
+// Sums of part `part` of a product in fp32, or its result.
+template <class C, class CT>
+__device__ __forceinline__ void store_result(const f32x4 (&acc)[C::BL][C::BR], lds_u8* lds, CT* c, float* sums, int64_t part,
+                                             int64_t rows, int64_t cols, int64_t tm, int64_t tn) {
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int64_t i0 = tm * C::TL + wave / C::WR * C::BL * 16, j0 = tn * C::TR + wave % C::WR * C::BR * 16;
+    lds_f32* slice = (lds_f32*)(lds + wave * C::kSlice);
+    const auto same = [](float v) { return v; };
+    if (sums)
+        store_tile<C>(acc, slice, sums + part * rows * cols, cols, i0, j0, rows, cols, true, lane, same);
+    else
+        store_tile<C>(acc, slice, c, cols, i0, j0, rows, cols, true, lane, same);
+}
+
+// The columns [k0, k0 + kb) of bytes of the summed axis that part `part` has.
+__device__ __forceinline__ int64_t part_of(int64_t kbytes, int64_t part_bytes, int64_t part, int64_t* k0) {
+    *k0 = part * part_bytes;
+    const int64_t kb = kbytes - *k0 < part_bytes ? kbytes - *k0 : part_bytes;
+    if (kb <= 0) *k0 = 0;
+    return kb > 0 ? kb : 0;
+}
+
+// dx = dg Wg + du Wu, or the part blockIdx.y of its sum over f.
+template <class C>
+__global__ __launch_bounds__(C::NT) void k_gated_dx(Operand Zg, Operand Zu, Operand Wg, Operand Wu, int64_t kbytes,
+                                                    int64_t part_bytes, Value<C::ELEM>* __restrict__ dx, float* __restrict__ sums,
+                                                    TileMap map) {
+    __shared__ i32x4 lds_v[C::kLds / 16];
+    lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
+    int64_t tm, tn, k0;
+    if (!map.at(blockIdx.x, &tm, &tn)) return;
+    const int64_t kb = part_of(kbytes, part_bytes, blockIdx.y, &k0);
+    Zg.data += k0, Zu.data += k0, Wg.data += k0 / 2 * Wg.ld, Wu.data += k0 / 2 * Wu.ld;
+    f32x4 acc[C::BL][C::BR];
+    tile_product<C>(acc, Zg, Wg, tm * C::TL, tn * C::TR, kb, lds);
+    tile_product<C>(acc, Zu, Wu, tm * C::TL, tn * C::TR, kb, lds, true);
+    store_result<C>(acc, lds, dx, sums, blockIdx.y, Zg.rows, Wg.rows, tm, tn);
+}
+
+// dWg = dg^T x (blockIdx.z 0) and dWu = du^T x (1), or the part blockIdx.y of
+// their sums over x's rows.
+template <class C>
+__global__ __launch_bounds__(C::NT) void k_gated_dw(Operand Zg, Operand Zu, Operand X, int64_t kbytes, int64_t part_bytes,
+                                                    Value<C::ELEM>* __restrict__ dwg, Value<C::ELEM>* __restrict__ dwu,
+                                                    float* __restrict__ sums, TileMap map) {
+    __shared__ i32x4 lds_v[C::kLds / 16];
+    lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
+    int64_t tm, tn, k0;
+    if (!map.at(blockIdx.x, &tn, &tm)) return;
+    const int64_t kb = part_of(kbytes, part_bytes, blockIdx.y, &k0);
+    const bool up = blockIdx.z != 0 || !dwg;
+    Operand Z = up ? Zu : Zg;
+    Z.data += k0 / 2 * Z.ld, X.data += k0 / 2 * X.ld;
+    f32x4 acc[C::BL][C::BR];
+    tile_product<C>(acc, Z, X, tm * C::TL, tn * C::TR, kb, lds);
+    store_result<C>(acc, lds, up ? dwu : dwg, sums, blockIdx.z * gridDim.y + blockIdx.y, Z.rows, X.rows, tm, tn);
+}
+
+// A result from the fp32 sums of its parts, eight at a time.
+template <class CT>
+__global__ __launch_bounds__(256) void k_join_parts(const float* __restrict__ sums, int parts, int64_t pieces, CT* __restrict__ out) {
+    typedef CT ct8 __attribute__((ext_vector_type(8)));
+    const int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (u >= pieces) return;
+    const f32x4* p = reinterpret_cast<const f32x4*>(sums) + 2 * u;
+    f32x4 s0 = p[0], s1 = p[1];
+    for (int i = 1; i < parts; ++i) s0 += p[2 * i * pieces], s1 += p[2 * i * pieces + 1];
+    ct8 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = static_cast<CT>(s0[i]), o[4 + i] = static_cast<CT>(s1[i]);
+    reinterpret_cast<ct8*>(out)[u] = o;
+}
+
+__global__ __launch_bounds__(256) void k_zero(i32x4* __restrict__ p, int64_t pieces) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; u < pieces; u += step) p[u] = i32x4{0, 0, 0, 0};
+}
+
+// Tiles of 256, 128 and 64 rows by 256.
+template <int ELEM> using Big = Config<ELEM, 0, 0, kNoScale, 4, 2, 4, 8>;
+template <int ELEM> using Mid = Config<ELEM, 0, 0, kNoScale, 2, 4, 4, 4>;
+template <int ELEM> using Low = Config<ELEM, 0, 0, kNoScale, 2, 4, 2, 4>;
+
+template <int ELEM, class F>
+hipError_t by_rows_of(int64_t tile_rows, F f) {
+    if (tile_rows == 64) return f(Low<ELEM>{});
+    if (tile_rows == 128) return f(Mid<ELEM>{});
+    return f(Big<ELEM>{});
+}
+template <class F>
+hipError_t by_act(int act, F f) {
+    if (act == SWZ_ACT_GELU) return f(std::integral_constant<int, SWZ_ACT_GELU>{});
+    if (act == SWZ_ACT_GELU_TANH) return f(std::integral_constant<int, SWZ_ACT_GELU_TANH>{});
+    return f(std::integral_constant<int, SWZ_ACT_SILU>{});
+}
+
+unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); }
+
+Operand operand(const void* p, int64_t ld, int64_t rows) {
+    return Operand{static_cast<const uint8_t*>(p), 2 * ld, rows, nullptr, 0, 0};
+}
+PairOperand pair_operand(const GatedJob& j) {
+    PairOperand w;
+    static_cast<Operand&>(w) = operand(j.wg, j.k, j.f);
+    w.second = static_cast<const uint8_t*>(j.wu);
+    return w;
+}
+
+template <int ELEM>
+hipError_t forward(const GatedJob& j, hipStream_t stream) {
+    using CT = Value<ELEM>;
+    return by_act(j.act, [&](auto a) {
+        constexpr int ACT = decltype(a)::value;
+        if (j.n <= kGatedFewRows) {
+            hipLaunchKernelGGL((k_gated_few<ELEM, ACT>), dim3(blocks_of(j.f, 16)), dim3(64 * kFewWaves), 0, stream,
+                               static_cast<const uint8_t*>(j.x), static_cast<const uint8_t*>(j.wg),
+                               static_cast<const uint8_t*>(j.wu), j.n, j.f, j.k, static_cast<CT*>(j.y), j.pre);
+            return hipGetLastError();
+        }
+        return by_rows_of<ELEM>(loss_tile_rows(j.n, (j.f + 127) / 128), [&](auto cfg) {
+            using C = Gated<decltype(cfg)>;
+            const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.f + C::TR / 2 - 1) / (C::TR / 2);
+            const TileMap map = TileMap::make(tm, tn);
+            const bool vec = j.f % 8 == 0 && reinterpret_cast<uintptr_t>(j.y) % 16 == 0 && reinterpret_cast<uintptr_t>(j.pre) % 16 == 0;
+            hipLaunchKernelGGL((k_gated<C, ACT>), dim3(map.grid), dim3(C::NT), 0, stream, operand(j.x, j.k, j.n), pair_operand(j),
+                               2 * j.k, static_cast<CT*>(j.y), j.pre, vec, map);
+            return hipGetLastError();
+        });
+    });
+}
+
+template <int ELEM>
+hipError_t backward(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
+    using CT = Value<ELEM>;
+    auto* ws = static_cast<uint8_t*>(j.ws);
+    auto* dg = reinterpret_cast<CT*>(ws + p.dg);
+    auto* du = reinterpret_cast<CT*>(ws + p.du);
+    auto* sums = reinterpret_cast<float*>(ws + p.sums);
+    const int64_t ldz = p.ldz;
+    hipError_t e = by_act(j.act, [&](auto a) {
+        constexpr int ACT = decltype(a)::value;
+        if (j.pre) {
+            const dim3 grid(blocks_of(j.f, 256), static_cast<unsigned>(j.n < 16384 ? j.n : 16384));
+            hipLaunchKernelGGL((k_gated_dz<CT, ACT>), grid, dim3(256), 0, stream, j.pre, static_cast<const CT*>(j.dy), j.n, j.f,
+                               ldz, dg, du);
+            return hipGetLastError();
+        }
+        return by_rows_of<ELEM>(loss_tile_rows(j.n, (j.f + 127) / 128), [&](auto cfg) {
+            using C = Gated<decltype(cfg)>;
+            const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.f + C::TR / 2 - 1) / (C::TR / 2);
+            const TileMap map = TileMap::make(tm, tn);
+            hipLaunchKernelGGL((k_gated_again_dz<C, ACT>), dim3(map.grid), dim3(C::NT), 0, stream, operand(j.x, j.k, j.n),
+                               pair_operand(j), 2 * j.k, static_cast<const CT*>(j.dy), ldz, dg, du, map);
+            return hipGetLastError();
+        });
+    });
+    const auto join = [&](const float* from, int64_t parts, int64_t values, void* out) {
+        hipLaunchKernelGGL(k_join_parts<CT>, dim3(blocks_of(values / 8, 256)), dim3(256), 0, stream, from, static_cast<int>(parts),
+                           values / 8, static_cast<CT*>(out));
+        return hipGetLastError();
+    };
+    if (e == hipSuccess && j.dx) {
+        e = by_rows_of<ELEM>(p.dx_rows, [&](auto cfg) {
+            using C = Across<decltype(cfg), false, true>;
+            const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
+            const TileMap map = TileMap::make(tm, tn);
+            const int64_t part_bytes = ((2 * j.f + 127) / 128 + p.dx_parts - 1) / p.dx_parts * 128;
+            hipLaunchKernelGGL(k_gated_dx<C>, dim3(map.grid, static_cast<unsigned>(p.dx_parts)), dim3(C::NT), 0, stream,
+                               operand(dg, ldz, j.n), operand(du, ldz, j.n), operand(j.wg, j.k, j.k), operand(j.wu, j.k, j.k),
+                               2 * j.f, part_bytes, static_cast<CT*>(j.dx), p.dx_parts > 1 ? sums : nullptr, map);
+            return hipGetLastError();
+        });
+        if (e == hipSuccess && p.dx_parts > 1) e = join(sums, p.dx_parts, j.n * j.k, j.dx);
+    }
+    if (e == hipSuccess && (j.dwg || j.dwu)) {
+        const unsigned both = j.dwg && j.dwu ? 2 : 1;
+        e = by_rows_of<ELEM>(p.dw_rows, [&](auto cfg) {
+            using C = Across<decltype(cfg), true, true>;
+            const int64_t tm = (j.f + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
+            const TileMap map = TileMap::make(tn, tm);
+            const int64_t part_bytes = ((2 * j.n + 127) / 128 + p.dw_parts - 1) / p.dw_parts * 128;
+            hipLaunchKernelGGL(k_gated_dw<C>, dim3(map.grid, static_cast<unsigned>(p.dw_parts), both), dim3(C::NT), 0, stream,
+                               operand(dg, ldz, j.f), operand(du, ldz, j.f), operand(j.x, j.k, j.k), 2 * j.n, part_bytes,
+                               static_cast<CT*>(j.dwg), static_cast<CT*>(j.dwu), p.dw_parts > 1 ? sums : nullptr, map);
+            return hipGetLastError();
+        });
+        if (p.dw_parts > 1) {
+            const int64_t one = p.dw_parts * j.f * j.k;
+            if (e == hipSuccess && j.dwg) e = join(sums, p.dw_parts, j.f * j.k, j.dwg);
+            if (e == hipSuccess && j.dwu) e = join(sums + (both == 2 ? one : 0), p.dw_parts, j.f * j.k, j.dwu);
+        }
+    }
+    return e;
+}
+
+}  // namespace
+
+hipError_t launch_gated(const GatedJob& j, hipStream_t stream) {
+    return j.bf16 ? forward<kBf16>(j, stream) : forward<kF16>(j, stream);
+}
+
+hipError_t launch_gated_grad(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
+    if (j.n == 0) {  // no rows: the weights' gradients are zero (f k is a multiple of 8)
+        for (void* w : {j.dwg, j.dwu}) {
+            const int64_t pieces = j.f * j.k / 8;
+            if (w)
+                hipLaunchKernelGGL(k_zero, dim3(pieces > 65536 * 256 ? 65536u : blocks_of(pieces, 256)), dim3(256), 0, stream,
+                                   static_cast<i32x4*>(w), pieces);
+        }
+        return hipGetLastError();
+    }
+    return j.bf16 ? backward<kBf16>(j, p, stream) : backward<kF16>(j, p, stream);
+}
+
+}  // namespace swz

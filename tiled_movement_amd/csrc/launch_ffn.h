@@ -1,0 +1,93 @@
+// Launchers of the feed-forward calls: the gated block, 4-bit weights, and the
+// gradients' norm.  Weak, so that the host code also links without kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "launch.h"
+#include "swz.h"
+
+namespace swz {
+
+#define SWZ_LAUNCHER __attribute__((weak)) hipError_t
+
+// swz_gated and its gradients.
+struct GatedJob {
+    const void *x, *wg, *wu;  // bf16 or fp16 [n][k], [f][k]
+    bool bf16;
+    int act;  // enum swz_act
+    int64_t n, f, k;
+    void* y;
+    float* pre;  // [2][n][f] or nullptr; the gradient reads it
+    const void* dy;
+    void *dx, *dwg, *dwu;  // each may be nullptr
+    void* ws;
+};
+// Workspace of the gradient: byte offsets, the pitch of dg and du in elements,
+// and for the products the rows of their tiles and the parts that their sums are
+// split into.
+struct GatedPlan {
+    int64_t dg, du, sums, bytes;
+    int64_t ldz, dx_rows, dx_parts, dw_rows, dw_parts;
+};
+constexpr int64_t kGatedFewRows = 16;
+SWZ_LAUNCHER launch_gated(const GatedJob& job, hipStream_t stream);
+SWZ_LAUNCHER launch_gated_grad(const GatedJob& job, const GatedPlan& plan, hipStream_t stream);
+
+// swz_quant_w4 and swz_dequant_w4.
+struct QuantW4Job {
+    const void* w;
+    int32_t w_type;  // enum swz_x_type
+    bool bf16;       // of the scales (and the result of the way back)
+    int64_t n, k;
+    int group;
+    void *q, *scale;
+    uint8_t* zero;  // or nullptr
+};
+SWZ_LAUNCHER launch_quant_w4(const QuantW4Job& job, hipStream_t stream);
+
+struct WeightsW4 {
+    const uint8_t* q;     // [n][k / 2]
+    const void* scale;    // x's type [n][ceil(k / group)]
+    const uint8_t* zero;  // the same, or nullptr: 8
+};
+SWZ_LAUNCHER launch_dequant_w4(const WeightsW4& w, bool bf16, int64_t n, int64_t k, int group, void* out, hipStream_t stream);
+
+// swz_gemm_w4 (act < 0) and swz_gated_w4 (both weights).
+struct GemmW4Job {
+    const void* x;  // [m][k]
+    bool bf16;
+    int64_t m, n, k;
+    int group, act;
+    WeightsW4 w[2];
+    void* c;  // [m][n]
+};
+SWZ_LAUNCHER launch_gemm_w4(const GemmW4Job& job, hipStream_t stream);
+
+// swz_grad_norm (out == nullptr) and swz_clip_grads: tensors by the list.
+struct NormJob {
+    const void* const* data;
+    void* const* out;
+    const int64_t* numel;
+    const int32_t* type;  // enum swz_x_type
+    int32_t count;
+    bool clip;
+    float max_norm;
+    float* norm;  // [1], or [2] with the factor
+    double* ws;
+};
+// A launch takes up to kNormTensors tensors and runs at most kNormBlocks
+// workgroups, each of which leaves a partial sum; work goes by chunks of
+// kNormPieces pieces of 16 bytes, from the boundary at or before a tensor's
+// start.
+constexpr int kNormTensors = 64;
+constexpr int64_t kNormPieces = 2048, kNormBlocks = 2048;
+inline int64_t norm_chunks(const void* p, int64_t numel, int32_t type) {
+    const int64_t es = type == SWZ_X_F32 ? 4 : 2, per = 16 / es;
+    const int64_t skew = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) % 16) / es;
+    return ((skew + numel + per - 1) / per + kNormPieces - 1) / kNormPieces;
+}
+SWZ_LAUNCHER launch_norm(const NormJob& job, hipStream_t stream);
+
+}  // namespace swz

@@ -64,6 +64,12 @@ struct Operand {
     int scale_shift;      // 0: a scale per row, 7: per 128 rows
 };
 
+// The two right operands of a gated product, of equal sizes (`data` and
+// `second`), whose rows a Gated configuration's tile holds in turn.
+struct PairOperand : Operand {
+    const uint8_t* second;
+};
+
 template <int ELEM_, int LT_, int RT_, int SC_, int WL_, int WR_, int BL_, int BR_>
 struct Config {
     static constexpr int ELEM = ELEM_, LT = LT_, RT = RT_, SC = SC_;
@@ -89,9 +95,25 @@ struct Config {
     static constexpr int kPitch = 16 * BR + 4;
     static constexpr int kSlice = 16 * kPitch * 4;
     static constexpr int kLds = kMain > WL * WR * kSlice ? kMain : WL * WR * kSlice;
+    static constexpr bool kPair = false, kLAcross = false, kRAcross = false;
     static_assert(NBUF >= 2, "two stages fit in LDS");
     static_assert(TL * 8 % NT == 0 && TR * 8 % NT == 0 && NT % 128 == 0, "the fills split evenly");
     static_assert(kLds <= 160 * 1024, "the stages fit in LDS");
+};
+
+// Two right operands: each wave's 16 BR rows of the R tile are 8 BR of the
+// first and the same 8 BR of the second, so that a lane holds both products of
+// its places and the epilogue needs nobody else's.
+template <class C>
+struct Gated : C {
+    static constexpr bool kPair = true;
+};
+// Two-byte operands whose rows run along the summed axis: L (R) is
+// [k][rows] with pitch ld, as the other products of a layer need them.  Their
+// tiles come and leave by AcrossFill and read_frag_across.
+template <class C, bool L_, bool R_>
+struct Across : C {
+    static constexpr bool kLAcross = L_, kRAcross = R_;
 };
 
 __device__ __forceinline__ void wg_barrier() {
@@ -161,6 +183,82 @@ struct Fill {
     }
 };
 
+// The same of a Gated configuration's R tile, from row0 of both operands on:
+// rows 2 G w + r of the tile are row G w + r of the first operand, rows 2 G w +
+// G + r of the second (r < G = 8 BR).  A wave's 8 rows of a step are of one of
+// them, and two steps are whole turns or none, so which one goes by the step's
+// parity and the wave.
+template <int T, int NT, int G>
+struct PairFill {
+    static constexpr int Q = T * 8 / NT;
+    static_assert(NT / 8 % G == 0 && G % 8 == 0, "which operand goes by the wave and the step's parity");
+    const uint8_t* base[2];
+    uint32_t off[Q];
+    uint32_t chunk16;
+    __device__ __forceinline__ void init(const PairOperand& o, int64_t row0, int t) {
+        const int first = __builtin_amdgcn_readfirstlane(t / 64) * 8;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) base[p] = (((first + NT / 8 * p) / G) & 1 ? o.second : o.data) + row0 * o.ld;
+        const uint32_t e = swz_slot(static_cast<uint32_t>(t));
+        chunk16 = 16 * (e % 8);
+        const int64_t left = o.rows - row0 - 1;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int tile_row = static_cast<int>(e / 8) + NT / 8 * q;
+            const int64_t r = tile_row / (2 * G) * G + tile_row % G;
+            off[q] = static_cast<uint32_t>((r < left ? r : left) * o.ld) + chunk16;
+        }
+    }
+    __device__ __forceinline__ void issue(int64_t stage, int64_t rem, lds_u8* dst, int wave) const {
+        const uint32_t back = static_cast<int64_t>(chunk16) < rem ? 0u : chunk16;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            __builtin_amdgcn_global_load_lds(base[q & 1] + stage * 128 + (off[q] - back), dst + 16 * (64 * wave + NT * q), 16, 0, 0);
+    }
+};
+
+// The same of an operand whose rows run along k: 64 of them a stage, 2 T
+// bytes each.  A transposing read takes 32 bytes (16 values of the tile's
+// rows) of each of 16 of these, 8 g + j with g, j < 4 (j + 4 for the other
+// half), and 32 lanes of it are served at once; so the 32-byte granule of a row
+// is XORed with j and g's low bit, and 32 lanes fall on 8 different granules of
+// the 256 bytes of banks.  Rows of 128 bytes come two to 256 bytes: there the
+// row's low bit already parts them.
+template <int T, int NT>
+struct AcrossFill {
+    static constexpr int Q = T * 8 / NT, PER = T / 8;  // 16-byte chunks of a row
+    static constexpr int kRowsOfStep = NT / PER;
+    static_assert(kRowsOfStep % 16 == 0, "the swizzle is the same in every step");
+    static __device__ __forceinline__ uint32_t turn(uint32_t k) {
+        return T >= 128 ? (k & 3u) | ((k >> 1) & 4u) : ((k >> 1) & 1u) | ((k >> 2) & 2u);
+    }
+    const uint8_t* base;
+    uint32_t row, row_off, step_off, col_off;
+    int64_t stage_bytes;
+    __device__ __forceinline__ void init(const Operand& o, int64_t row0, int t) {
+        row = static_cast<uint32_t>(t) / PER;
+        uint32_t c = (static_cast<uint32_t>(t) % PER) ^ (turn(row) << 1);
+        base = o.data + 2 * row0;
+        // chunks behind the operand's last are read as its last one; their results are not stored
+        const int64_t last = (o.rows - row0 - 1) / 8;
+        c = static_cast<int64_t>(c) < last ? c : static_cast<uint32_t>(last);
+        row_off = row * static_cast<uint32_t>(o.ld);
+        step_off = kRowsOfStep * static_cast<uint32_t>(o.ld);
+        col_off = 16 * c;
+        stage_bytes = 64 * o.ld;
+    }
+    // Rows behind the last are read as the stage's first (masked when used).
+    __device__ __forceinline__ void issue(int64_t stage, int64_t rem, lds_u8* dst, int wave) const {
+        const uint8_t* b = base + stage * stage_bytes;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const uint32_t r = row_off + step_off * q;
+            __builtin_amdgcn_global_load_lds(b + ((2 * static_cast<int64_t>(row + kRowsOfStep * q) < rem ? r : 0u) + col_off),
+                                             dst + 16 * (64 * wave + NT * q), 16, 0, 0);
+        }
+    }
+};
+
 // 2^(b - 127) of the low byte of a word; 255 is NaN.
 __device__ __forceinline__ float e8m0_value(uint32_t w) {
     const uint32_t b = w & 255u;
@@ -169,15 +267,17 @@ __device__ __forceinline__ float e8m0_value(uint32_t w) {
 
 template <class C>
 struct Stager {
-    Fill<C::TL, C::NT> fl;
-    Fill<C::TR, C::NT> fr;
+    static_assert(!(C::kPair && C::kRAcross), "gated operands run along k");
+    std::conditional_t<C::kLAcross, AcrossFill<C::TL, C::NT>, Fill<C::TL, C::NT>> fl;
+    std::conditional_t<C::kPair, PairFill<C::TR, C::NT, 8 * C::BR>,
+                       std::conditional_t<C::kRAcross, AcrossFill<C::TR, C::NT>, Fill<C::TR, C::NT>>> fr;
     const uint8_t* sp[C::NS ? C::NS : 1];  // this thread's scales, advanced stage by stage
     uint32_t sv[C::NS ? C::NS : 1];
     int t, wave;
     int64_t kbytes;
 
-    __device__ __forceinline__ void init(const Operand& L, const Operand& R, int64_t l0, int64_t r0, int64_t kb,
-                                         int tid) {
+    template <class OR>
+    __device__ __forceinline__ void init(const Operand& L, const OR& R, int64_t l0, int64_t r0, int64_t kb, int tid) {
         t = tid;
         wave = __builtin_amdgcn_readfirstlane(tid / 64);
         kbytes = kb;
@@ -216,7 +316,7 @@ struct Stager {
     // number of loads into LDS and nothing else: the aligned word that holds
     // an E8M0 scale's byte (in its page, and what else it holds is not used),
     // or the fp32 scale.
-    static constexpr int kLoads = Fill<C::TL, C::NT>::Q + Fill<C::TR, C::NT>::Q + (C::SC == kNoScale ? 0 : C::NS);
+    static constexpr int kLoads = Fill<C::TL, C::NT>::Q + Fill<C::TR, C::NT>::Q + (C::SC == kNoScale ? 0 : C::NS);  // of any fill
     __device__ __forceinline__ void issue_deep(int64_t s, lds_u8* buf) const {
         fl.issue(s, kbytes - s * 128, buf, wave);
         fr.issue(s, kbytes - s * 128, buf + C::TL * 128, wave);
@@ -271,6 +371,50 @@ __device__ __forceinline__ i32x8 read_frag(const lds_u8* tile, uint32_t at, uint
         hi = keep_bytes(hi, rem - 16 * g - 64);
     }
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// The same of a tile of rows along k: block `block` of the tile's T rows.  at:
+// this lane's byte for block 0 (across_at).  Each transposing read of 8 bytes a
+// lane takes four rows of k for 16 rows of the tile; two of them are the
+// instruction's 8 values of k, in the order that read_frag has.
+template <int T>
+__device__ __forceinline__ uint32_t across_at(int lane) {
+    const uint32_t k = 8 * (lane / 16) + lane % 16 / 4;
+    return k * 2 * T + 32 * AcrossFill<T, 16 * (T / 8)>::turn(k) + 8 * (lane % 4);
+}
+template <bool TAIL, int T>
+__device__ __forceinline__ i32x8 read_frag_across(const lds_u8* tile, uint32_t at, int block, int g, int rem) {
+    typedef short i16x4 __attribute__((ext_vector_type(4)));
+    typedef int i32x2 __attribute__((ext_vector_type(2)));
+    typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+    // the turn moves the granule's bits within the low 8 (4 granules: 4) of a row only
+    constexpr int M = T >= 128 ? 8 : 4;
+    const lds_u8* p = tile + block / M * M * 32 + (at ^ (32u * (block % M)));
+    i32x2 v[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+        v[h] = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + (h / 2 * 32 + h % 2 * 4) * 2 * T)));
+    i32x4 lo = __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3), hi = __builtin_shufflevector(v[2], v[3], 0, 1, 2, 3);
+    if constexpr (TAIL) {
+        lo = keep_bytes(lo, rem - 16 * g);
+        hi = keep_bytes(hi, rem - 16 * g - 64);
+    }
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+// Block x (y) of this wave's rows of the L (R) tile.
+template <class C, bool TAIL>
+__device__ __forceinline__ i32x8 frag_l(const lds_u8* buf, uint32_t lat, int x, int wl, int g, int rem) {
+    if constexpr (C::kLAcross)
+        return read_frag_across<TAIL, C::TL>(buf, lat, wl * C::BL + x, g, rem);
+    else
+        return read_frag<TAIL>(buf, lat, 2048 * x, g, rem);
+}
+template <class C, bool TAIL>
+__device__ __forceinline__ i32x8 frag_r(const lds_u8* buf, uint32_t rat, int y, int wr, int g, int rem) {
+    if constexpr (C::kRAcross)
+        return read_frag_across<TAIL, C::TR>(buf + C::TL * 128, rat, wr * C::BR + y, g, rem);
+    else
+        return read_frag<TAIL>(buf + C::TL * 128, rat, 2048 * y, g, rem);
 }
 
 template <class C, int OL, int OR>
@@ -477,10 +621,10 @@ __device__ __forceinline__ void stage_products(f32x4 (&acc)[C::BL][C::BR], const
         const int g = lane / 16;
         i32x8 lf[C::BL];
 #pragma unroll
-        for (int x = 0; x < C::BL; ++x) lf[x] = read_frag<TAIL>(buf, lat, 2048 * x, g, rem);
+        for (int x = 0; x < C::BL; ++x) lf[x] = frag_l<C, TAIL>(buf, lat, x, wl, g, rem);
 #pragma unroll
         for (int y = 0; y < C::BR; ++y) {
-            const i32x8 rf = read_frag<TAIL>(buf + C::TL * 128, rat, 2048 * y, g, rem);
+            const i32x8 rf = frag_r<C, TAIL>(buf, rat, y, wr, g, rem);
             const f32x4 rs = sc.rvec(sbuf, wr, y, lane);
 #pragma unroll
             for (int x = 0; x < C::BL; ++x)
@@ -530,11 +674,11 @@ __device__ __forceinline__ void pingpong(f32x4 (&acc)[C::BL][C::BR], Stager<C>& 
     i32x8 l[2][2], r[2][4];
     auto read_r = [&](const lds_u8* buf, int h) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) r[h][y] = read_frag<false>(buf + C::TL * 128, rat, 2048 * (4 * h + y), g, 128);
+        for (int y = 0; y < 4; ++y) r[h][y] = frag_r<C, false>(buf, rat, 4 * h + y, wr, g, 128);
     };
     auto read_l = [&](const lds_u8* buf, int h) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) l[h][x] = read_frag<false>(buf, lat, 2048 * (2 * h + x), g, 128);
+        for (int x = 0; x < 2; ++x) l[h][x] = frag_l<C, false>(buf, lat, 2 * h + x, wl, g, 128);
     };
     // stage 0 has landed; stage 1 (or stage 0 again) goes to the other buffer
     constexpr bool kSplit = C::ELEM == kF8;
@@ -590,24 +734,28 @@ __device__ __forceinline__ void pingpong(f32x4 (&acc)[C::BL][C::BR], Stager<C>& 
 }
 
 // The whole product of one tile: rows l0 .. of L against rows r0 .. of R over
-// kbytes bytes of k.  Sums run over k in increasing order.
-template <class C>
-__device__ __forceinline__ void tile_product(f32x4 (&acc)[C::BL][C::BR], const Operand& L, const Operand& R, int64_t l0,
-                                             int64_t r0, int64_t kbytes, lds_u8* lds) {
+// kbytes bytes of k (of rows along k: two for each).  Sums run over k in
+// increasing order.  add: to what acc holds.
+template <class C, class OR>
+__device__ __forceinline__ void tile_product(f32x4 (&acc)[C::BL][C::BR], const Operand& L, const OR& R, int64_t l0,
+                                             int64_t r0, int64_t kbytes, lds_u8* lds, bool add = false) {
     const int t = threadIdx.x, lane = t % 64;
     const int wave = __builtin_amdgcn_readfirstlane(t / 64);
     const int wl = wave / C::WR, wr = wave % C::WR;
+    if (!add) {
 #pragma unroll
-    for (int x = 0; x < C::BL; ++x)
+        for (int x = 0; x < C::BL; ++x)
 #pragma unroll
-        for (int y = 0; y < C::BR; ++y) acc[x][y] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int y = 0; y < C::BR; ++y) acc[x][y] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
     const int64_t stages = (kbytes + 127) / 128, full = kbytes / 128;
     if (stages == 0) return;
     Stager<C> st;
     st.init(L, R, l0, r0, kbytes, t);
     const int l16 = lane % 16, rem = static_cast<int>(kbytes - full * 128);
     const uint32_t at = l16 * 128 + 16 * ((lane / 16) ^ ((l16 >> 1) & 7));
-    const uint32_t lat = wl * C::BL * 2048 + at, rat = wr * C::BR * 2048 + at;
+    const uint32_t lat = C::kLAcross ? across_at<C::TL>(lane) : wl * C::BL * 2048 + at;
+    const uint32_t rat = C::kRAcross ? across_at<C::TR>(lane) : wr * C::BR * 2048 + at;
     LaneScales<C> sc;
     if constexpr (C::kSlots) {
         lds_u8* sbufs = lds + 2 * C::kBuf;
