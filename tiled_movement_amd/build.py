@@ -33,6 +33,7 @@ SOURCES = [
     "kernels_loss.hip",
     "kernels_gated.hip",
     "kernels_w4.hip",
+    "kernels_w4_gemm.hip",
     "kernels_norm.hip",
     "kernels_map.hip",
     "kernels_rows.hip",
