@@ -140,17 +140,42 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(const uint8_t* __r
     y[i * f + j] = static_cast<Value<ELEM>>(act::both<ACT, false>(z[0]).x * z[1]);
 }
 
-// dg and du ([n][ldz], x's type) from the kept g and u.  Rows by blockIdx.y.
+// dg and du ([n][ldz], x's type) from the kept g and u, eight places a thread;
+// rows by blockIdx.y.  Bound by the bytes.  Rows of an f that is no multiple of 8
+// begin at any element: their pieces are loaded as they lie, and the last one by
+// elements.
 template <class CT, int ACT>
 __global__ __launch_bounds__(256) void k_gated_dz(const float* __restrict__ pre, const CT* __restrict__ dy, int64_t n, int64_t f,
                                                   int64_t ldz, CT* __restrict__ dg, CT* __restrict__ du) {
-    const int64_t j = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    typedef float f32x8 __attribute__((ext_vector_type(8), aligned(4)));
+    typedef CT ct8 __attribute__((ext_vector_type(8)));
+    typedef CT ct8_any __attribute__((ext_vector_type(8), aligned(2)));
+    const int64_t j = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
     if (j >= f) return;
+    const int here = f - j < 8 ? static_cast<int>(f - j) : 8;
     for (int64_t i = blockIdx.y; i < n; i += gridDim.y) {
-        const float g = pre[i * f + j], u = pre[(n + i) * f + j], d = static_cast<float>(dy[i * f + j]);
-        const float2 a = act::both<ACT, true>(g);
-        dg[i * ldz + j] = static_cast<CT>(d * u * a.y);
-        du[i * ldz + j] = static_cast<CT>(d * a.x);
+        f32x8 g = 0.f, u = 0.f;
+        ct8_any d = 0;
+        if (here == 8) {
+            g = *reinterpret_cast<const f32x8*>(pre + i * f + j);
+            u = *reinterpret_cast<const f32x8*>(pre + (n + i) * f + j);
+            d = *reinterpret_cast<const ct8_any*>(dy + i * f + j);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < here) g[e] = pre[i * f + j + e], u[e] = pre[(n + i) * f + j + e], d[e] = dy[i * f + j + e];
+        }
+        ct8 zg, zu;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float2 a = act::both<ACT, true>(g[e]);
+            const float de = static_cast<float>(d[e]);
+            zg[e] = static_cast<CT>(de * u[e] * a.y);
+            zu[e] = static_cast<CT>(de * a.x);
+        }
+        // whole pieces: ldz is a multiple of 8, and what lies behind f is not used
+        *reinterpret_cast<ct8*>(dg + i * ldz + j) = zg;
+        *reinterpret_cast<ct8*>(du + i * ldz + j) = zu;
     }
 }
 
@@ -337,7 +362,7 @@ hipError_t backward(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
     hipError_t e = by_act(j.act, [&](auto a) {
         constexpr int ACT = decltype(a)::value;
         if (j.pre) {
-            const dim3 grid(blocks_of(j.f, 256), static_cast<unsigned>(j.n < 16384 ? j.n : 16384));
+            const dim3 grid(blocks_of(j.f, 2048), static_cast<unsigned>(j.n < 16384 ? j.n : 16384));
             hipLaunchKernelGGL((k_gated_dz<CT, ACT>), grid, dim3(256), 0, stream, j.pre, static_cast<const CT*>(j.dy), j.n, j.f,
                                ldz, dg, du);
             return hipGetLastError();

@@ -47,19 +47,30 @@ __device__ __forceinline__ int tensor_of(const Pack& p, uint32_t chunk) {
     return lo;
 }
 
-// f(whole, first element, elements) for each of this thread's pieces of a chunk.
-template <int TYPE, class F>
-__device__ __forceinline__ void pieces_of(const uint8_t* in, int64_t numel, int64_t chunk, F f) {
-    constexpr int E = Kind<TYPE>::E;
-    constexpr int ES = 16 / E;
+// A thread's part of a chunk: all(first element of each of its kPer pieces,
+// whether it is the tensor's as a whole; another's place where not), and
+// edge(first element, elements) for a tensor's first and last piece where they are
+// not whole.  No load waits for a branch.
+constexpr int kPer = kNormPieces / 256;
+template <int TYPE, class A, class S>
+__device__ __forceinline__ void pieces_of(const uint8_t* in, int64_t numel, int64_t chunk, A all, S edge) {
+    constexpr int E = Kind<TYPE>::E, ES = 16 / E;
     const int64_t skew = static_cast<int64_t>(reinterpret_cast<uintptr_t>(in) % 16) / ES;
-    const int64_t pieces = (skew + numel + E - 1) / E, p0 = chunk * kNormPieces;
-    const int64_t end = p0 + kNormPieces < pieces ? p0 + kNormPieces : pieces;
-#pragma unroll 4
-    for (int64_t p = p0 + threadIdx.x; p < end; p += 256) {
-        const int64_t at = p * E - skew, lo = at < 0 ? 0 : at, hi = at + E < numel ? at + E : numel;
-        f(hi - lo == E, lo, static_cast<int>(hi - lo));
+    const int64_t p0 = chunk * kNormPieces, whole0 = skew ? 1 : 0, whole1 = (skew + numel) / E;  // whole pieces
+    if (whole0 < whole1) {
+        int64_t at[kPer];
+        bool valid[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int64_t p = p0 + 256 * i + threadIdx.x, q = p < whole0 ? whole0 : p < whole1 ? p : whole1 - 1;
+            valid[i] = p == q;
+            at[i] = q * E - skew;
+        }
+        all(at, valid);
     }
+    if (threadIdx.x == 0 && chunk == 0 && skew) edge(int64_t(0), static_cast<int>(numel < E - skew ? numel : E - skew));
+    if (threadIdx.x == 64 && whole1 >= whole0 && (skew + numel) % E && whole1 >= p0 && whole1 < p0 + kNormPieces)
+        edge(whole1 * E - skew, static_cast<int>((skew + numel) % E));
 }
 
 template <int TYPE>
@@ -69,21 +80,27 @@ __device__ __forceinline__ double squares(const uint8_t* in, int64_t numel, int6
     constexpr int E = Kind<TYPE>::E;
     const T* x = reinterpret_cast<const T*>(in);
     double s = 0.0;
-    pieces_of<TYPE>(in, numel, chunk, [&](bool whole, int64_t at, int n) {
-        if (whole) {
-            const V v = *reinterpret_cast<const V*>(x + at);
+    auto add = [](double& to, T v) {
+        const double d = static_cast<double>(static_cast<float>(v));
+        to = __builtin_fma(d, d, to);
+    };
+    pieces_of<TYPE>(
+        in, numel, chunk,
+        [&](const int64_t (&at)[kPer], const bool (&valid)[kPer]) {
+            V v[kPer];
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const double d = static_cast<double>(static_cast<float>(v[i]));
-                s = __builtin_fma(d, d, s);
+            for (int i = 0; i < kPer; ++i) v[i] = *reinterpret_cast<const V*>(x + at[i]);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                double part = 0.0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) add(part, v[i][e]);
+                s += valid[i] ? part : 0.0;
             }
-        } else {
-            for (int i = 0; i < n; ++i) {
-                const double d = static_cast<double>(static_cast<float>(x[at + i]));
-                s = __builtin_fma(d, d, s);
-            }
-        }
-    });
+        },
+        [&](int64_t at, int n) {
+            for (int i = 0; i < n; ++i) add(s, x[at + i]);
+        });
     return s;
 }
 
@@ -148,27 +165,38 @@ __device__ __forceinline__ void scale_chunk(const uint8_t* in, uint8_t* to, int6
     const T* x = reinterpret_cast<const T*>(in);
     T* o = reinterpret_cast<T*>(to);
     const bool alike = (reinterpret_cast<uintptr_t>(in) - reinterpret_cast<uintptr_t>(to)) % 16 == 0;
-    pieces_of<TYPE>(in, numel, chunk, [&](bool whole, int64_t at, int n) {
-        if (whole) {
-            const V v = *reinterpret_cast<const V*>(x + at);
-            V r;
+    auto one = [&](T v) { return factor == 1.f ? v : scaled<T>(v, factor); };
+    pieces_of<TYPE>(
+        in, numel, chunk,
+        [&](const int64_t (&at)[kPer], const bool (&valid)[kPer]) {
+            V v[kPer];
 #pragma unroll
-            for (int i = 0; i < E; ++i) r[i] = factor == 1.f ? v[i] : scaled<T>(v[i], factor);
-            if (alike) {
-                *reinterpret_cast<V*>(o + at) = r;
-            } else {
+            for (int i = 0; i < kPer; ++i) v[i] = __builtin_nontemporal_load(reinterpret_cast<const V*>(x + at[i]));
+            asm volatile("" ::: "memory");  // in place: nothing is read again behind a store
 #pragma unroll
-                for (int i = 0; i < E; ++i) o[at + i] = r[i];
+            for (int i = 0; i < kPer; ++i) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[i][e] = one(v[i][e]);
+                if (!valid[i]) continue;
+                if (alike) {
+                    __builtin_nontemporal_store(v[i], reinterpret_cast<V*>(o + at[i]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[at[i] + e] = v[i][e];
+                }
             }
-        } else {
-            for (int i = 0; i < n; ++i) o[at + i] = factor == 1.f ? x[at + i] : scaled<T>(x[at + i], factor);
-        }
-    });
+        },
+        [&](int64_t at, int n) {
+            for (int i = 0; i < n; ++i) o[at + i] = one(x[at + i]);
+        });
 }
 
+// Chunks from the last to the first: what the squares read last is still in the
+// 256 MB cache.
 __global__ __launch_bounds__(256) void k_scale(Pack p, const float* __restrict__ norm) {
     const float factor = norm[1];
-    for (uint32_t c = blockIdx.x; c < p.first[p.count]; c += gridDim.x) {
+    for (uint32_t i = blockIdx.x; i < p.first[p.count]; i += gridDim.x) {
+        const uint32_t c = p.first[p.count] - 1 - i;
         const int t = tensor_of(p, c);
         if (factor == 1.f && p.in[t] == p.out[t]) continue;
         const int64_t chunk = c - p.first[t];
@@ -181,36 +209,41 @@ __global__ __launch_bounds__(256) void k_scale(Pack p, const float* __restrict__
     }
 }
 
-// The launches of a list: f(pack, blocks).
+// The launches of a list, from its first tensor or from its last: f(pack, blocks).
 template <class F>
-hipError_t by_packs(const NormJob& j, F f) {
-    for (int32_t t = 0; t < j.count;) {
-        Pack p;
-        p.count = 0;
-        uint32_t chunks = 0;
-        for (; t < j.count && p.count < kNormTensors; ++t) {
-            if (j.numel[t] == 0) continue;
-            const int64_t c = norm_chunks(j.data[t], j.numel[t], j.type[t]);
-            p.in[p.count] = static_cast<const uint8_t*>(j.data[t]);
-            p.out[p.count] = static_cast<uint8_t*>(j.clip ? (j.out ? j.out[t] : const_cast<void*>(j.data[t])) : nullptr);
-            p.numel[p.count] = j.numel[t];
-            p.type[p.count] = static_cast<uint8_t>(j.type[t]);
-            p.first[p.count++] = chunks;
-            chunks += static_cast<uint32_t>(c);
-        }
-        if (p.count == 0) break;
+hipError_t by_packs(const NormJob& j, bool backwards, F f) {
+    Pack p;
+    p.count = 0;
+    uint32_t chunks = 0;
+    auto launch = [&] {
+        if (p.count == 0) return hipSuccess;
         p.first[p.count] = chunks;
         const hipError_t e = f(p, static_cast<unsigned>(chunks < kNormBlocks ? chunks : kNormBlocks));
+        p.count = 0;
+        chunks = 0;
+        return e;
+    };
+    for (int32_t i = 0; i < j.count; ++i) {
+        const int32_t t = backwards ? j.count - 1 - i : i;
+        if (j.numel[t] == 0) continue;
+        p.in[p.count] = static_cast<const uint8_t*>(j.data[t]);
+        p.out[p.count] = static_cast<uint8_t*>(j.clip ? (j.out ? j.out[t] : const_cast<void*>(j.data[t])) : nullptr);
+        p.numel[p.count] = j.numel[t];
+        p.type[p.count] = static_cast<uint8_t>(j.type[t]);
+        p.first[p.count++] = chunks;
+        chunks += static_cast<uint32_t>(norm_chunks(j.data[t], j.numel[t], j.type[t]));
+        if (p.count < kNormTensors) continue;
+        const hipError_t e = launch();
         if (e != hipSuccess) return e;
     }
-    return hipSuccess;
+    return launch();
 }
 
 }  // namespace
 
 hipError_t launch_norm(const NormJob& j, hipStream_t stream) {
     double* partial = j.ws;
-    hipError_t e = by_packs(j, [&](const Pack& p, unsigned blocks) {
+    hipError_t e = by_packs(j, false, [&](const Pack& p, unsigned blocks) {
         hipLaunchKernelGGL(k_squares, dim3(blocks), dim3(256), 0, stream, p, partial);
         partial += blocks;
         return hipGetLastError();
@@ -219,7 +252,7 @@ hipError_t launch_norm(const NormJob& j, hipStream_t stream) {
     hipLaunchKernelGGL(k_norm, dim3(1), dim3(1024), 0, stream, j.ws, partial - j.ws, j.max_norm, j.clip, j.norm);
     e = hipGetLastError();
     if (e != hipSuccess || !j.clip) return e;
-    return by_packs(j, [&](const Pack& p, unsigned blocks) {
+    return by_packs(j, true, [&](const Pack& p, unsigned blocks) {
         hipLaunchKernelGGL(k_scale, dim3(blocks), dim3(256), 0, stream, p, j.norm);
         return hipGetLastError();
     });

@@ -11,89 +11,172 @@ using Value = std::conditional_t<BF16, __bf16, _Float16>;
 unsigned blocks_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); }
 
 // ------------------------------------------------------------- quantizer
-// A lane has 8 consecutive values of a row, GROUP / 8 lanes a group.  Bound by
-// its bytes but for the divisions, which have to be exact: a 16-bit value is
-// often halfway between two codes.
+// v / s rounded to a whole number, ties to even, as the correctly rounded
+// quotient gives it, where |v / s| stays below 32; as the bits of kWhole + it (a
+// sum that holds no digits behind the point rounds so by itself).
+// 16-bit values are often halfway between two whole numbers (exactly: then one
+// step of Newton's iteration ends on the halfway point itself) and never within
+// 2^-12 of such a point without being on it, far more than the step's error.  fp32
+// values within 2^-17 of one, where a product by 1 / s could be on the other
+// side, are divided.  A division for each value would take longer than the bytes
+// (8192 x 4096 bf16: 28 us, 18 so).
+constexpr float kWhole = 12582912.f;  // 1.5 2^23
+template <bool HALF>
+struct Rounded {
+    float s, r, up;
+    __device__ __forceinline__ explicit Rounded(float scale) : s(scale), up(1.f) {
+        if (s < 0x1p-100f) up = 0x1p100f;  // 1 / s has to be a number; both are multiplied exactly
+        s *= up;
+        r = __builtin_amdgcn_rcpf(s);
+    }
+    __device__ __forceinline__ float quotient(float v) const {
+        v *= up;
+        const float q = v * r;
+        return HALF ? __builtin_fmaf(__builtin_fmaf(-q, s, v), r, q) : q;
+    }
+    // Whether a quotient may be on the wrong side.
+    __device__ __forceinline__ bool unsure(float q) const { return !HALF && !(fabsf(q - (q + kWhole - kWhole)) <= 0.5f - 0x1p-17f); }
+    __device__ __forceinline__ float divided(float v) const { return v * up / s; }
+};
+// A quotient cut to lo .. hi, whole numbers.
+__device__ __forceinline__ int whole_bits(float q, float lo, float hi) {
+    return __float_as_int(__builtin_amdgcn_fmed3f(q, lo, hi) + kWhole);
+}
+
+// A maximum (f) over aligned runs of LANES lanes, 16 at most: exchanges within
+// four lanes, and mirrored halves, which hold the same once the fours agree.
+template <int LANES, class T, class F>
+__device__ __forceinline__ T over_lanes(T v, F f) {
+    auto with = [&](auto ctrl) {
+        v = f(v, __builtin_bit_cast(T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), decltype(ctrl)::value, 0xf, 0xf, true)));
+    };
+    with(std::integral_constant<int, 0xb1>{});                         // quad_perm 1 0 3 2
+    with(std::integral_constant<int, 0x4e>{});                         // quad_perm 2 3 0 1
+    if constexpr (LANES > 4) with(std::integral_constant<int, 0x141>{});  // row_half_mirror
+    if constexpr (LANES > 8) with(std::integral_constant<int, 0x140>{});  // row_mirror
+    return v;
+}
+
+// The largest magnitude of 8 values as the bits of an fp32 number, where
+// infinities and NaN come out on top.
+template <class WT, class V>
+__device__ __forceinline__ uint32_t largest_bits(V x) {
+    if constexpr (sizeof(WT) == 2) {
+        typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+        const u16x8 m = __builtin_bit_cast(u16x8, x) & uint16_t(0x7fff);
+        uint16_t big = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = m[i] > big ? m[i] : big;
+        return __float_as_uint(static_cast<float>(__builtin_bit_cast(WT, big)));
+    } else {
+        uint32_t big = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = max(big, __float_as_uint(x[i]) & 0x7fffffffu);
+        return big;
+    }
+}
+
+// A thread has 8 consecutive values of a row, GROUP / 8 of them a group; 2^log_tx
+// threads along the row, the others in rows below.
 template <class WT, class ST, int GROUP, bool ZERO>
-__global__ __launch_bounds__(256) void k_quant_w4(const WT* __restrict__ w, int64_t n, int64_t k, int64_t groups,
+__global__ __launch_bounds__(256) void k_quant_w4(const WT* __restrict__ w, int64_t n, int64_t k, int64_t groups, int log_tx,
                                                   uint32_t* __restrict__ q, ST* __restrict__ scale, uint8_t* __restrict__ zero) {
     constexpr int LANES = GROUP / 8;
     typedef WT wt8 __attribute__((ext_vector_type(8), aligned(16)));
-    // the block's first group, then this thread's by 32 bits
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 / LANES), row0 = first / groups;
-    const uint64_t at = static_cast<uint64_t>(first - row0 * groups) + threadIdx.x / LANES;
-    const int64_t skip = static_cast<int64_t>(at / static_cast<uint64_t>(groups));
-    const int64_t row = row0 + skip, grp = static_cast<int64_t>(at) - skip * groups;
-    const int64_t col = grp * GROUP + threadIdx.x % LANES * 8;
-    const bool in = row < n && col < k;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (in) {
-        const wt8 x = *reinterpret_cast<const wt8*>(w + row * k + col);
+    const int tx = threadIdx.x & ((1 << log_tx) - 1), ty = threadIdx.x >> log_tx, down = 256 >> log_tx;
+    const int64_t piece = (static_cast<int64_t>(blockIdx.x) << log_tx) + tx, col = piece * 8;
+    for (int64_t row = static_cast<int64_t>(blockIdx.y) * down + ty; row - ty < n; row += static_cast<int64_t>(gridDim.y) * down) {
+        const bool in = row < n && col < k;
+        wt8 x = 0;
+        if (in) x = *reinterpret_cast<const wt8*>(w + row * k + col);
+        uint32_t big = largest_bits<WT>(x);
+        float lo = 0.f, hi = 0.f;
+        if constexpr (ZERO) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(x[i]);
-    }
-    // the largest magnitude by its bits, where infinities and NaN come out on top
-    uint32_t big = 0;
-    float lo = 0.f, hi = 0.f;
+            for (int i = 0; i < 8; ++i) lo = fminf(lo, static_cast<float>(x[i])), hi = fmaxf(hi, static_cast<float>(x[i]));
+        }
+        big = over_lanes<LANES>(big, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+        if constexpr (ZERO) {
+            lo = over_lanes<LANES>(lo, [](float a, float b) { return fminf(a, b); });
+            hi = over_lanes<LANES>(hi, [](float a, float b) { return fmaxf(a, b); });
+        }
+        float unrounded = ZERO ? (hi - lo) * (1.f / 15.f) : __uint_as_float(big) * (1.f / 7.f);
+        asm("" : "+v"(unrounded));  // rounded to fp32 first, not to fp16 at once by a mixed-precision multiply
+        ST st = static_cast<ST>(unrounded);
+        float s = static_cast<float>(st);
+        if (big >= 0x7f800000u || !(s < __builtin_inff())) {
+            s = __builtin_nanf("");
+            st = static_cast<ST>(s);
+        }
+        const bool some = s > 0.f;
+        const Rounded<sizeof(WT) == 2> over(some ? s : 1.f);
+        const int whole = __float_as_int(kWhole);
+        const int z = ZERO ? (some ? whole_bits(over.divided(-lo), 0.f, 15.f) - whole : 0) : 8;
+        const float least = static_cast<float>(-z), most = static_cast<float>(15 - z);
+        // codes are whole numbers plus z - whole, all taken off at once (modulo 2^32)
+        uint32_t word = static_cast<uint32_t>(z - whole) * 0x11111111u;
+        bool unsure = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        big = max(big, __float_as_uint(v[i]) & 0x7fffffffu);
-        if constexpr (ZERO) lo = fminf(lo, v[i]), hi = fmaxf(hi, v[i]);
-    }
-#pragma unroll
-    for (int d = 1; d < LANES; d *= 2) {
-        big = max(big, static_cast<uint32_t>(__shfl_xor(static_cast<int>(big), d)));
-        if constexpr (ZERO) lo = fminf(lo, __shfl_xor(lo, d)), hi = fmaxf(hi, __shfl_xor(hi, d));
-    }
-    float unrounded = ZERO ? (hi - lo) * (1.f / 15.f) : __uint_as_float(big) * (1.f / 7.f);
-    asm("" : "+v"(unrounded));  // rounded to fp32 first, not to fp16 at once by a mixed-precision multiply
-    ST st = static_cast<ST>(unrounded);
-    float s = static_cast<float>(st);
-    if (big >= 0x7f800000u || !(s < __builtin_inff())) {
-        s = __builtin_nanf("");
-        st = static_cast<ST>(s);
-    }
-    const bool some = s > 0.f;
-    const float z = ZERO ? (some ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 0.f) : 8.f;
-    uint32_t word = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float c = some ? fminf(fmaxf(rintf(v[i] / s) + z, 0.f), 15.f) : z;
-        word |= static_cast<uint32_t>(c) << (4 * i);
-    }
-    if (!in) return;
-    q[(row * k + col) / 8] = word;
-    if (threadIdx.x % LANES == 0) {
-        scale[row * groups + grp] = st;
-        if constexpr (ZERO) zero[row * groups + grp] = static_cast<uint8_t>(z);
+        for (int i = 0; i < 8; ++i) {
+            const float v = over.quotient(static_cast<float>(x[i]));
+            unsure |= over.unsure(v);
+            word += static_cast<uint32_t>(whole_bits(v, least, most)) << (4 * i);
+        }
+        if (unsure) {
+            word = static_cast<uint32_t>(z - whole) * 0x11111111u;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i)
+                word += static_cast<uint32_t>(whole_bits(over.divided(static_cast<float>(w[row * k + col + i])), least, most)) << (4 * i);
+        }
+        if (!some) word = static_cast<uint32_t>(z) * 0x11111111u;
+        if (!in) continue;
+        q[(row * k + col) / 8] = word;
+        if (tx % LANES == 0) {
+            scale[row * groups + piece / LANES] = st;
+            if constexpr (ZERO) zero[row * groups + piece / LANES] = static_cast<uint8_t>(z);
+        }
     }
 }
 
 // ------------------------------------------------------------ and back
 template <bool BF16>
-__global__ __launch_bounds__(256) void k_dequant_w4(WeightsW4 w, int64_t k8, int64_t pieces, int group8, int64_t groups,
+__global__ __launch_bounds__(256) void k_dequant_w4(WeightsW4 w, int64_t n, int64_t k8, int log_group8, int64_t groups, int log_tx,
                                                     Value<BF16>* __restrict__ out) {
     typedef Value<BF16> v8 __attribute__((ext_vector_type(8)));
-    const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; u < pieces; u += step) {
-        const int64_t row = u / k8, at = row * groups + (u - row * k8) / group8;
-        const uint32_t word = reinterpret_cast<const uint32_t*>(w.q)[u];
+    const int tx = threadIdx.x & ((1 << log_tx) - 1), ty = threadIdx.x >> log_tx, down = 256 >> log_tx;
+    const int64_t piece = (static_cast<int64_t>(blockIdx.x) << log_tx) + tx;
+    if (piece >= k8) return;
+    for (int64_t row = static_cast<int64_t>(blockIdx.y) * down + ty; row < n; row += static_cast<int64_t>(gridDim.y) * down) {
+        const int64_t at = row * groups + (piece >> log_group8);
+        const uint32_t word = reinterpret_cast<const uint32_t*>(w.q)[row * k8 + piece];
         const float s = static_cast<float>(static_cast<const Value<BF16>*>(w.scale)[at]);
         const float z = w.zero ? static_cast<float>(w.zero[at]) : 8.f;
         v8 o;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            o[i] = static_cast<Value<BF16>>((static_cast<float>((word >> (4 * i)) & 15u) - z) * s);
-        reinterpret_cast<v8*>(out)[u] = o;
+        for (int i = 0; i < 8; ++i) o[i] = static_cast<Value<BF16>>((static_cast<float>((word >> (4 * i)) & 15u) - z) * s);
+        __builtin_nontemporal_store(o, reinterpret_cast<v8*>(out) + row * k8 + piece);
     }
 }
 
+// A grid of 256 threads over rows of `pieces` pieces: 2^log_tx threads along a
+// row (16 at least: a group stays in a wave), the others in rows below.
+struct RowGrid {
+    int log_tx = 4;
+    dim3 grid;
+    RowGrid(int64_t n, int64_t pieces) {
+        while (log_tx < 8 && (int64_t(1) << log_tx) < pieces) ++log_tx;
+        const int64_t down = (n + (256 >> log_tx) - 1) / (256 >> log_tx);
+        grid = dim3(blocks_of(pieces, 1 << log_tx), static_cast<unsigned>(down < 32768 ? down : 32768));
+    }
+};
+
 template <class WT, class ST, int GROUP>
 hipError_t quant_of(const QuantW4Job& j, hipStream_t stream) {
-    const int64_t groups = (j.k + GROUP - 1) / GROUP, per = 256 / (GROUP / 8);
+    const int64_t groups = (j.k + GROUP - 1) / GROUP;
+    const RowGrid g(j.n, groups * (GROUP / 8));
     const auto kernel = j.zero ? k_quant_w4<WT, ST, GROUP, true> : k_quant_w4<WT, ST, GROUP, false>;
-    hipLaunchKernelGGL(kernel, dim3(blocks_of(j.n * groups, per)), dim3(256), 0, stream, static_cast<const WT*>(j.w), j.n, j.k,
-                       groups, static_cast<uint32_t*>(j.q), static_cast<ST*>(j.scale), j.zero);
+    hipLaunchKernelGGL(kernel, g.grid, dim3(256), 0, stream, static_cast<const WT*>(j.w), j.n, j.k, groups, g.log_tx,
+                       static_cast<uint32_t*>(j.q), static_cast<ST*>(j.scale), j.zero);
     return hipGetLastError();
 }
 template <class WT, class ST>
@@ -114,12 +197,14 @@ hipError_t launch_quant_w4(const QuantW4Job& j, hipStream_t stream) {
 }
 
 hipError_t launch_dequant_w4(const WeightsW4& w, bool bf16, int64_t n, int64_t k, int group, void* out, hipStream_t stream) {
-    const int64_t pieces = n * (k / 8), groups = (k + group - 1) / group;
-    const dim3 grid(pieces > 65536 * 256 ? 65536u : blocks_of(pieces, 256));
+    const RowGrid g(n, k / 8);
+    const int log_group8 = group == 32 ? 2 : group == 64 ? 3 : 4;
+    const int64_t groups = (k + group - 1) / group;
     if (bf16)
-        hipLaunchKernelGGL(k_dequant_w4<true>, grid, dim3(256), 0, stream, w, k / 8, pieces, group / 8, groups, static_cast<__bf16*>(out));
+        hipLaunchKernelGGL(k_dequant_w4<true>, g.grid, dim3(256), 0, stream, w, n, k / 8, log_group8, groups, g.log_tx,
+                           static_cast<__bf16*>(out));
     else
-        hipLaunchKernelGGL(k_dequant_w4<false>, grid, dim3(256), 0, stream, w, k / 8, pieces, group / 8, groups,
+        hipLaunchKernelGGL(k_dequant_w4<false>, g.grid, dim3(256), 0, stream, w, n, k / 8, log_group8, groups, g.log_tx,
                            static_cast<_Float16*>(out));
     return hipGetLastError();
 }
