@@ -687,18 +687,18 @@ int swz_gated_w4(const void* d_x, int32_t x_type, int32_t act, const void* d_qg,
                  void* d_c, int64_t m, int64_t n, int64_t k, void* stream);
 
 /* Host only.  Bytes of workspace (8-byte aligned device memory) of the two
- * calls below for a list of tensors; it carries nothing from one call to the
- * next, and calls that may run at the same time need one each.
- *   d_t, numel, type : host arrays of `count` device addresses, sizes in
- *                      elements (0 allowed, then with any address) and types
- *                      (enum swz_x_type).  They are read during the call only.
- * Errors: as swz_grad_norm. */
-int swz_grad_norm_workspace(const void* const* d_t, const int64_t* numel, const int32_t* type, int32_t count,
-                            int64_t* bytes);
+ * calls below for `count` tensors: 16 KiB for each 64 of them.  It carries
+ * nothing from one call to the next, and calls that may run at the same time
+ * need one each.
+ * Errors: SWZ_EINVAL (count < 0, NULL), SWZ_EUNSUPPORTED (over 2^20 tensors). */
+int swz_grad_norm_workspace(int32_t count, int64_t* bytes);
 
 /* d_norm[0] = sqrt(sum over all tensors of the sum of their squares), squares
- * and sums in fp64; the same call gives the same bits.  Tensors aligned to
- * their element; 16-byte aligned ones are read in whole pieces.
+ * and sums in fp64; the same call gives the same bits.
+ *   d_t, numel, type : host arrays of `count` device addresses, sizes in
+ *                      elements (0 allowed, then with any address) and types
+ *                      (enum swz_x_type), read during the call only.
+ * Tensors aligned to their element.
  * Errors: SWZ_EINVAL (NULL, sizes, types, alignment, overlap of what is written
  * with anything, a workspace below swz_grad_norm_workspace), SWZ_EUNSUPPORTED
  * (over 2^20 tensors, or one of 2^38 elements and more). */

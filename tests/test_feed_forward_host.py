@@ -143,9 +143,9 @@ def arrays(at, numel, kind):
     return (ctypes.c_void_p * n)(*at), (ctypes.c_int64 * n)(*numel), (ctypes.c_int32 * n)(*kind), n
 
 
-def norm_workspace(*a):
+def norm_workspace(count):
     out = ctypes.c_int64(-1)
-    return lib.swz_grad_norm_workspace(*a, ctypes.byref(out)), out.value
+    return lib.swz_grad_norm_workspace(count, ctypes.byref(out)), out.value
 
 
 LIST = ([A, B, C], [100, 7, 5000], [T.X_BF16, T.X_F32, T.X_F16])
@@ -154,8 +154,7 @@ LIST = ([A, B, C], [100, 7, 5000], [T.X_BF16, T.X_F32, T.X_F16])
 def clip(at=LIST[0], numel=LIST[1], kind=LIST[2], out=None, norm=D, ws=WS, wsb=None, max_norm=1.0, which="clip"):
     a = arrays(at, numel, kind)
     if wsb is None:
-        st, wsb = norm_workspace(*a)
-        wsb = wsb if st == OK else 1 << 40
+        wsb = norm_workspace(len(at))[1]
     if which == "norm":
         return lib.swz_grad_norm(*a, norm, ws, wsb, None)
     return lib.swz_clip_grads(a[0], None if out is None else (ctypes.c_void_p * len(out))(*out), *a[1:], max_norm, norm, ws, wsb, None)
@@ -172,9 +171,7 @@ def test_norm_refusals(which):
     for i in range(3):
         b = list(a)
         b[i] = None
-        assert lib.swz_grad_norm_workspace(*b, ctypes.byref(ctypes.c_int64())) == EINVAL
         assert lib.swz_grad_norm(*b, D, WS, 1 << 30, None) == EINVAL
-    assert lib.swz_grad_norm_workspace(*a, None) == EINVAL
     for bad in (-1, (1 << 20) + 1):
         assert lib.swz_grad_norm(*a[:3], bad, D, WS, 1 << 30, None) == (EINVAL if bad < 0 else EUNSUP)
 
@@ -217,13 +214,10 @@ def test_accepted_calls():
 
 
 def test_norm_workspace():
-    assert norm_workspace(*arrays([], [], [])) == (OK, 0)
-    assert norm_workspace(*arrays([A], [0], [0])) == (OK, 0)
-    assert norm_workspace(*arrays([A], [16384], [T.X_BF16])) == (OK, 8)
-    assert norm_workspace(*arrays([A + 2], [16384], [T.X_BF16])) == (OK, 16)  # it begins in the middle of a piece
-    assert norm_workspace(*arrays([A], [8193], [T.X_F32])) == (OK, 16)
-    assert norm_workspace(*arrays([A] * 65, [1] * 65, [0] * 65)) == (OK, 8 * 65)
-    assert norm_workspace(*arrays([A] * 3, [1 << 30] * 3, [2] * 3)) == (OK, 8 * 2048)
+    for count, packs in ((0, 0), (1, 1), (64, 1), (65, 2), (1 << 20, 1 << 14)):
+        assert norm_workspace(count) == (OK, packs * 16384)
+    assert norm_workspace(-1)[0] == EINVAL and norm_workspace((1 << 20) + 1)[0] == EUNSUP
+    assert lib.swz_grad_norm_workspace(1, None) == EINVAL
 
 
 # ------------------------------------------------------------------ binding
@@ -329,7 +323,7 @@ def test_binding_checks_tensor_lists(monkeypatch):
     for bad, text in ((Typed(F64), "tensor 1 is not"), (Typed(I32), "tensor 1 is not"), (torch.zeros(3), "tensor 1 must be a CUDA"),
                       (Typed(BF, contiguous=False), "tensor 1 must be contiguous"), (Typed(BF, device="cuda:1"), "tensor 1 is on cuda:1"),
                       (A, "tensor 1 is not")):
-        for call in (lambda t: T.swz_grad_norm(t, norm, ws), lambda t: T.swz_clip_grads(t, 1.0, norm, ws), T.swz_grad_norm_workspace):
+        for call in (lambda t: T.swz_grad_norm(t, norm, ws), lambda t: T.swz_clip_grads(t, 1.0, norm, ws)):
             with pytest.raises(ValueError, match=text):
                 call([ok[0], bad])
     with pytest.raises(ValueError, match="current device"):

@@ -11,10 +11,13 @@ is given, and raise ``SwzError`` on a negative status.
 
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 from typing import Optional, Tuple
 
+_dtype = operator.attrgetter("dtype")
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libswz.so")
 
@@ -185,7 +188,7 @@ def _load() -> ctypes.CDLL:
         "swz_dequant_w4": [vp, vp, vp, i64, i64, i32, i32, vp, vp],
         "swz_gemm_w4": [vp, i32, vp, vp, vp, i32, vp, i64, i64, i64, vp],
         "swz_gated_w4": [vp, i32, i32, vp, vp, vp, vp, vp, vp, i32, vp, i64, i64, i64, vp],
-        "swz_grad_norm_workspace": [vp, vp, vp, i32, P(i64)],
+        "swz_grad_norm_workspace": [i32, P(i64)],
         "swz_grad_norm": [vp, vp, vp, i32, vp, vp, i64, vp],
         "swz_clip_grads": [vp, vp, vp, vp, i32, f32, vp, vp, i64, vp],
     }
@@ -224,9 +227,13 @@ def _buf(call: str, **bufs) -> None:
     type it reads (name=(tensor, bytes) or name=(tensor, bytes, type)).
     Raw integer addresses and None pass unchecked (the library checks what
     it can: NULL, alignment, overlap).  Raises ValueError."""
+    _bufs(call, [(name, *spec) if len(spec) == 3 else (name, *spec, None) for name, spec in bufs.items()])
+
+
+def _bufs(call: str, specs) -> None:
+    """_buf of (name, tensor, bytes, type or None)."""
     device, other = None, None
-    for name, spec in bufs.items():
-        t = spec[0]
+    for name, t, need, kind in specs:
         if t is None or isinstance(t, int):
             continue
         if not getattr(t, "is_cuda", False):
@@ -240,11 +247,11 @@ def _buf(call: str, **bufs) -> None:
         elif here != device:
             raise ValueError(f"{call}: {name} is on {here}, the other buffers on {device}")
         have = t.numel() * t.element_size()
-        if have < spec[1]:
-            raise ValueError(f"{call}: {name} holds {have} bytes, the call needs {int(spec[1])}")
-        if len(spec) == 3 and spec[2] is not None and getattr(t, "dtype", None) not in spec[2].seen:
+        if have < need:
+            raise ValueError(f"{call}: {name} holds {have} bytes, the call needs {int(need)}")
+        if kind is not None and getattr(t, "dtype", None) not in kind.seen:
             other = other or []
-            other.append((name, t, spec[2]))
+            other.append((name, t, kind))
     for name, t, kind in other or ():
         kind.check(call, name, t)
     if device is not None and device.index is not None:
@@ -257,14 +264,22 @@ def _buf(call: str, **bufs) -> None:
                              f"(call inside torch.cuda.device({device.index}))")
 
 
+_raw_stream = None  # torch's current stream of a device index as an address
+
+
 def _stream(stream, *tensors):
+    global _raw_stream
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     for t in tensors:
         if hasattr(t, "is_cuda") and t.is_cuda:
-            import torch
+            if _raw_stream is None:
+                import torch
 
-            return torch.cuda.current_stream(t.device).cuda_stream
+                # the address alone: a stream object costs as much as a launch
+                _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                    lambda index: torch.cuda.current_stream(index).cuda_stream)
+            return _raw_stream(t.device.index)
     return None
 
 
@@ -504,8 +519,8 @@ def swz_linear_distill_grad(h, w, index, teacher, lse, zt, upstream, dh, dw, n: 
 def swz_gated(x, wg, wu, y, n: int, f: int, k: int, x_type: int = X_BF16, act: int = ACT_SILU, pre=None, stream=None) -> None:
     """y [n][f] = act(x wg^T) * (x wu^T); pre (fp32 [2][n][f]), if given, keeps both products for the gradients."""
     xt = _X.get(x_type)
-    _buf("swz_gated", x=(x, 2 * n * k, xt), wg=(wg, 2 * f * k, xt), wu=(wu, 2 * f * k, xt), y=(y, 2 * n * f, xt),
-         pre=(pre, 8 * n * f, _FLOAT))
+    _bufs("swz_gated", (("x", x, 2 * n * k, xt), ("wg", wg, 2 * f * k, xt), ("wu", wu, 2 * f * k, xt), ("y", y, 2 * n * f, xt),
+                        ("pre", pre, 8 * n * f, _FLOAT)))
     _check(lib.swz_gated(_ptr(x), _ptr(wg), _ptr(wu), x_type, act, _ptr(y), _ptr(pre), n, f, k, _stream(stream, x, wg)),
            "swz_gated")
 
@@ -522,8 +537,9 @@ def swz_gated_grad(x, wg, wu, dy, dx, dwg, dwu, n: int, f: int, k: int, ws, x_ty
     """dx [n][k], dwg and dwu [f][k] of sum(dy * y); each may be None (not all).  Without pre the products are made again."""
     need = swz_gated_workspace(n, f, k)
     xt = _X.get(x_type)
-    _buf("swz_gated_grad", x=(x, 2 * n * k, xt), wg=(wg, 2 * f * k, xt), wu=(wu, 2 * f * k, xt), dy=(dy, 2 * n * f, xt),
-         pre=(pre, 8 * n * f, _FLOAT), dx=(dx, 2 * n * k, xt), dwg=(dwg, 2 * f * k, xt), dwu=(dwu, 2 * f * k, xt), ws=(ws, need))
+    _bufs("swz_gated_grad", (("x", x, 2 * n * k, xt), ("wg", wg, 2 * f * k, xt), ("wu", wu, 2 * f * k, xt), ("dy", dy, 2 * n * f, xt),
+                             ("pre", pre, 8 * n * f, _FLOAT), ("dx", dx, 2 * n * k, xt), ("dwg", dwg, 2 * f * k, xt),
+                             ("dwu", dwu, 2 * f * k, xt), ("ws", ws, need, None)))
     _check(lib.swz_gated_grad(_ptr(x), _ptr(wg), _ptr(wu), x_type, act, _ptr(dy), _ptr(pre), _ptr(dx), _ptr(dwg), _ptr(dwu), n,
                               f, k, _ptr(ws), _ws_bytes(ws, need), _stream(stream, x, wg)), "swz_gated_grad")
 
@@ -531,34 +547,34 @@ def swz_gated_grad(x, wg, wu, dy, dx, dwg, dwu, n: int, f: int, k: int, ws, x_ty
 _CODES = _Type(1, "uint8")
 
 
-def _w4(n: int, k: int, group: int, q, scale, zero, st, suffix: str = "") -> dict:
-    """The buffers of 4-bit weights for _buf."""
-    groups = n * -(-k // group) if group > 0 else 0
-    return {"q" + suffix: (q, n * (k // 2), _CODES), "scale" + suffix: (scale, 2 * groups, st),
-            "zero" + suffix: (zero, groups, _CODES)}
+def _w4_groups(n: int, k: int, group: int) -> int:
+    return n * -(-k // group) if group > 0 else 0
 
 
 def swz_quant_w4(w, q, scale, n: int, k: int, group: int = 128, w_type: int = X_BF16, x_type: int = X_BF16, zero=None,
                  stream=None) -> None:
     """w [n][k] to 4-bit codes q [n][k / 2] with scales of x_type per group (and zero points, uint8, if zero is given)."""
-    _buf("swz_quant_w4", w=(w, n * k * (4 if w_type == X_F32 else 2), _X.get(w_type)),
-         **_w4(n, k, group, q, scale, zero, _X.get(x_type)))
+    groups = _w4_groups(n, k, group)
+    _bufs("swz_quant_w4", (("w", w, n * k * (4 if w_type == X_F32 else 2), _X.get(w_type)), ("q", q, n * (k // 2), _CODES),
+                           ("scale", scale, 2 * groups, _X.get(x_type)), ("zero", zero, groups, _CODES)))
     _check(lib.swz_quant_w4(_ptr(w), w_type, n, k, group, x_type, _ptr(q), _ptr(scale), _ptr(zero), _stream(stream, w, q)),
            "swz_quant_w4")
 
 
 def swz_dequant_w4(q, scale, w, n: int, k: int, group: int = 128, x_type: int = X_BF16, zero=None, stream=None) -> None:
     """w [n][k] (x_type) = (code - zero) * scale."""
-    xt = _X.get(x_type)
-    _buf("swz_dequant_w4", w=(w, 2 * n * k, xt), **_w4(n, k, group, q, scale, zero, xt))
+    xt, groups = _X.get(x_type), _w4_groups(n, k, group)
+    _bufs("swz_dequant_w4", (("w", w, 2 * n * k, xt), ("q", q, n * (k // 2), _CODES), ("scale", scale, 2 * groups, xt),
+                             ("zero", zero, groups, _CODES)))
     _check(lib.swz_dequant_w4(_ptr(q), _ptr(scale), _ptr(zero), n, k, group, x_type, _ptr(w), _stream(stream, q, w)),
            "swz_dequant_w4")
 
 
 def swz_gemm_w4(x, q, scale, c, m: int, n: int, k: int, group: int = 128, x_type: int = X_BF16, zero=None, stream=None) -> None:
     """c [m][n] = x [m][k] W^T of 4-bit weights, for few rows of x."""
-    xt = _X.get(x_type)
-    _buf("swz_gemm_w4", x=(x, 2 * m * k, xt), c=(c, 2 * m * n, xt), **_w4(n, k, group, q, scale, zero, xt))
+    xt, groups = _X.get(x_type), _w4_groups(n, k, group)
+    _bufs("swz_gemm_w4", (("x", x, 2 * m * k, xt), ("c", c, 2 * m * n, xt), ("q", q, n * (k // 2), _CODES),
+                          ("scale", scale, 2 * groups, xt), ("zero", zero, groups, _CODES)))
     _check(lib.swz_gemm_w4(_ptr(x), x_type, _ptr(q), _ptr(scale), _ptr(zero), group, _ptr(c), m, n, k, _stream(stream, x, q)),
            "swz_gemm_w4")
 
@@ -566,9 +582,10 @@ def swz_gemm_w4(x, q, scale, c, m: int, n: int, k: int, group: int = 128, x_type
 def swz_gated_w4(x, qg, scale_g, qu, scale_u, c, m: int, n: int, k: int, group: int = 128, x_type: int = X_BF16,
                  act: int = ACT_SILU, zero_g=None, zero_u=None, stream=None) -> None:
     """c [m][n] = act(x Wg^T) * (x Wu^T) of 4-bit weights, for few rows of x."""
-    xt = _X.get(x_type)
-    _buf("swz_gated_w4", x=(x, 2 * m * k, xt), c=(c, 2 * m * n, xt), **_w4(n, k, group, qg, scale_g, zero_g, xt, "_g"),
-         **_w4(n, k, group, qu, scale_u, zero_u, xt, "_u"))
+    xt, groups, codes = _X.get(x_type), _w4_groups(n, k, group), n * (k // 2)
+    _bufs("swz_gated_w4", (("x", x, 2 * m * k, xt), ("c", c, 2 * m * n, xt), ("q_g", qg, codes, _CODES),
+                           ("scale_g", scale_g, 2 * groups, xt), ("zero_g", zero_g, groups, _CODES), ("q_u", qu, codes, _CODES),
+                           ("scale_u", scale_u, 2 * groups, xt), ("zero_u", zero_u, groups, _CODES)))
     _check(lib.swz_gated_w4(_ptr(x), x_type, act, _ptr(qg), _ptr(scale_g), _ptr(zero_g), _ptr(qu), _ptr(scale_u), _ptr(zero_u),
                             group, _ptr(c), m, n, k, _stream(stream, x, qg)), "swz_gated_w4")
 
@@ -576,81 +593,88 @@ def swz_gated_w4(x, qg, scale_g, qu, scale_u, c, m: int, n: int, k: int, group: 
 _X_OF = {}  # torch element types of the norm calls, filled by their first call
 
 
-def _tensors(call: str, tensors, like=None):
-    """A list of tensors as the host arrays that the norm calls read: (addresses, sizes, types, count).  like: the list
-    that these tensors have to match in size and type."""
+def _check_tensor(call: str, i: int, t, device) -> None:
+    """What is wrong with one of a norm call's tensors, if anything."""
+    if getattr(t, "dtype", None) not in _X_OF:
+        raise ValueError(f"{call}: tensor {i} is not a bfloat16, float16 or float32 tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{call}: tensor {i} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{call}: tensor {i} must be contiguous (a strided view is not its own bytes)")
+    if t.device.index != device:
+        raise ValueError(f"{call}: tensor {i} is on {t.device}, the current device is cuda:{device} "
+                         f"(call inside torch.cuda.device({t.device.index}))")
+
+
+def _tensors(call: str, tensors):
+    """A list of tensors as the norm calls read it: (addresses, sizes, types) as arrays of the host, their types and the
+    device.  Attributes are asked for list by list, which takes half as long as tensor by tensor."""
     import torch
 
     if not _X_OF:
         _X_OF.update({torch.bfloat16: X_BF16, torch.float16: X_F16, torch.float32: X_F32})
-    n = len(tensors)
-    if like is not None and n != len(like):
-        raise ValueError(f"{call}: {n} tensors to write, {len(like)} to read")
-    at, numel, kinds = [0] * n, [0] * n, [0] * n
-    device = None
-    for i, t in enumerate(tensors):
-        kind = _X_OF.get(getattr(t, "dtype", None))
-        if kind is None:
-            raise ValueError(f"{call}: tensor {i} is not a bfloat16, float16 or float32 tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{call}: tensor {i} must be a CUDA tensor")
-        if not t.is_contiguous():
-            raise ValueError(f"{call}: tensor {i} must be contiguous (a strided view is not its own bytes)")
-        here = t.device
-        if device is None:
-            device = here
-            if here.index != torch.cuda.current_device():
-                raise ValueError(f"{call}: tensor {i} is on {here}, the current device is cuda:{torch.cuda.current_device()} "
-                                 f"(call inside torch.cuda.device({here.index}))")
-        elif here != device:
-            raise ValueError(f"{call}: tensor {i} is on {here}, the other tensors on {device}")
-        at[i], numel[i], kinds[i] = t.data_ptr(), t.numel(), kind
-        if like is not None and (t.dtype != like[i].dtype or numel[i] != like[i].numel()):
-            raise ValueError(f"{call}: tensor {i} to write differs from the one to read in size or type")
-    return (ctypes.c_void_p * n)(*at), (ctypes.c_int64 * n)(*numel), (ctypes.c_int32 * n)(*kinds), n, device
+    tensors = list(tensors)
+    device = torch.cuda.current_device() if tensors else None
+    alike = {type(t) for t in tensors} <= {torch.Tensor, torch.nn.Parameter}
+    if not (alike and set(map(torch.Tensor.get_device, tensors)) <= {device} and all(map(torch.Tensor.is_contiguous, tensors))
+            and all(map(_X_OF.__contains__, map(_dtype, tensors)))):
+        for i, t in enumerate(tensors):
+            _check_tensor(call, i, t, device)
+    if alike:
+        at, numel = map(torch.Tensor.data_ptr, tensors), map(torch.Tensor.numel, tensors)
+    else:
+        at, numel = (t.data_ptr() for t in tensors), (t.numel() for t in tensors)
+    kinds = list(map(_dtype, tensors))
+    return array.array("Q", at), array.array("q", numel), array.array("i", map(_X_OF.__getitem__, kinds)), kinds, device
 
 
-def _norm_workspace(call: str, arrays) -> int:
-    out = ctypes.c_int64()
-    _check(lib.swz_grad_norm_workspace(*arrays[:4], ctypes.byref(out)), call)
-    return out.value
+def _at(a) -> int:
+    return a.buffer_info()[0]
 
 
 def swz_grad_norm_workspace(tensors) -> int:
     """Bytes of workspace for the norm of these tensors."""
-    return _norm_workspace("swz_grad_norm_workspace", _tensors("swz_grad_norm_workspace", tensors))
+    return _norm_workspace("swz_grad_norm_workspace", len(tensors))
+
+
+def _norm_workspace(call: str, count: int) -> int:
+    out = ctypes.c_int64()
+    _check(lib.swz_grad_norm_workspace(count, ctypes.byref(out)), call)
+    return out.value
+
+
+def _norm_buffers(call: str, device, norm, floats: int, ws, need: int) -> None:
+    here = getattr(norm, "device", None)
+    if device is not None and here is not None and here.index != device:
+        raise ValueError(f"{call}: norm is on {here}, the tensors on cuda:{device}")
+    _bufs(call, (("norm", norm, 4 * floats, _FLOAT), ("ws", ws, need, None)))
 
 
 def swz_grad_norm(tensors, norm, ws, stream=None) -> None:
     """norm[0] (fp32) = sqrt of the sum of all the tensors' squares."""
-    a = _tensors("swz_grad_norm", tensors)
-    need = _norm_workspace("swz_grad_norm", a)
-    _same_device("swz_grad_norm", a[4], norm)
-    _buf("swz_grad_norm", norm=(norm, 4, _FLOAT), ws=(ws, need))
-    _check(lib.swz_grad_norm(*a[:4], _ptr(norm), _ptr(ws), _ws_bytes(ws, need), _stream(stream, norm, ws)), "swz_grad_norm")
+    at, numel, types, _, device = _tensors("swz_grad_norm", tensors)
+    need = _norm_workspace("swz_grad_norm", len(at))
+    _norm_buffers("swz_grad_norm", device, norm, 1, ws, need)
+    _check(lib.swz_grad_norm(_at(at), _at(numel), _at(types), len(at), _ptr(norm), _ptr(ws), _ws_bytes(ws, need),
+                             _stream(stream, norm, ws)), "swz_grad_norm")
 
 
 def swz_clip_grads(tensors, max_norm: float, norm, ws, out=None, stream=None) -> None:
     """The tensors scaled so that their norm together is at most max_norm, in place or into the tensors of `out`;
     norm (fp32 [2]): the norm before, and the factor."""
-    a = _tensors("swz_clip_grads", tensors)
+    at, numel, types, kinds, device = _tensors("swz_clip_grads", tensors)
     to = None
     if out is not None:
-        b = _tensors("swz_clip_grads", out, tensors)
-        to = b[0]
-        if b[4] != a[4]:
-            raise ValueError(f"swz_clip_grads: the tensors to write are on {b[4]}, those to read on {a[4]}")
-    need = _norm_workspace("swz_clip_grads", a)
-    _same_device("swz_clip_grads", a[4], norm)
-    _buf("swz_clip_grads", norm=(norm, 8, _FLOAT), ws=(ws, need))
-    _check(lib.swz_clip_grads(a[0], to, *a[1:4], max_norm, _ptr(norm), _ptr(ws), _ws_bytes(ws, need), _stream(stream, norm, ws)),
-           "swz_clip_grads")
-
-
-def _same_device(call: str, device, t) -> None:
-    here = getattr(t, "device", None)
-    if device is not None and here is not None and here != device:
-        raise ValueError(f"{call}: norm is on {here}, the tensors on {device}")
+        to, to_numel, _, to_kinds, _ = _tensors("swz_clip_grads", out)
+        if len(to) != len(at):
+            raise ValueError(f"swz_clip_grads: {len(to)} tensors to write, {len(at)} to read")
+        if to_numel != numel or to_kinds != kinds:
+            i = next(i for i in range(len(at)) if to_numel[i] != numel[i] or to_kinds[i] != kinds[i])
+            raise ValueError(f"swz_clip_grads: tensor {i} to write differs from the one to read in size or type")
+    need = _norm_workspace("swz_clip_grads", len(at))
+    _norm_buffers("swz_clip_grads", device, norm, 2, ws, need)
+    _check(lib.swz_clip_grads(_at(at), None if to is None else _at(to), _at(numel), _at(types), len(at), max_norm, _ptr(norm),
+                              _ptr(ws), _ws_bytes(ws, need), _stream(stream, norm, ws)), "swz_clip_grads")
 
 
 def swz_fold(params, base: int, active: int):

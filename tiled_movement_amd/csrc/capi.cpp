@@ -212,24 +212,21 @@ int gemm_w4(const void* d_x, int32_t x_type, int32_t act, const swz::WeightsW4* 
     return hip_status(swz::launch_gemm_w4(j, static_cast<hipStream_t>(stream)));
 }
 
-// The list of a norm call: SWZ_OK and its partial sums' bytes, or why not.
-int check_norm_list(const void* const* d_t, const int64_t* numel, const int32_t* type, int32_t count, int64_t* ws_bytes) {
-    if (count < 0 || (count > 0 && (!d_t || !numel || !type))) return SWZ_EINVAL;
+int norm_workspace(int32_t count, int64_t* bytes) {
+    if (count < 0) return SWZ_EINVAL;
     if (count > 1 << 20) return SWZ_EUNSUPPORTED;
-    int64_t partials = 0, chunks = 0;
-    int here = 0;
+    *bytes = 8 * swz::kNormBlocks * ((count + swz::kNormTensors - 1) / swz::kNormTensors);
+    return SWZ_OK;
+}
+
+// The list of a norm call: SWZ_OK, or why not.
+int check_norm_list(const void* const* d_t, const int64_t* numel, const int32_t* type, int32_t count) {
+    if (count > 0 && (!d_t || !numel || !type)) return SWZ_EINVAL;
     for (int32_t i = 0; i < count; ++i) {
         if (numel[i] < 0 || (type[i] != SWZ_X_BF16 && type[i] != SWZ_X_F16 && type[i] != SWZ_X_F32)) return SWZ_EINVAL;
         if (numel[i] >= int64_t(1) << 38) return SWZ_EUNSUPPORTED;
-        if (numel[i] == 0) continue;
-        if (!d_t[i] || reinterpret_cast<uintptr_t>(d_t[i]) % (type[i] == SWZ_X_F32 ? 4 : 2)) return SWZ_EINVAL;
-        chunks += swz::norm_chunks(d_t[i], numel[i], type[i]);
-        if (++here == swz::kNormTensors) {
-            partials += std::min(chunks, swz::kNormBlocks);
-            chunks = here = 0;
-        }
+        if (numel[i] > 0 && (!d_t[i] || reinterpret_cast<uintptr_t>(d_t[i]) % (type[i] == SWZ_X_F32 ? 4 : 2))) return SWZ_EINVAL;
     }
-    *ws_bytes = 8 * (partials + std::min(chunks, swz::kNormBlocks));
     return SWZ_OK;
 }
 
@@ -251,9 +248,11 @@ bool apart(Span* s, int64_t count) {
 int norm_call(const void* const* d_t, void* const* d_out, const int64_t* numel, const int32_t* type, int32_t count, bool clip,
               float max_norm, float* d_norm, void* d_ws, int64_t ws_bytes, void* stream) {
     int64_t need;
-    const int st = check_norm_list(d_t, numel, type, count, &need);
+    int st = norm_workspace(count, &need);
+    if (st == SWZ_OK) st = check_norm_list(d_t, numel, type, count);
     if (st != SWZ_OK) return st;
     if (!d_norm || reinterpret_cast<uintptr_t>(d_norm) % 4) return SWZ_EINVAL;
+    if (std::all_of(numel, numel + count, [](int64_t n) { return n == 0; })) need = 0;  // nothing to sum
     if (need > 0 && (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 8 || ws_bytes < need)) return SWZ_EINVAL;
     const std::unique_ptr<Span[]> s(new (std::nothrow) Span[2 * static_cast<size_t>(count) + 2]);
     if (!s) return SWZ_EUNSUPPORTED;
@@ -1036,11 +1035,7 @@ SWZ_API int swz_gated_w4(const void* d_x, int32_t x_type, int32_t act, const voi
     return gemm_w4(d_x, x_type, act, w, 2, group, d_c, m, n, k, stream);
 }
 
-SWZ_API int swz_grad_norm_workspace(const void* const* d_t, const int64_t* numel, const int32_t* type, int32_t count,
-                                    int64_t* bytes) {
-    if (!bytes) return SWZ_EINVAL;
-    return check_norm_list(d_t, numel, type, count, bytes);
-}
+SWZ_API int swz_grad_norm_workspace(int32_t count, int64_t* bytes) { return bytes ? norm_workspace(count, bytes) : SWZ_EINVAL; }
 
 SWZ_API int swz_grad_norm(const void* const* d_t, const int64_t* numel, const int32_t* type, int32_t count, float* d_norm,
                           void* d_ws, int64_t ws_bytes, void* stream) {
