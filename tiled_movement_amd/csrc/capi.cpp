@@ -162,22 +162,42 @@ int check_gated_sizes(int64_t n, int64_t f, int64_t k) {
 bool half_type(int32_t x_type) { return x_type == SWZ_X_BF16 || x_type == SWZ_X_F16; }
 bool act_known(int32_t act) { return act == SWZ_ACT_SILU || act == SWZ_ACT_GELU || act == SWZ_ACT_GELU_TANH; }
 
-// Rows of a gradient product's tiles and the parts that its sum is split into:
-// where there are fewer tiles than the 256 compute units, parts of at least 8
-// stages with fp32 sums of their own.
-void plan_product(int64_t rows, int64_t cols, int64_t products, int64_t stages, int64_t* tile_rows, int64_t* parts) {
-    *tile_rows = rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
-    const int64_t tiles = (rows + *tile_rows - 1) / *tile_rows * ((cols + 255) / 256) * products;
-    *parts = tiles >= 256 || tiles == 0 ? 1 : 256 / tiles;
-    if (*parts > 32) *parts = 32;
-    if (*parts > stages / 8) *parts = stages / 8 ? stages / 8 : 1;
+// The tile of a gradient product and the parts that its sum over `stages` (of 64)
+// is split into, with fp32 sums of their own: the cheapest by what was measured,
+// in us: a workgroup's start and end, a stage, the parts' sums written and read at
+// 4.5 TB/s, and a launch.  A compute unit holds one workgroup, two of 64 x 64.
+// Gradients of 333 x 1000 to 2777 in 256 x 256 tiles alone 58 us, so 46; of 700 x 1024
+// to 4000 97 and 69; from 4096 x 4096 to 8192 on it comes out at 256 x 256.
+void plan_product(int64_t rows, int64_t cols, int64_t products, int64_t stages, swz::ProductTile* tile, int64_t* parts) {
+    static const struct {
+        swz::ProductTile tile;
+        int64_t rows, cols, at_once;
+        double fixed, stage;
+    } kinds[] = {{swz::ProductTile::k256x256, 256, 256, 256, 7.5, 1.5}, {swz::ProductTile::k128x256, 128, 256, 256, 5.3, 1.6},
+                 {swz::ProductTile::k64x256, 64, 256, 256, 3.7, 1.3},   {swz::ProductTile::k128x128, 128, 128, 256, 4.6, 1.1},
+                 {swz::ProductTile::k64x64, 64, 64, 512, 5.1, 0.7}};
+    static const int64_t tries[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32};
+    double best = -1;
+    for (const auto& k : kinds) {
+        const int64_t tiles = (rows + k.rows - 1) / k.rows * ((cols + k.cols - 1) / k.cols) * products;
+        for (const int64_t p : tries) {
+            if (p > 1 && p > stages / 4) break;
+            const double rounds = static_cast<double>((tiles * p + k.at_once - 1) / k.at_once);
+            double us = rounds * (k.fixed + k.stage * static_cast<double>((stages + p - 1) / p));
+            if (p > 1) us += 4 + static_cast<double>(p * rows) * static_cast<double>(cols * products) * 8 / 4.5e6;
+            if (best >= 0 && us >= best) continue;
+            best = us;
+            *tile = k.tile;
+            *parts = p;
+        }
+    }
 }
 
 swz::GatedPlan plan_gated(int64_t n, int64_t f, int64_t k) {
     swz::GatedPlan p{};
     p.ldz = up(f, 8);
-    plan_product(n, k, 1, 2 * ((f + 63) / 64), &p.dx_rows, &p.dx_parts);
-    plan_product(f, k, 2, (n + 63) / 64, &p.dw_rows, &p.dw_parts);
+    plan_product(n, k, 1, 2 * ((f + 63) / 64), &p.dx_tile, &p.dx_parts);
+    plan_product(f, k, 2, (n + 63) / 64, &p.dw_tile, &p.dw_parts);
     const int64_t dx = p.dx_parts > 1 ? 4 * p.dx_parts * n * k : 0, dw = p.dw_parts > 1 ? 8 * p.dw_parts * f * k : 0;
     p.dg = 0;
     p.du = up(2 * n * p.ldz, 256);

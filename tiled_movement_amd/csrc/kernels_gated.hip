@@ -80,64 +80,94 @@ __global__ __launch_bounds__(C::NT) void k_gated(Operand X, PairOperand W, int64
     store_tile<H>(part, slice, y, f, at.i0, at.f0, n, f, vec, at.lane, [](float v) { return v; });
 }
 
-// Up to 16 rows of x: the time is the weights' bytes.  A workgroup owns 16
-// features of both weights; its waves split k, wave w taking the blocks of 64
-// w, w + kFewWaves, ..., and the weights go from HBM straight into matrix
-// fragments; the waves' sums are joined through LDS in their order.
+template <bool DERIV>
+__device__ __forceinline__ float2 act_of(int act, float z) {
+    if (act == SWZ_ACT_GELU) return act::both<SWZ_ACT_GELU, DERIV>(z);
+    if (act == SWZ_ACT_GELU_TANH) return act::both<SWZ_ACT_GELU_TANH, DERIV>(z);
+    return act::both<SWZ_ACT_SILU, DERIV>(z);
+}
+
+// Up to 16 MB rows of x: the time is the weights' bytes.  A workgroup owns 16
+// features of both weights and all rows; its waves split k into runs of blocks of
+// 64, and operands go from memory straight into matrix fragments (a fragment is 16
+// rows of 64 bytes, and the weights are used once): no barrier and no LDS
+// between a load and its product, so that all loads of U blocks are in flight
+// together.  The waves' sums are joined through LDS in their order.
 constexpr int kFewWaves = 8;
-template <int ELEM, int ACT>
+template <int ELEM, int MB>
 __global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(const uint8_t* __restrict__ x, const uint8_t* __restrict__ wg,
-                                                              const uint8_t* __restrict__ wu, int64_t n, int64_t f, int64_t k,
+                                                              const uint8_t* __restrict__ wu, int64_t n, int64_t f, int64_t k, int act,
                                                               Value<ELEM>* __restrict__ y, float* __restrict__ pre) {
     __shared__ f32x4 red[2][kFewWaves][64];
     const int t = threadIdx.x, lane = t % 64, g = lane / 16, l16 = lane % 16;
     const int wave = __builtin_amdgcn_readfirstlane(t / 64);
     const int64_t f0 = static_cast<int64_t>(blockIdx.x) * 16;
     // this lane's rows; the last stands in for rows behind it, whose results are not stored
-    const int64_t rx = l16 < n ? l16 : n - 1, rw = f0 + l16 < f ? f0 + l16 : f - 1;
-    const uint8_t* row[3] = {x + 2 * rx * k, wg + 2 * rw * k, wu + 2 * rw * k};
-    const int64_t kbytes = 2 * k, full = kbytes / 128;
-    f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    // U blocks of this wave from b on, all loads before the products
+    const int64_t rw = f0 + l16 < f ? f0 + l16 : f - 1;
+    const uint8_t* row[2 + MB] = {wg + 2 * rw * k, wu + 2 * rw * k};
+#pragma unroll
+    for (int a = 0; a < MB; ++a) row[2 + a] = x + 2 * (16 * a + l16 < n ? 16 * a + l16 : n - 1) * k;
+    const int64_t kbytes = 2 * k, full = kbytes / 128, blocks = (kbytes + 127) / 128;
+    f32x4 acc[2][MB];
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int a = 0; a < MB; ++a) acc[o][a] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // UN blocks from b on, all loads before the products
     auto step = [&](int64_t b, auto un, bool lo_in, bool hi_in) {
-        constexpr int U = decltype(un)::value;
-        const i32x4 none = {0, 0, 0, 0};
-        i32x8 v[U][3];
+        constexpr int UN = decltype(un)::value;
+        i32x8 v[UN][2 + MB];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < UN; ++u)
 #pragma unroll
-            for (int o = 2; o >= 0; --o) {
-                const uint8_t* p = row[o] + (b + u * kFewWaves) * 128 + 16 * g;
-                const i32x4 lo = lo_in ? *reinterpret_cast<const i32x4*>(p) : none;
-                const i32x4 hi = hi_in ? *reinterpret_cast<const i32x4*>(p + 64) : none;
+            for (int o = 0; o < 2 + MB; ++o) {
+                const uint8_t* p = row[o] + (b + u) * 128;
+                i32x4 lo = *reinterpret_cast<const i32x4*>(p + (lo_in ? 16 * g : 0));
+                i32x4 hi = *reinterpret_cast<const i32x4*>(p + (hi_in ? 16 * g + 64 : 0));
                 v[u][o] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
             }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < UN; ++u) {
+            if (UN == 1 && !(lo_in && hi_in)) {  // behind k nothing counts
 #pragma unroll
-            for (int o = 0; o < 2; ++o) acc[o] = mfma_pair<ELEM>(v[u][o + 1], v[u][0], acc[o]);
+                for (int o = 0; o < 2 + MB; ++o)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (!lo_in) v[u][o][i] = 0;
+                        if (!hi_in) v[u][o][4 + i] = 0;
+                    }
+            }
+#pragma unroll
+            for (int a = 0; a < MB; ++a)
+#pragma unroll
+                for (int o = 0; o < 2; ++o) acc[o][a] = mfma_pair<ELEM>(v[u][o], v[u][2 + a], acc[o][a]);
+        }
     };
-    constexpr int U = 4;
-    int64_t b = wave;
-    for (; b + (U - 1) * kFewWaves < full; b += U * kFewWaves) step(b, std::integral_constant<int, U>{}, true, true);
-    for (; b < full; b += kFewWaves) step(b, std::integral_constant<int, 1>{}, true, true);
+    constexpr int U = 2;
+    const int64_t end = blocks * (wave + 1) / kFewWaves, whole = end < full ? end : full;
+    int64_t b = blocks * wave / kFewWaves;
+    for (; b + U <= whole; b += U) step(b, std::integral_constant<int, U>{}, true, true);
+    if constexpr (U > 1)
+        for (; b < whole; ++b) step(b, std::integral_constant<int, 1>{}, true, true);
     // k is a multiple of 8: 16-byte chunks are inside or outside as a whole
-    if (full * 128 < kbytes && full % kFewWaves == wave)
-        step(full, std::integral_constant<int, 1>{}, full * 128 + 16 * g < kbytes, full * 128 + 16 * g + 64 < kbytes);
+    if (b < end) step(b, std::integral_constant<int, 1>{}, b * 128 + 16 * g < kbytes, b * 128 + 16 * g + 64 < kbytes);
 
     // lane (g, l16): row l16 of x, features 4g .. 4g+3
 #pragma unroll
-    for (int o = 0; o < 2; ++o) red[o][wave][l16 * 4 + g] = acc[o];
-    __syncthreads();
-    if (t >= 256) return;
-    const float* rf = reinterpret_cast<const float*>(red);
-    float z[2] = {0.f, 0.f};
+    for (int a = 0; a < MB; ++a) {
+        if (a > 0) __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) z[0] += rf[w * 256 + t], z[1] += rf[(kFewWaves + w) * 256 + t];
-    const int64_t i = t / 16, j = f0 + t % 16;
-    if (i >= n || j >= f) return;
-    if (pre) pre[i * f + j] = z[0], pre[(n + i) * f + j] = z[1];
-    y[i * f + j] = static_cast<Value<ELEM>>(act::both<ACT, false>(z[0]).x * z[1]);
+        for (int o = 0; o < 2; ++o) red[o][wave][l16 * 4 + g] = acc[o][a];
+        __syncthreads();
+        const int64_t i = 16 * a + t / 16, j = f0 + t % 16;
+        if (t >= 256 || i >= n || j >= f) continue;
+        const float* rf = reinterpret_cast<const float*>(red);
+        float z[2] = {0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w) z[0] += rf[w * 256 + t], z[1] += rf[(kFewWaves + w) * 256 + t];
+        if (pre) pre[i * f + j] = z[0], pre[(n + i) * f + j] = z[1];
+        y[i * f + j] = static_cast<Value<ELEM>>(act_of<false>(act, z[0]).x * z[1]);
+    }
 }
 
 // dg and du ([n][ldz], x's type) from the kept g and u, eight places a thread;
@@ -298,16 +328,34 @@ __global__ __launch_bounds__(256) void k_zero(i32x4* __restrict__ p, int64_t pie
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; u < pieces; u += step) p[u] = i32x4{0, 0, 0, 0};
 }
 
-// Tiles of 256, 128 and 64 rows by 256.
-template <int ELEM> using Big = Config<ELEM, 0, 0, kNoScale, 4, 2, 4, 8>;
-template <int ELEM> using Mid = Config<ELEM, 0, 0, kNoScale, 2, 4, 4, 4>;
-template <int ELEM> using Low = Config<ELEM, 0, 0, kNoScale, 2, 4, 2, 4>;
+// Tiles of GatedTile and of ProductTile.
+template <int ELEM> using T256x256 = Config<ELEM, 0, 0, kNoScale, 4, 2, 4, 8>;
+template <int ELEM> using T128x256 = Config<ELEM, 0, 0, kNoScale, 2, 4, 4, 4>;
+template <int ELEM> using T64x256 = Config<ELEM, 0, 0, kNoScale, 2, 4, 2, 4>;
+template <int ELEM> using T128x128 = Config<ELEM, 0, 0, kNoScale, 2, 2, 4, 4>;
+template <int ELEM> using T64x64 = Config<ELEM, 0, 0, kNoScale, 2, 2, 2, 2>;
+template <int ELEM> using T128x64 = Config<ELEM, 0, 0, kNoScale, 4, 1, 2, 4>;
+template <int ELEM> using T64x64Slim = Config<ELEM, 0, 0, kNoScale, 4, 1, 1, 4>;  // a wave has both halves of its features
 
 template <int ELEM, class F>
-hipError_t by_rows_of(int64_t tile_rows, F f) {
-    if (tile_rows == 64) return f(Low<ELEM>{});
-    if (tile_rows == 128) return f(Mid<ELEM>{});
-    return f(Big<ELEM>{});
+hipError_t by_gated_tile(GatedTile tile, F f) {
+    switch (tile) {
+        case GatedTile::k64x32: return f(Gated<T64x64Slim<ELEM>>{});
+        case GatedTile::k128x32: return f(Gated<T128x64<ELEM>>{});
+        case GatedTile::k64x128: return f(Gated<T64x256<ELEM>>{});
+        case GatedTile::k128x128: return f(Gated<T128x256<ELEM>>{});
+        default: return f(Gated<T256x256<ELEM>>{});
+    }
+}
+template <int ELEM, bool L, bool R, class F>
+hipError_t by_product_tile(ProductTile tile, F f) {
+    switch (tile) {
+        case ProductTile::k64x64: return f(Across<T64x64<ELEM>, L, R>{});
+        case ProductTile::k64x256: return f(Across<T64x256<ELEM>, L, R>{});
+        case ProductTile::k128x128: return f(Across<T128x128<ELEM>, L, R>{});
+        case ProductTile::k128x256: return f(Across<T128x256<ELEM>, L, R>{});
+        default: return f(Across<T256x256<ELEM>, L, R>{});
+    }
 }
 template <class F>
 hipError_t by_act(int act, F f) {
@@ -331,16 +379,19 @@ PairOperand pair_operand(const GatedJob& j) {
 template <int ELEM>
 hipError_t forward(const GatedJob& j, hipStream_t stream) {
     using CT = Value<ELEM>;
+    if (gated_few(j.n, j.f, j.k)) {
+        const auto few = [&](auto mb) {
+            hipLaunchKernelGGL((k_gated_few<ELEM, decltype(mb)::value>), dim3(blocks_of(j.f, 16)), dim3(64 * kFewWaves), 0, stream,
+                               static_cast<const uint8_t*>(j.x), static_cast<const uint8_t*>(j.wg), static_cast<const uint8_t*>(j.wu),
+                               j.n, j.f, j.k, j.act, static_cast<CT*>(j.y), j.pre);
+            return hipGetLastError();
+        };
+        return j.n <= 16 ? few(std::integral_constant<int, 1>{}) : few(std::integral_constant<int, 2>{});
+    }
     return by_act(j.act, [&](auto a) {
         constexpr int ACT = decltype(a)::value;
-        if (j.n <= kGatedFewRows) {
-            hipLaunchKernelGGL((k_gated_few<ELEM, ACT>), dim3(blocks_of(j.f, 16)), dim3(64 * kFewWaves), 0, stream,
-                               static_cast<const uint8_t*>(j.x), static_cast<const uint8_t*>(j.wg),
-                               static_cast<const uint8_t*>(j.wu), j.n, j.f, j.k, static_cast<CT*>(j.y), j.pre);
-            return hipGetLastError();
-        }
-        return by_rows_of<ELEM>(loss_tile_rows(j.n, (j.f + 127) / 128), [&](auto cfg) {
-            using C = Gated<decltype(cfg)>;
+        return by_gated_tile<ELEM>(gated_tile(j.n, j.f), [&](auto cfg) {
+            using C = decltype(cfg);
             const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.f + C::TR / 2 - 1) / (C::TR / 2);
             const TileMap map = TileMap::make(tm, tn);
             const bool vec = j.f % 8 == 0 && reinterpret_cast<uintptr_t>(j.y) % 16 == 0 && reinterpret_cast<uintptr_t>(j.pre) % 16 == 0;
@@ -367,8 +418,8 @@ hipError_t backward(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
                                ldz, dg, du);
             return hipGetLastError();
         }
-        return by_rows_of<ELEM>(loss_tile_rows(j.n, (j.f + 127) / 128), [&](auto cfg) {
-            using C = Gated<decltype(cfg)>;
+        return by_gated_tile<ELEM>(gated_tile(j.n, j.f), [&](auto cfg) {
+            using C = decltype(cfg);
             const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.f + C::TR / 2 - 1) / (C::TR / 2);
             const TileMap map = TileMap::make(tm, tn);
             hipLaunchKernelGGL((k_gated_again_dz<C, ACT>), dim3(map.grid), dim3(C::NT), 0, stream, operand(j.x, j.k, j.n),
@@ -382,8 +433,8 @@ hipError_t backward(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
         return hipGetLastError();
     };
     if (e == hipSuccess && j.dx) {
-        e = by_rows_of<ELEM>(p.dx_rows, [&](auto cfg) {
-            using C = Across<decltype(cfg), false, true>;
+        e = by_product_tile<ELEM, false, true>(p.dx_tile, [&](auto cfg) {
+            using C = decltype(cfg);
             const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
             const TileMap map = TileMap::make(tm, tn);
             const int64_t part_bytes = ((2 * j.f + 127) / 128 + p.dx_parts - 1) / p.dx_parts * 128;
@@ -396,8 +447,8 @@ hipError_t backward(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
     }
     if (e == hipSuccess && (j.dwg || j.dwu)) {
         const unsigned both = j.dwg && j.dwu ? 2 : 1;
-        e = by_rows_of<ELEM>(p.dw_rows, [&](auto cfg) {
-            using C = Across<decltype(cfg), true, true>;
+        e = by_product_tile<ELEM, true, true>(p.dw_tile, [&](auto cfg) {
+            using C = decltype(cfg);
             const int64_t tm = (j.f + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
             const TileMap map = TileMap::make(tn, tm);
             const int64_t part_bytes = ((2 * j.n + 127) / 128 + p.dw_parts - 1) / p.dw_parts * 128;

@@ -24,14 +24,35 @@ struct GatedJob {
     void *dx, *dwg, *dwu;  // each may be nullptr
     void* ws;
 };
+// Whether a forward call goes to the kernel that streams the weights without LDS:
+// up to 16 rows, and up to 32 of small weights (20 x 520 to 600: 4.0 us, 6.5 in
+// tiles; but 24 x 4096 to 8192 37 and 32).
+inline bool gated_few(int64_t n, int64_t f, int64_t k) { return n <= 16 || (n <= 32 && f <= (int64_t(1) << 22) / k); }
+// Rows x features of a tile of the forward product: the smallest that covers the
+// rows, and up to 128 x 128 the smallest that leaves no more than 256
+// workgroups, one a compute unit.  us, tiles in the order below: 64 x 4096 to 8192
+// 32, 37, 53, 59, 91; 128 x 4096 to 8192 44, 39, 54, 62, 97; 77 x 2056 to 5000 29,
+// 24, 40, 47, 64; 256 x 4096 to 8192 80, 73, 53, 65, 103; 512 x 4096 to 8192 139,
+// 136, 96, 73, 103; 1000 x 4096 to 8192 256, 271, 183, 138, 114; 128 x 1024 to 1024
+// 8.7, 10.9, 12.5, 17, 25.
+enum class GatedTile { k64x32, k128x32, k64x128, k128x128, k256x128 };
+inline GatedTile gated_tile(int64_t n, int64_t f) {
+    auto fits = [&](int64_t rows, int64_t cols) { return ((n + rows - 1) / rows) * ((f + cols - 1) / cols) <= 256; };
+    if (n <= 64 || fits(64, 32)) return GatedTile::k64x32;
+    if (n <= 128 || fits(128, 32)) return GatedTile::k128x32;
+    if (fits(64, 128)) return GatedTile::k64x128;
+    if (fits(128, 128)) return GatedTile::k128x128;
+    return GatedTile::k256x128;
+}
+// Rows x columns of a tile of the gradients' products.
+enum class ProductTile { k64x64, k64x256, k128x128, k128x256, k256x256 };
 // Workspace of the gradient: byte offsets, the pitch of dg and du in elements,
-// and for the products the rows of their tiles and the parts that their sums are
-// split into.
+// and for the products their tiles and the parts that their sums are split into.
 struct GatedPlan {
     int64_t dg, du, sums, bytes;
-    int64_t ldz, dx_rows, dx_parts, dw_rows, dw_parts;
+    int64_t ldz, dx_parts, dw_parts;
+    ProductTile dx_tile, dw_tile;
 };
-constexpr int64_t kGatedFewRows = 16;
 SWZ_LAUNCHER launch_gated(const GatedJob& job, hipStream_t stream);
 SWZ_LAUNCHER launch_gated_grad(const GatedJob& job, const GatedPlan& plan, hipStream_t stream);
 
