@@ -168,7 +168,9 @@ bool act_known(int32_t act) { return act == SWZ_ACT_SILU || act == SWZ_ACT_GELU 
 // 4.5 TB/s, and a launch.  A compute unit holds one workgroup, two of 64 x 64.
 // Gradients of 333 x 1000 to 2777 in 256 x 256 tiles alone 58 us, so 46; of 700 x 1024
 // to 4000 97 and 69; from 4096 x 4096 to 8192 on it comes out at 256 x 256.
-void plan_product(int64_t rows, int64_t cols, int64_t products, int64_t stages, swz::ProductTile* tile, int64_t* parts) {
+// pairs: of operands whose sums follow one another, each with a start of its own.
+void plan_product(int64_t rows, int64_t cols, int64_t products, int64_t pairs, int64_t stages, swz::ProductTile* tile,
+                  int64_t* parts) {
     static const struct {
         swz::ProductTile tile;
         int64_t rows, cols, at_once;
@@ -183,7 +185,7 @@ void plan_product(int64_t rows, int64_t cols, int64_t products, int64_t stages, 
         for (const int64_t p : tries) {
             if (p > 1 && p > stages / 4) break;
             const double rounds = static_cast<double>((tiles * p + k.at_once - 1) / k.at_once);
-            double us = rounds * (k.fixed + k.stage * static_cast<double>((stages + p - 1) / p));
+            double us = rounds * (k.fixed + 5 * static_cast<double>(pairs - 1) + k.stage * static_cast<double>((stages + p - 1) / p));
             if (p > 1) us += 4 + static_cast<double>(p * rows) * static_cast<double>(cols * products) * 8 / 4.5e6;
             if (best >= 0 && us >= best) continue;
             best = us;
@@ -196,8 +198,8 @@ void plan_product(int64_t rows, int64_t cols, int64_t products, int64_t stages, 
 swz::GatedPlan plan_gated(int64_t n, int64_t f, int64_t k) {
     swz::GatedPlan p{};
     p.ldz = up(f, 8);
-    plan_product(n, k, 1, 2 * ((f + 63) / 64), &p.dx_tile, &p.dx_parts);
-    plan_product(f, k, 2, (n + 63) / 64, &p.dw_tile, &p.dw_parts);
+    plan_product(n, k, 1, 2, 2 * ((f + 63) / 64), &p.dx_tile, &p.dx_parts);
+    plan_product(f, k, 2, 1, (n + 63) / 64, &p.dw_tile, &p.dw_parts);
     const int64_t dx = p.dx_parts > 1 ? 4 * p.dx_parts * n * k : 0, dw = p.dw_parts > 1 ? 8 * p.dw_parts * f * k : 0;
     p.dg = 0;
     p.du = up(2 * n * p.ldz, 256);

@@ -250,10 +250,11 @@ struct AcrossFill {
     // Rows behind the last are read as the stage's first (masked when used).
     __device__ __forceinline__ void issue(int64_t stage, int64_t rem, lds_u8* dst, int wave) const {
         const uint8_t* b = base + stage * stage_bytes;
+        const uint32_t rows = rem < 128 ? static_cast<uint32_t>(rem) / 2 : 64u;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const uint32_t r = row_off + step_off * q;
-            __builtin_amdgcn_global_load_lds(b + ((2 * static_cast<int64_t>(row + kRowsOfStep * q) < rem ? r : 0u) + col_off),
+            __builtin_amdgcn_global_load_lds(b + ((row + kRowsOfStep * q < rows ? r : 0u) + col_off),
                                              dst + 16 * (64 * wave + NT * q), 16, 0, 0);
         }
     }
@@ -681,7 +682,10 @@ __device__ __forceinline__ void pingpong(f32x4 (&acc)[C::BL][C::BR], Stager<C>& 
         for (int x = 0; x < 2; ++x) l[h][x] = frag_l<C, false>(buf, lat, 2 * h + x, wl, g, 128);
     };
     // stage 0 has landed; stage 1 (or stage 0 again) goes to the other buffer
-    constexpr bool kSplit = C::ELEM == kF8;
+#ifndef KSP
+#define KSP 0
+#endif
+    constexpr bool kSplit = C::ELEM == kF8 || C::kPair || (C::kRAcross && !C::kLAcross) || KSP;
     if constexpr (!kSplit) st.issue_l(stages > 1 ? 1 : 0, lds + C::kBuf);
     st.issue_r(stages > 1 ? 1 : 0, lds + C::kBuf);
     read_r(lds, 0);
