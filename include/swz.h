@@ -600,8 +600,7 @@ enum swz_act { SWZ_ACT_SILU = 0, SWZ_ACT_GELU = 1, SWZ_ACT_GELU_TANH = 2 };
  *   g = x Wg^T,  u = x Wu^T,  y = act(g) u.
  *   d_x      : x_type (SWZ_X_BF16 or SWZ_X_F16) [n][k]; d_wg, d_wu : the same
  *              type [f][k]; k a multiple of 8, all 16-byte aligned.
- *   d_y      : x_type [n][f], aligned to its element (16-byte pieces where f is a
- *              multiple of 8 and d_y, d_pre are 16-byte aligned).
+ *   d_y      : x_type [n][f], aligned to its element.
  *   d_pre    : NULL, or float [2][n][f]: g, then u, for the gradient call.
  * g and u are exact products summed in fp32; y is rounded once.  Calls of up to
  * 16 rows go to a kernel that streams both weights once.  Nothing written may

@@ -166,8 +166,8 @@ bool act_known(int32_t act) { return act == SWZ_ACT_SILU || act == SWZ_ACT_GELU 
 // is split into, with fp32 sums of their own: the cheapest by what was measured,
 // in us: a workgroup's start and end, a stage, the parts' sums written and read at
 // 4.5 TB/s, and a launch.  A compute unit holds one workgroup, two of 64 x 64.
-// Gradients of 333 x 1000 to 2777 in 256 x 256 tiles alone 58 us, so 46; of 700 x 1024
-// to 4000 97 and 69; from 4096 x 4096 to 8192 on it comes out at 256 x 256.
+// Gradients of 333 x 1000 to 2777 in 256 x 256 tiles alone 55 us, so 45; of 700 x 1024
+// to 4000 102 and 68; from 4096 x 4096 to 8192 on it comes out at 256 x 256.
 // pairs: of operands whose sums follow one another, each with a start of its own.
 void plan_product(int64_t rows, int64_t cols, int64_t products, int64_t pairs, int64_t stages, swz::ProductTile* tile,
                   int64_t* parts) {

@@ -31,6 +31,26 @@ struct HalfR {
 template <int ELEM>
 using Value = std::conditional_t<ELEM == kBf16, __bf16, _Float16>;
 
+// The order of a grid's tiles, `times` times over (parts, products): TileMap's,
+// which keeps neighbours on one XCD, unless all workgroups could run at once and
+// it would give some XCD more than its 32 compute units (700 x 1024 from 4000, 24
+// tiles in 10 parts: on four of the eight XCDs, 70 us, 46 in plain order).
+struct Order {
+    TileMap map;
+    bool plain;
+    static Order make(int64_t f, int64_t s, int64_t times) {
+        const TileMap m = TileMap::make(f, s);
+        return Order{m, f * s * times <= 256 && static_cast<int64_t>(m.grid / 8) * times > 32};
+    }
+    unsigned grid() const { return plain ? map.f * map.s : map.grid; }
+    __device__ __forceinline__ bool at(uint32_t id, int64_t* fi, int64_t* si) const {
+        if (!plain) return map.at(id, fi, si);
+        *fi = id % map.f;
+        *si = id / map.f;
+        return true;
+    }
+};
+
 // What a workgroup of a tile kernel works on.
 template <class C>
 struct Place {
@@ -45,13 +65,53 @@ struct Place {
     }
 };
 
+// store_tile for rows of any length at any element: whole pieces as they lie
+// (stores of 16 bytes need no alignment here; those of 333 x 1000 to 2777 by
+// elements took 4 us more), a row's last one by elements.  Rows of whole aligned
+// pieces, and the 256 x 256 tiles, whose registers are full, go by store_tile.
+template <class H, class CT>
+__device__ __forceinline__ void store_rows(const f32x4 (&acc)[H::BL][H::BR], lds_f32* slice, CT* __restrict__ c, int64_t i0,
+                                           int64_t j0, int64_t rows, int64_t cols, int lane) {
+    constexpr int W = 16 * H::BR, P = H::kPitch, V = 16 / sizeof(CT), PER = W / V;
+    typedef CT ctv __attribute__((ext_vector_type(V), aligned(sizeof(CT))));
+    static_assert(16 * PER % 64 == 0, "whole pieces per wave");
+    const int g = lane / 16, l16 = lane % 16;
+#pragma unroll
+    for (int x = 0; x < H::BL; ++x) {
+#pragma unroll
+        for (int y = 0; y < H::BR; ++y) *reinterpret_cast<lds_f32x4*>(slice + l16 * P + 16 * y + 4 * g) = acc[x][y];
+        const int64_t ib = i0 + 16 * x;
+        if (ib >= rows) continue;
+#pragma unroll
+        for (int q = 0; q < 16 * PER / 64; ++q) {
+            const int u = 64 * q + lane, r = u / PER, cc = V * (u % PER);
+            ctv o;
+#pragma unroll
+            for (int h = 0; h < V / 4; ++h) {
+                const f32x4 v = *reinterpret_cast<const lds_f32x4*>(slice + r * P + cc + 4 * h);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[4 * h + i] = static_cast<CT>(v[i]);
+            }
+            if (ib + r >= rows) continue;
+            CT* to = c + (ib + r) * cols + j0 + cc;
+            if (j0 + cc + V <= cols) {
+                __builtin_nontemporal_store(o, reinterpret_cast<ctv*>(to));
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (j0 + cc + i < cols) to[i] = o[i];
+            }
+        }
+    }
+}
+
 template <class C, int ACT>
 __global__ __launch_bounds__(C::NT) void k_gated(Operand X, PairOperand W, int64_t kbytes, Value<C::ELEM>* __restrict__ y,
-                                                 float* __restrict__ pre, int vec, TileMap map) {
+                                                 float* __restrict__ pre, int vec, Order order) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
     int64_t tm, tn;
-    if (!map.at(blockIdx.x, &tm, &tn)) return;
+    if (!order.at(blockIdx.x, &tm, &tn)) return;
     f32x4 acc[C::BL][C::BR];
     tile_product<C>(acc, X, W, tm * C::TL, tn * (C::TR / 2), kbytes, lds);
     const Place<C> at(tm, tn);
@@ -59,6 +119,12 @@ __global__ __launch_bounds__(C::NT) void k_gated(Operand X, PairOperand W, int64
     lds_f32* slice = (lds_f32*)(lds + at.wave * C::kSlice);
     const int64_t n = X.rows, f = W.rows;
     f32x4 part[H::BL][H::BR];
+    auto store = [&](auto* to) {
+        if (C::kSlots || vec)
+            store_tile<H>(part, slice, to, f, at.i0, at.f0, n, f, vec, at.lane, [](float v) { return v; });
+        else
+            store_rows<H>(part, slice, to, at.i0, at.f0, n, f, at.lane);
+    };
     if (pre) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -66,7 +132,7 @@ __global__ __launch_bounds__(C::NT) void k_gated(Operand X, PairOperand W, int64
             for (int x = 0; x < H::BL; ++x)
 #pragma unroll
                 for (int b = 0; b < H::BR; ++b) part[x][b] = acc[x][p * H::BR + b];
-            store_tile<H>(part, slice, pre + p * n * f, f, at.i0, at.f0, n, f, vec, at.lane, [](float v) { return v; });
+            store(pre + p * n * f);
         }
     }
 #pragma unroll
@@ -77,7 +143,7 @@ __global__ __launch_bounds__(C::NT) void k_gated(Operand X, PairOperand W, int64
 #pragma unroll
             for (int i = 0; i < 4; ++i) part[x][b][i] = act::both<ACT, false>(acc[x][b][i]).x * acc[x][H::BR + b][i];
         }
-    store_tile<H>(part, slice, y, f, at.i0, at.f0, n, f, vec, at.lane, [](float v) { return v; });
+    store(y);
 }
 
 template <bool DERIV>
@@ -214,11 +280,11 @@ template <class C, int ACT>
 __global__ __launch_bounds__(C::NT) void k_gated_again_dz(Operand X, PairOperand W, int64_t kbytes,
                                                           const Value<C::ELEM>* __restrict__ dy, int64_t ldz,
                                                           Value<C::ELEM>* __restrict__ dg, Value<C::ELEM>* __restrict__ du,
-                                                          TileMap map) {
+                                                          Order order) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
     int64_t tm, tn;
-    if (!map.at(blockIdx.x, &tm, &tn)) return;
+    if (!order.at(blockIdx.x, &tm, &tn)) return;
     f32x4 acc[C::BL][C::BR];
     tile_product<C>(acc, X, W, tm * C::TL, tn * (C::TR / 2), kbytes, lds);
     const Place<C> at(tm, tn);
@@ -276,11 +342,11 @@ __device__ __forceinline__ int64_t part_of(int64_t kbytes, int64_t part_bytes, i
 template <class C>
 __global__ __launch_bounds__(C::NT) void k_gated_dx(Operand Zg, Operand Zu, Operand Wg, Operand Wu, int64_t kbytes,
                                                     int64_t part_bytes, Value<C::ELEM>* __restrict__ dx, float* __restrict__ sums,
-                                                    TileMap map) {
+                                                    Order order) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
     int64_t tm, tn, k0;
-    if (!map.at(blockIdx.x, &tm, &tn)) return;
+    if (!order.at(blockIdx.x, &tm, &tn)) return;
     const int64_t kb = part_of(kbytes, part_bytes, blockIdx.y, &k0);
     Zg.data += k0, Zu.data += k0, Wg.data += k0 / 2 * Wg.ld, Wu.data += k0 / 2 * Wu.ld;
     f32x4 acc[C::BL][C::BR];
@@ -294,11 +360,11 @@ __global__ __launch_bounds__(C::NT) void k_gated_dx(Operand Zg, Operand Zu, Oper
 template <class C>
 __global__ __launch_bounds__(C::NT) void k_gated_dw(Operand Zg, Operand Zu, Operand X, int64_t kbytes, int64_t part_bytes,
                                                     Value<C::ELEM>* __restrict__ dwg, Value<C::ELEM>* __restrict__ dwu,
-                                                    float* __restrict__ sums, TileMap map) {
+                                                    float* __restrict__ sums, Order order) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
     int64_t tm, tn, k0;
-    if (!map.at(blockIdx.x, &tn, &tm)) return;
+    if (!order.at(blockIdx.x, &tn, &tm)) return;
     const int64_t kb = part_of(kbytes, part_bytes, blockIdx.y, &k0);
     const bool up = blockIdx.z != 0 || !dwg;
     Operand Z = up ? Zu : Zg;
@@ -393,10 +459,10 @@ hipError_t forward(const GatedJob& j, hipStream_t stream) {
         return by_gated_tile<ELEM>(gated_tile(j.n, j.f), [&](auto cfg) {
             using C = decltype(cfg);
             const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.f + C::TR / 2 - 1) / (C::TR / 2);
-            const TileMap map = TileMap::make(tm, tn);
-            const bool vec = j.f % 8 == 0 && reinterpret_cast<uintptr_t>(j.y) % 16 == 0 && reinterpret_cast<uintptr_t>(j.pre) % 16 == 0;
-            hipLaunchKernelGGL((k_gated<C, ACT>), dim3(map.grid), dim3(C::NT), 0, stream, operand(j.x, j.k, j.n), pair_operand(j),
-                               2 * j.k, static_cast<CT*>(j.y), j.pre, vec, map);
+            const Order order = Order::make(tm, tn, 1);
+            const bool vec = j.f % 8 == 0 && (reinterpret_cast<uintptr_t>(j.y) | reinterpret_cast<uintptr_t>(j.pre)) % 16 == 0;
+            hipLaunchKernelGGL((k_gated<C, ACT>), dim3(order.grid()), dim3(C::NT), 0, stream, operand(j.x, j.k, j.n), pair_operand(j),
+                               2 * j.k, static_cast<CT*>(j.y), j.pre, vec, order);
             return hipGetLastError();
         });
     });
@@ -421,9 +487,9 @@ hipError_t backward(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
         return by_gated_tile<ELEM>(gated_tile(j.n, j.f), [&](auto cfg) {
             using C = decltype(cfg);
             const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.f + C::TR / 2 - 1) / (C::TR / 2);
-            const TileMap map = TileMap::make(tm, tn);
-            hipLaunchKernelGGL((k_gated_again_dz<C, ACT>), dim3(map.grid), dim3(C::NT), 0, stream, operand(j.x, j.k, j.n),
-                               pair_operand(j), 2 * j.k, static_cast<const CT*>(j.dy), ldz, dg, du, map);
+            const Order order = Order::make(tm, tn, 1);
+            hipLaunchKernelGGL((k_gated_again_dz<C, ACT>), dim3(order.grid()), dim3(C::NT), 0, stream, operand(j.x, j.k, j.n),
+                               pair_operand(j), 2 * j.k, static_cast<const CT*>(j.dy), ldz, dg, du, order);
             return hipGetLastError();
         });
     });
@@ -436,11 +502,11 @@ hipError_t backward(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
         e = by_product_tile<ELEM, false, true>(p.dx_tile, [&](auto cfg) {
             using C = decltype(cfg);
             const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
-            const TileMap map = TileMap::make(tm, tn);
+            const Order order = Order::make(tm, tn, p.dx_parts);
             const int64_t part_bytes = ((2 * j.f + 127) / 128 + p.dx_parts - 1) / p.dx_parts * 128;
-            hipLaunchKernelGGL(k_gated_dx<C>, dim3(map.grid, static_cast<unsigned>(p.dx_parts)), dim3(C::NT), 0, stream,
+            hipLaunchKernelGGL(k_gated_dx<C>, dim3(order.grid(), static_cast<unsigned>(p.dx_parts)), dim3(C::NT), 0, stream,
                                operand(dg, ldz, j.n), operand(du, ldz, j.n), operand(j.wg, j.k, j.k), operand(j.wu, j.k, j.k),
-                               2 * j.f, part_bytes, static_cast<CT*>(j.dx), p.dx_parts > 1 ? sums : nullptr, map);
+                               2 * j.f, part_bytes, static_cast<CT*>(j.dx), p.dx_parts > 1 ? sums : nullptr, order);
             return hipGetLastError();
         });
         if (e == hipSuccess && p.dx_parts > 1) e = join(sums, p.dx_parts, j.n * j.k, j.dx);
@@ -450,11 +516,11 @@ hipError_t backward(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
         e = by_product_tile<ELEM, true, true>(p.dw_tile, [&](auto cfg) {
             using C = decltype(cfg);
             const int64_t tm = (j.f + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
-            const TileMap map = TileMap::make(tn, tm);
+            const Order order = Order::make(tn, tm, p.dw_parts * both);
             const int64_t part_bytes = ((2 * j.n + 127) / 128 + p.dw_parts - 1) / p.dw_parts * 128;
-            hipLaunchKernelGGL(k_gated_dw<C>, dim3(map.grid, static_cast<unsigned>(p.dw_parts), both), dim3(C::NT), 0, stream,
+            hipLaunchKernelGGL(k_gated_dw<C>, dim3(order.grid(), static_cast<unsigned>(p.dw_parts), both), dim3(C::NT), 0, stream,
                                operand(dg, ldz, j.f), operand(du, ldz, j.f), operand(j.x, j.k, j.k), 2 * j.n, part_bytes,
-                               static_cast<CT*>(j.dwg), static_cast<CT*>(j.dwu), p.dw_parts > 1 ? sums : nullptr, map);
+                               static_cast<CT*>(j.dwg), static_cast<CT*>(j.dwu), p.dw_parts > 1 ? sums : nullptr, order);
             return hipGetLastError();
         });
         if (p.dw_parts > 1) {

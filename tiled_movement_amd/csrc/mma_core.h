@@ -682,10 +682,7 @@ __device__ __forceinline__ void pingpong(f32x4 (&acc)[C::BL][C::BR], Stager<C>& 
         for (int x = 0; x < 2; ++x) l[h][x] = frag_l<C, false>(buf, lat, 2 * h + x, wl, g, 128);
     };
     // stage 0 has landed; stage 1 (or stage 0 again) goes to the other buffer
-#ifndef KSP
-#define KSP 0
-#endif
-    constexpr bool kSplit = C::ELEM == kF8 || C::kPair || (C::kRAcross && !C::kLAcross) || KSP;
+    constexpr bool kSplit = C::ELEM == kF8 || C::kPair || (C::kRAcross && !C::kLAcross);
     if constexpr (!kSplit) st.issue_l(stages > 1 ? 1 : 0, lds + C::kBuf);
     st.issue_r(stages > 1 ? 1 : 0, lds + C::kBuf);
     read_r(lds, 0);
