@@ -669,10 +669,12 @@ int swz_dequant_w4(const void* d_q, const void* d_scale, const uint8_t* d_zero, 
  *   to its element; d_x and d_q 16-byte aligned.
  * Products are exact in fp32 (x times 16 + code) and summed in fp32, a group's
  * sum less (16 + zero) times the group's sum of x, and that times its scale in
- * fp32; the result is rounded once.  |x| has to stay below the type's largest
- * value over 2^9 k; a row of X that holds an infinity or NaN comes out NaN.
- * Meant for up to some 64 rows: 16 rows of X read the weights once.  m = 0 does
- * nothing; any n.
+ * fp32; the result is rounded once.  A group's sum of |x| (32 + zero) has to stay
+ * within fp32 (any fp16 x does); a row of X that holds an infinity or NaN comes
+ * out NaN, and the other rows as they would without it.
+ * Meant for few rows: up to 64 read the weights once, and for hundreds
+ * swz_dequant_w4 with a product of that is the faster one.  m = 0 does nothing;
+ * any n.
  * Errors: SWZ_EINVAL (sizes, alignment, NULL, overlap, enum values, group),
  * SWZ_EUNSUPPORTED (m or k of 2^22 and more, n of 2^26 and more, n k of 2^34
  * and more). */
