@@ -81,8 +81,9 @@ def test_gated_workspace():
         for f in (1, 127, 4096, 50001):
             for k in (8, 1000, 4096):
                 st, b = workspace(n, f, k)
-                # dg and du, and at most 32 parts of 256 tiles' sums
-                assert st == OK and 4 * n * f <= b <= 4 * n * (f + 8) + 4 * 32 * 256 * 256 * 256 + 4096
+                # dg and du, twice of each for small products, and at most 32 parts of 256 tiles' sums
+                terms = 2 if n * f * k <= 1 << 23 else 1
+                assert st == OK and 4 * terms * n * f <= b <= 4 * terms * n * (f + 8) + 4 * 32 * 256 * 256 * 256 + 4096
     assert T.swz_gated_workspace(4096, 8192, 4096) == workspace(4096, 8192, 4096)[1]
 
 

@@ -18,9 +18,9 @@ PROGRAM = f"""
 int main(int argc, char** argv) {{
     const int64_t n = atoll(argv[1]), k = atoll(argv[2]), f = atoll(argv[3]);
     const swz::GatedPlan p = plan_gated(n, f, k);
-    printf("%d %d %d %lld %d %lld\\n", swz::gated_few(n, f, k) ? 1 : 0, static_cast<int>(swz::gated_tile(n, f)),
+    printf("%d %d %d %lld %d %lld %d\\n", swz::gated_few(n, f, k) ? 1 : 0, static_cast<int>(swz::gated_tile(n, f)),
            static_cast<int>(p.dx_tile), static_cast<long long>(p.dx_parts), static_cast<int>(p.dw_tile),
-           static_cast<long long>(p.dw_parts));
+           static_cast<long long>(p.dw_parts), p.rest != 0);
 }}
 """
 
@@ -36,8 +36,8 @@ def rules(tmp_path_factory):
 
     def run(shape):
         out = subprocess.run([str(d / "rules"), *map(str, shape)], capture_output=True, text=True, check=True).stdout
-        few, gated, dx, dxp, dw, dwp = (int(x) for x in out.split())
-        return "few" if few else GATED[gated], (TILES[dx], dxp > 1), (TILES[dw], dwp > 1)
+        few, gated, dx, dxp, dw, dwp, two = (int(x) for x in out.split())
+        return "few" if few else GATED[gated], (TILES[dx], dxp > 1, two == 1), (TILES[dw], dwp > 1, two == 1)
 
     return run
 
@@ -59,4 +59,12 @@ def test_dw_shapes_take_their_tiles(rules, kind):
 
 def test_cases_reach_every_tile():
     assert set(FORWARD) == {"few", *GATED}
-    assert set(DX) == set(DW) == {(t, split) for t in TILES for split in (False, True)}
+    tiles = {(t, split, False) for t in TILES for split in (False, True)}
+    assert set(DX) == set(DW) == tiles | {("k64x64", False, True), ("k64x64", True, True), ("k128x256", False, True)}
+
+
+def test_small_products_take_two_terms(rules):
+    for n, k, f in ((1, 8, 1), (1, 8, 1 << 20), (256, 256, 128), (255, 8, 4112)):
+        assert rules((n, k, f))[1][2] and rules((n, k, f))[2][2]
+    for n, k, f in ((256, 256, 129), (1 << 20, 16, 1), (1, 1032, 8192)):
+        assert not rules((n, k, f))[1][2] and not rules((n, k, f))[2][2]

@@ -79,7 +79,9 @@ class Case:
         dx, dwg, dwu, dg, du = F.gated_grad(x, wg, wu, self.act, dy)
         edg = np.abs(dy) * (np.abs(da) * eu + (np.abs(u) + eu) * eda) + 4 * U * np.abs(dg)
         edu = np.abs(dy) * ea + 4 * U * np.abs(du)
-        edg, edu = (e + step * (np.abs(v) + e) + tiny for e, v in ((edg, dg), (edu, du)))
+        # dg and du are rounded once, or held as two terms: what the first leaves, at most a half step, is rounded again
+        held = step * step if self.n * self.f * self.k <= 1 << 23 else step
+        edg, edu = (e + held * (np.abs(v) + e) + tiny for e, v in ((edg, dg), (edu, du)))
         sums = lambda e, v, r, terms: e @ r + (terms + 40) * U * ((np.abs(v) + e) @ r)  # noqa: E731
         bound = {"dx": sums(edg, dg, np.abs(wg), 2 * self.f) + sums(edu, du, np.abs(wu), 2 * self.f),
                  "dwg": sums(edg.T, dg.T, np.abs(x), self.n), "dwu": sums(edu.T, du.T, np.abs(x), self.n)}

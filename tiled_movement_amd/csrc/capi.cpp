@@ -168,8 +168,10 @@ bool act_known(int32_t act) { return act == SWZ_ACT_SILU || act == SWZ_ACT_GELU 
 // 4.5 TB/s, and a launch.  A compute unit holds one workgroup, two of 64 x 64.
 // Gradients of 333 x 1000 to 2777 in 256 x 256 tiles alone 55 us, so 45; of 700 x 1024
 // to 4000 102 and 68; from 4096 x 4096 to 8192 on it comes out at 256 x 256.
-// pairs: of operands whose sums follow one another, each with a start of its own.
-void plan_product(int64_t rows, int64_t cols, int64_t products, int64_t pairs, int64_t stages, swz::ProductTile* tile,
+// pairs: of operands whose sums follow one another, each with a start of its own;
+// two: over two terms, twice the pairs and stages, in 64 x 64 and 128 x 256 tiles
+// only (dW of 8192 x 1024 from one row in 64 x 64 36 us, 18 so).
+void plan_product(int64_t rows, int64_t cols, int64_t products, int64_t pairs, int64_t stages, bool two, swz::ProductTile* tile,
                   int64_t* parts) {
     static const struct {
         swz::ProductTile tile;
@@ -180,7 +182,9 @@ void plan_product(int64_t rows, int64_t cols, int64_t products, int64_t pairs, i
                  {swz::ProductTile::k64x64, 64, 64, 512, 5.1, 0.7}};
     static const int64_t tries[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32};
     double best = -1;
+    if (two) pairs *= 2, stages *= 2;
     for (const auto& k : kinds) {
+        if (two && k.tile != swz::ProductTile::k64x64 && k.tile != swz::ProductTile::k128x256) continue;
         const int64_t tiles = (rows + k.rows - 1) / k.rows * ((cols + k.cols - 1) / k.cols) * products;
         for (const int64_t p : tries) {
             if (p > 1 && p > stages / 4) break;
@@ -198,12 +202,14 @@ void plan_product(int64_t rows, int64_t cols, int64_t products, int64_t pairs, i
 swz::GatedPlan plan_gated(int64_t n, int64_t f, int64_t k) {
     swz::GatedPlan p{};
     p.ldz = up(f, 8);
-    plan_product(n, k, 1, 2, 2 * ((f + 63) / 64), &p.dx_tile, &p.dx_parts);
-    plan_product(f, k, 2, 1, (n + 63) / 64, &p.dw_tile, &p.dw_parts);
+    const bool two = swz::gated_two_terms(n, f, k);
+    plan_product(n, k, 1, 2, 2 * ((f + 63) / 64), two, &p.dx_tile, &p.dx_parts);
+    plan_product(f, k, 2, 1, (n + 63) / 64, two, &p.dw_tile, &p.dw_parts);
     const int64_t dx = p.dx_parts > 1 ? 4 * p.dx_parts * n * k : 0, dw = p.dw_parts > 1 ? 8 * p.dw_parts * f * k : 0;
     p.dg = 0;
     p.du = up(2 * n * p.ldz, 256);
-    p.sums = 2 * p.du;
+    p.rest = two ? 2 * p.du : 0;
+    p.sums = 2 * p.du + p.rest;
     p.bytes = p.sums + up(dx > dw ? dx : dw, 256);
     return p;
 }

@@ -8,7 +8,8 @@
 // rounding.  On request g and u are kept in fp32 for the backward pass (8 bytes a
 // place against 4 k operations to make them again).
 //
-// Backward: dg and du are made once, in x's type, by elements from the kept g
+// Backward: dg and du are made once, in x's type (as two terms for small
+// products: gated_two_terms()), by elements from the kept g
 // and u or by the forward products over again.  The products that follow sum over
 // f (dx) and over the rows of x (dW), where the weights, dg, du and x
 // lie across the sum; they are read as they lie, by transposing reads out of
@@ -236,13 +237,20 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(const uint8_t* __r
     }
 }
 
+// What is left of v when it is rounded to CT; nothing where that has no end.
+template <class CT>
+__device__ __forceinline__ float rest_of(float v) {
+    const float r = static_cast<float>(static_cast<CT>(v));
+    return __builtin_isfinite(r) ? v - r : 0.f;
+}
+
 // dg and du ([n][ldz], x's type) from the kept g and u, eight places a thread;
 // rows by blockIdx.y.  Bound by the bytes.  Rows of an f that is no multiple of 8
 // begin at any element: their pieces are loaded as they lie, and the last one by
 // elements.
 template <class CT, int ACT>
 __global__ __launch_bounds__(256) void k_gated_dz(const float* __restrict__ pre, const CT* __restrict__ dy, int64_t n, int64_t f,
-                                                  int64_t ldz, CT* __restrict__ dg, CT* __restrict__ du) {
+                                                  int64_t ldz, CT* __restrict__ dg, CT* __restrict__ du, int64_t rest) {
     typedef float f32x8 __attribute__((ext_vector_type(8), aligned(4)));
     typedef CT ct8 __attribute__((ext_vector_type(8)));
     typedef CT ct8_any __attribute__((ext_vector_type(8), aligned(2)));
@@ -261,17 +269,21 @@ __global__ __launch_bounds__(256) void k_gated_dz(const float* __restrict__ pre,
             for (int e = 0; e < 8; ++e)
                 if (e < here) g[e] = pre[i * f + j + e], u[e] = pre[(n + i) * f + j + e], d[e] = dy[i * f + j + e];
         }
-        ct8 zg, zu;
+        ct8 zg, zu, rg, ru;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float2 a = act::both<ACT, true>(g[e]);
-            const float de = static_cast<float>(d[e]);
-            zg[e] = static_cast<CT>(de * u[e] * a.y);
-            zu[e] = static_cast<CT>(de * a.x);
+            const float de = static_cast<float>(d[e]), vg = de * u[e] * a.y, vu = de * a.x;
+            zg[e] = static_cast<CT>(vg), zu[e] = static_cast<CT>(vu);
+            rg[e] = static_cast<CT>(rest_of<CT>(vg)), ru[e] = static_cast<CT>(rest_of<CT>(vu));
         }
         // whole pieces: ldz is a multiple of 8, and what lies behind f is not used
         *reinterpret_cast<ct8*>(dg + i * ldz + j) = zg;
         *reinterpret_cast<ct8*>(du + i * ldz + j) = zu;
+        if (rest) {
+            *reinterpret_cast<ct8*>(dg + rest + i * ldz + j) = rg;
+            *reinterpret_cast<ct8*>(du + rest + i * ldz + j) = ru;
+        }
     }
 }
 
@@ -280,7 +292,7 @@ template <class C, int ACT>
 __global__ __launch_bounds__(C::NT) void k_gated_again_dz(Operand X, PairOperand W, int64_t kbytes,
                                                           const Value<C::ELEM>* __restrict__ dy, int64_t ldz,
                                                           Value<C::ELEM>* __restrict__ dg, Value<C::ELEM>* __restrict__ du,
-                                                          Order order) {
+                                                          int64_t rest, Order order) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
     int64_t tm, tn;
@@ -308,12 +320,15 @@ __global__ __launch_bounds__(C::NT) void k_gated_again_dz(Operand X, PairOperand
         }
     // whole pieces: ldz is a multiple of 8, and what lies behind f is not used
     const auto same = [](float v) { return v; };
+    const auto left = [](float v) { return rest_of<Value<C::ELEM>>(v); };
     store_tile<H>(z, slice, dg, ldz, at.i0, at.f0, n, ldz, true, at.lane, same);
+    if (rest) store_tile<H>(z, slice, dg + rest, ldz, at.i0, at.f0, n, ldz, true, at.lane, left);
 #pragma unroll
     for (int x = 0; x < H::BL; ++x)
 #pragma unroll
         for (int b = 0; b < H::BR; ++b) z[x][b] = acc[x][b];
     store_tile<H>(z, slice, du, ldz, at.i0, at.f0, n, ldz, true, at.lane, same);
+    if (rest) store_tile<H>(z, slice, du + rest, ldz, at.i0, at.f0, n, ldz, true, at.lane, left);
 }
 
 // Sums of part `part` of a product in fp32, or its result.
@@ -338,10 +353,13 @@ __device__ __forceinline__ int64_t part_of(int64_t kbytes, int64_t part_bytes, i
     return kb > 0 ? kb : 0;
 }
 
-// dx = dg Wg + du Wu, or the part blockIdx.y of its sum over f.
-template <class C>
+// dx = dg Wg + du Wu, or the part blockIdx.y of its sum over f; TWO: over the
+// rests of dg and du too, `rest` bytes on.  (As a loop in the large tiles it
+// costs registers: dx of 4096 x 4096 from 8192 484 us, 563.)
+template <class C, bool TWO>
 __global__ __launch_bounds__(C::NT) void k_gated_dx(Operand Zg, Operand Zu, Operand Wg, Operand Wu, int64_t kbytes,
-                                                    int64_t part_bytes, Value<C::ELEM>* __restrict__ dx, float* __restrict__ sums,
+                                                    int64_t part_bytes, int64_t rest, Value<C::ELEM>* __restrict__ dx,
+                                                    float* __restrict__ sums,
                                                     Order order) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
@@ -352,15 +370,20 @@ __global__ __launch_bounds__(C::NT) void k_gated_dx(Operand Zg, Operand Zu, Oper
     f32x4 acc[C::BL][C::BR];
     tile_product<C>(acc, Zg, Wg, tm * C::TL, tn * C::TR, kb, lds);
     tile_product<C>(acc, Zu, Wu, tm * C::TL, tn * C::TR, kb, lds, true);
+    if (TWO) {
+        Zg.data += rest, Zu.data += rest;
+        tile_product<C>(acc, Zg, Wg, tm * C::TL, tn * C::TR, kb, lds, true);
+        tile_product<C>(acc, Zu, Wu, tm * C::TL, tn * C::TR, kb, lds, true);
+    }
     store_result<C>(acc, lds, dx, sums, blockIdx.y, Zg.rows, Wg.rows, tm, tn);
 }
 
 // dWg = dg^T x (blockIdx.z 0) and dWu = du^T x (1), or the part blockIdx.y of
-// their sums over x's rows.
-template <class C>
+// their sums over x's rows; TWO: of the rests of dg and du too.
+template <class C, bool TWO>
 __global__ __launch_bounds__(C::NT) void k_gated_dw(Operand Zg, Operand Zu, Operand X, int64_t kbytes, int64_t part_bytes,
-                                                    Value<C::ELEM>* __restrict__ dwg, Value<C::ELEM>* __restrict__ dwu,
-                                                    float* __restrict__ sums, Order order) {
+                                                    int64_t rest, Value<C::ELEM>* __restrict__ dwg,
+                                                    Value<C::ELEM>* __restrict__ dwu, float* __restrict__ sums, Order order) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
     int64_t tm, tn, k0;
@@ -371,6 +394,10 @@ __global__ __launch_bounds__(C::NT) void k_gated_dw(Operand Zg, Operand Zu, Oper
     Z.data += k0 / 2 * Z.ld, X.data += k0 / 2 * X.ld;
     f32x4 acc[C::BL][C::BR];
     tile_product<C>(acc, Z, X, tm * C::TL, tn * C::TR, kb, lds);
+    if (TWO) {
+        Z.data += rest;
+        tile_product<C>(acc, Z, X, tm * C::TL, tn * C::TR, kb, lds, true);
+    }
     store_result<C>(acc, lds, up ? dwu : dwg, sums, blockIdx.z * gridDim.y + blockIdx.y, Z.rows, X.rows, tm, tn);
 }
 
@@ -413,14 +440,18 @@ hipError_t by_gated_tile(GatedTile tile, F f) {
         default: return f(Gated<T256x256<ELEM>>{});
     }
 }
+// f of a tile and whether the product is over two terms.
 template <int ELEM, bool L, bool R, class F>
-hipError_t by_product_tile(ProductTile tile, F f) {
+hipError_t by_product_tile(ProductTile tile, bool two, F f) {
+    if (two)
+        return tile == ProductTile::k64x64 ? f(Across<T64x64<ELEM>, L, R>{}, std::true_type{})
+                                           : f(Across<T128x256<ELEM>, L, R>{}, std::true_type{});
     switch (tile) {
-        case ProductTile::k64x64: return f(Across<T64x64<ELEM>, L, R>{});
-        case ProductTile::k64x256: return f(Across<T64x256<ELEM>, L, R>{});
-        case ProductTile::k128x128: return f(Across<T128x128<ELEM>, L, R>{});
-        case ProductTile::k128x256: return f(Across<T128x256<ELEM>, L, R>{});
-        default: return f(Across<T256x256<ELEM>, L, R>{});
+        case ProductTile::k64x64: return f(Across<T64x64<ELEM>, L, R>{}, std::false_type{});
+        case ProductTile::k64x256: return f(Across<T64x256<ELEM>, L, R>{}, std::false_type{});
+        case ProductTile::k128x128: return f(Across<T128x128<ELEM>, L, R>{}, std::false_type{});
+        case ProductTile::k128x256: return f(Across<T128x256<ELEM>, L, R>{}, std::false_type{});
+        default: return f(Across<T256x256<ELEM>, L, R>{}, std::false_type{});
     }
 }
 template <class F>
@@ -481,7 +512,7 @@ hipError_t backward(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
         if (j.pre) {
             const dim3 grid(blocks_of(j.f, 2048), static_cast<unsigned>(j.n < 16384 ? j.n : 16384));
             hipLaunchKernelGGL((k_gated_dz<CT, ACT>), grid, dim3(256), 0, stream, j.pre, static_cast<const CT*>(j.dy), j.n, j.f,
-                               ldz, dg, du);
+                               ldz, dg, du, p.rest / 2);
             return hipGetLastError();
         }
         return by_gated_tile<ELEM>(gated_tile(j.n, j.f), [&](auto cfg) {
@@ -489,7 +520,7 @@ hipError_t backward(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
             const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.f + C::TR / 2 - 1) / (C::TR / 2);
             const Order order = Order::make(tm, tn, 1);
             hipLaunchKernelGGL((k_gated_again_dz<C, ACT>), dim3(order.grid()), dim3(C::NT), 0, stream, operand(j.x, j.k, j.n),
-                               pair_operand(j), 2 * j.k, static_cast<const CT*>(j.dy), ldz, dg, du, order);
+                               pair_operand(j), 2 * j.k, static_cast<const CT*>(j.dy), ldz, dg, du, p.rest / 2, order);
             return hipGetLastError();
         });
     });
@@ -499,28 +530,28 @@ hipError_t backward(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
         return hipGetLastError();
     };
     if (e == hipSuccess && j.dx) {
-        e = by_product_tile<ELEM, false, true>(p.dx_tile, [&](auto cfg) {
+        e = by_product_tile<ELEM, false, true>(p.dx_tile, p.rest != 0, [&](auto cfg, auto two) {
             using C = decltype(cfg);
             const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
             const Order order = Order::make(tm, tn, p.dx_parts);
             const int64_t part_bytes = ((2 * j.f + 127) / 128 + p.dx_parts - 1) / p.dx_parts * 128;
-            hipLaunchKernelGGL(k_gated_dx<C>, dim3(order.grid(), static_cast<unsigned>(p.dx_parts)), dim3(C::NT), 0, stream,
+            hipLaunchKernelGGL((k_gated_dx<C, decltype(two)::value>), dim3(order.grid(), static_cast<unsigned>(p.dx_parts)), dim3(C::NT), 0, stream,
                                operand(dg, ldz, j.n), operand(du, ldz, j.n), operand(j.wg, j.k, j.k), operand(j.wu, j.k, j.k),
-                               2 * j.f, part_bytes, static_cast<CT*>(j.dx), p.dx_parts > 1 ? sums : nullptr, order);
+                               2 * j.f, part_bytes, p.rest, static_cast<CT*>(j.dx), p.dx_parts > 1 ? sums : nullptr, order);
             return hipGetLastError();
         });
         if (e == hipSuccess && p.dx_parts > 1) e = join(sums, p.dx_parts, j.n * j.k, j.dx);
     }
     if (e == hipSuccess && (j.dwg || j.dwu)) {
         const unsigned both = j.dwg && j.dwu ? 2 : 1;
-        e = by_product_tile<ELEM, true, true>(p.dw_tile, [&](auto cfg) {
+        e = by_product_tile<ELEM, true, true>(p.dw_tile, p.rest != 0, [&](auto cfg, auto two) {
             using C = decltype(cfg);
             const int64_t tm = (j.f + C::TL - 1) / C::TL, tn = (j.k + C::TR - 1) / C::TR;
             const Order order = Order::make(tn, tm, p.dw_parts * both);
             const int64_t part_bytes = ((2 * j.n + 127) / 128 + p.dw_parts - 1) / p.dw_parts * 128;
-            hipLaunchKernelGGL(k_gated_dw<C>, dim3(order.grid(), static_cast<unsigned>(p.dw_parts), both), dim3(C::NT), 0, stream,
+            hipLaunchKernelGGL((k_gated_dw<C, decltype(two)::value>), dim3(order.grid(), static_cast<unsigned>(p.dw_parts), both), dim3(C::NT), 0, stream,
                                operand(dg, ldz, j.f), operand(du, ldz, j.f), operand(j.x, j.k, j.k), 2 * j.n, part_bytes,
-                               static_cast<CT*>(j.dwg), static_cast<CT*>(j.dwu), p.dw_parts > 1 ? sums : nullptr, order);
+                               p.rest, static_cast<CT*>(j.dwg), static_cast<CT*>(j.dwu), p.dw_parts > 1 ? sums : nullptr, order);
             return hipGetLastError();
         });
         if (p.dw_parts > 1) {
