@@ -24,6 +24,7 @@
 #include "activation.h"
 #include "launch_ffn.h"
 #include "mma_core.h"
+#include "w4_layout.h"
 
 namespace swz {
 namespace {
@@ -78,17 +79,6 @@ __device__ __forceinline__ void swap16(int& a, int& b) {
     a = static_cast<int>(r[0]), b = static_cast<int>(r[1]);
 }
 
-// Which 8 values of k (of 16 in a block of 128) lane g has in product s.
-template <int GROUP>
-__device__ __forceinline__ int unit_of(int s, int g) {
-    if constexpr (GROUP == 128) return 4 * g + s;
-    // words s and s + 2 exchanged between lanes g and g ^ 2: lanes 0, 1 keep the
-    // first group's, lanes 2, 3 take theirs
-    if constexpr (GROUP == 64) return 8 * (s / 2) + 4 * (g & 1) + 2 * (g / 2) + s % 2;
-    // and words s and s + 1 between lanes g and g ^ 1
-    return 4 * s + 2 * (g / 2) + (g & 1);
-}
-
 // What bounds it beside W's bytes is the way of addresses: an instruction whose
 // lanes touch many lines costs by the line.  So X comes in whole 256-byte runs, four
 // rows an instruction, and the scales and zero points of 32 groups at a time.  8 x
@@ -104,20 +94,15 @@ __device__ __forceinline__ int unit_of(int s, int g) {
 // that runs each instruction a few times waits for the instructions (4 x 2048 x 1024
 // gated: 4.7 us, 12 with four blocks in a step).
 //
-// In LDS: row r's 16-byte piece c of W at 4 r + (c ^ (r / 4)), its 16-byte unit u of X
-// at 16 r + (u ^ (r mod 16)), so that the 16 rows of a fragment fall on different banks.
+// What a wave holds in LDS, and where: W4Layout.
 // MATS: 1, or 2 for a gated block.  XL: X's rows in fours.
 template <bool BF16, int GROUP, bool ZERO, int MATS, int NB, int XL, int WAVES>
 __device__ __forceinline__ void gemm_w4(const uint8_t* __restrict__ x, const WeightsW4& w0, const WeightsW4& w1, int64_t m, int64_t n,
                                         int64_t k, int act, Value<BF16>* __restrict__ c) {
     using V = Value<BF16>;
-    constexpr int MB = XL < 4 ? 1 : XL / 4;             // blocks of 16 rows of X
-    constexpr int PER = 128 / GROUP, COLS = MATS * NB;  // groups of a block; blocks of 16 rows of either W
-    // A wave's LDS: the scales and zero points of kRun groups, each row's behind the
-    // other's with a gap; a block of W; of X.
-    constexpr int kRun = 32, kScaleRow = 2 * kRun + 4, kZeroRow = kRun + 4, kZero = COLS * 16 * kScaleRow;
-    constexpr int kW = (kZero + (ZERO ? COLS * 16 * kZeroRow : 0) + 15) / 16 * 16, kX = kW + COLS * 1024;
-    constexpr int kRed = MB * COLS * 1024, kOwn = kX + XL * 1024;
+    using L = W4Layout<GROUP, ZERO, MATS, NB, XL>;
+    constexpr int MB = L::MB, PER = L::PER, COLS = L::COLS, kRun = L::kRun, kScaleRow = L::kScaleRow, kZeroRow = L::kZeroRow;
+    constexpr int kZero = L::kZero, kW = L::kW, kX = L::kX, kRed = L::kRed, kOwn = L::kOwn;
     __shared__ i32x4 lds_v[WAVES * (kOwn > kRed ? kOwn : kRed) / 16];
     const int t = threadIdx.x, lane = t % 64, g = lane / 16, l16 = lane % 16;
     const int wave = __builtin_amdgcn_readfirstlane(t / 64);
@@ -217,18 +202,18 @@ __device__ __forceinline__ void gemm_w4(const uint8_t* __restrict__ x, const Wei
     auto read = [&](Block& v, int units) {
 #pragma unroll
         for (int o = 0; o < COLS; ++o)
-            v.q[o] = *reinterpret_cast<const lds_i32x4*>(own + kW + o * 1024 + 16 * (4 * l16 + (g ^ (l16 / 4))));
+            v.q[o] = *reinterpret_cast<const lds_i32x4*>(own + L::w_at(o, l16, g));
 #pragma unroll
         for (int a = 0; a < MB; ++a)
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-                v.x[a][s] = *reinterpret_cast<const lds_i32x4*>(own + kX + a * 4096 + 16 * (16 * l16 + (unit_of<GROUP>(s, g) ^ l16)));
+                v.x[a][s] = *reinterpret_cast<const lds_i32x4*>(own + L::x_at(a, L::x_row(l16), w4_unit_of<GROUP>(s, g)));
         if (units < 16) {
 #pragma unroll
             for (int a = 0; a < MB; ++a)
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
-                    if (unit_of<GROUP>(s, g) >= units) v.x[a][s] = i32x4{0, 0, 0, 0};
+                    if (w4_unit_of<GROUP>(s, g) >= units) v.x[a][s] = i32x4{0, 0, 0, 0};
         }
     };
     auto scale = [](const uint32_t* s, int p) {
