@@ -5,8 +5,9 @@ libswz.so; there is no Python or CPU fallback, and importing this package
 raises if the library has not been built (``python tiled_movement_amd/build.py``).
 
 Functions take torch tensors (or raw device addresses as ints) and the
-library's enum values; they run on the current torch stream unless a stream
-is given, and raise ``SwzError`` on a negative status.
+library's enum values; they run on the current torch stream of their tensors'
+device unless a stream is given (a call of addresses alone on the NULL
+stream), and raise ``SwzError`` on a negative status.
 """
 
 from __future__ import annotations
@@ -437,7 +438,7 @@ def swz_quant_f8(x, q, scale, rows: int, cols: int, x_type: int = X_BF16, f8_typ
          q=(q, _span(rows, cols, ld_q), f8), scale=(scale, _f8_scale_bytes(rows, cols, block, scale_type), sc),
          qt=(qt, _span(cols, rows, ld_qt), f8), scale_t=(scale_t, _f8_scale_bytes(cols, rows, block, scale_type), sc))
     _check(lib.swz_quant_f8(_ptr(x), x_type, rows, cols, ld_x, f8_type, block, scale_type, _ptr(q), _ptr(scale), ld_q,
-                            _ptr(qt), _ptr(scale_t), ld_qt, _stream(stream, x, q, qt)), "swz_quant_f8")
+                            _ptr(qt), _ptr(scale_t), ld_qt, _stream(stream, x, q, scale, qt, scale_t)), "swz_quant_f8")
 
 
 def swz_gemm_f8(a, scale_a, b, scale_b, c, m: int, n: int, k: int, lda: Optional[int] = None,
@@ -452,7 +453,7 @@ def swz_gemm_f8(a, scale_a, b, scale_b, c, m: int, n: int, k: int, lda: Optional
          b=(b, _span(n, k16, ldb), _F8.get(b_type)), scale_b=(scale_b, _f8_scale_bytes(n, k, b_block, scale_type), sc),
          c=(c, (2 if c_type == C_BF16 else 4) * m * n, _C.get(c_type)))
     _check(lib.swz_gemm_f8(_ptr(a), _ptr(scale_a), _ptr(b), _ptr(scale_b), _ptr(c), m, n, k, lda, ldb, a_type, b_type,
-                           a_block, b_block, scale_type, c_type, _stream(stream, a, b, c)), "swz_gemm_f8")
+                           a_block, b_block, scale_type, c_type, _stream(stream, a, b, c, scale_a, scale_b)), "swz_gemm_f8")
 
 
 def swz_linear_loss_workspace(n: int, v: int, k: int, top: int = 1, grad: bool = False) -> int:
@@ -474,7 +475,7 @@ def swz_linear_ce(h, w, target, loss, lse, zt, n: int, v: int, k: int, ws, x_typ
     _buf("swz_linear_ce", h=(h, 2 * n * k, xt), w=(w, 2 * v * k, xt), target=(target, 8 * n, _INDEX),
          loss=(loss, 4 * n, _FLOAT), lse=(lse, 4 * n, _FLOAT), zt=(zt, 4 * n, _FLOAT), ws=(ws, need))
     _check(lib.swz_linear_ce(_ptr(h), _ptr(w), x_type, _ptr(target), _ptr(loss), _ptr(lse), _ptr(zt), n, v, k, _ptr(ws),
-                             _ws_bytes(ws, need), _stream(stream, h, w)), "swz_linear_ce")
+                             _ws_bytes(ws, need), _stream(stream, h, w, target, loss, lse, zt, ws)), "swz_linear_ce")
 
 
 def swz_linear_ce_grad(h, w, target, lse, zt, upstream, dh, dw, n: int, v: int, k: int, ws, x_type: int = X_BF16,
@@ -486,7 +487,8 @@ def swz_linear_ce_grad(h, w, target, lse, zt, upstream, dh, dw, n: int, v: int, 
          lse=(lse, 4 * n, _FLOAT), zt=(zt, 4 * n, _FLOAT), upstream=(upstream, 4 * n, _FLOAT), dh=(dh, 2 * n * k, xt),
          dw=(dw, 2 * v * k, xt), ws=(ws, need))
     _check(lib.swz_linear_ce_grad(_ptr(h), _ptr(w), x_type, _ptr(target), _ptr(lse), _ptr(zt), _ptr(upstream), _ptr(dh),
-                                  _ptr(dw), n, v, k, _ptr(ws), _ws_bytes(ws, need), _stream(stream, h, w)),
+                                  _ptr(dw), n, v, k, _ptr(ws), _ws_bytes(ws, need),
+                                  _stream(stream, h, w, target, lse, zt, upstream, dh, dw, ws)),
            "swz_linear_ce_grad")
 
 
@@ -499,7 +501,8 @@ def swz_linear_distill(h, w, index, teacher, loss, lse, zt, n: int, v: int, k: i
          teacher=(teacher, 4 * n * top, _FLOAT), loss=(loss, 4 * n, _FLOAT), lse=(lse, 4 * n, _FLOAT),
          zt=(zt, 4 * n * top, _FLOAT), ws=(ws, need))
     _check(lib.swz_linear_distill(_ptr(h), _ptr(w), x_type, _ptr(index), _ptr(teacher), top, tau, _ptr(loss), _ptr(lse),
-                                  _ptr(zt), n, v, k, _ptr(ws), _ws_bytes(ws, need), _stream(stream, h, w)),
+                                  _ptr(zt), n, v, k, _ptr(ws), _ws_bytes(ws, need),
+                                  _stream(stream, h, w, index, teacher, loss, lse, zt, ws)),
            "swz_linear_distill")
 
 
@@ -513,7 +516,8 @@ def swz_linear_distill_grad(h, w, index, teacher, lse, zt, upstream, dh, dw, n: 
          upstream=(upstream, 4 * n, _FLOAT), dh=(dh, 2 * n * k, xt), dw=(dw, 2 * v * k, xt), ws=(ws, need))
     _check(lib.swz_linear_distill_grad(_ptr(h), _ptr(w), x_type, _ptr(index), _ptr(teacher), top, tau, _ptr(lse), _ptr(zt),
                                        _ptr(upstream), _ptr(dh), _ptr(dw), n, v, k, _ptr(ws), _ws_bytes(ws, need),
-                                       _stream(stream, h, w)), "swz_linear_distill_grad")
+
+                                       _stream(stream, h, w, index, teacher, lse, zt, upstream, dh, dw, ws)), "swz_linear_distill_grad")
 
 
 def swz_gated(x, wg, wu, y, n: int, f: int, k: int, x_type: int = X_BF16, act: int = ACT_SILU, pre=None, stream=None) -> None:
@@ -521,7 +525,7 @@ def swz_gated(x, wg, wu, y, n: int, f: int, k: int, x_type: int = X_BF16, act: i
     xt = _X.get(x_type)
     _bufs("swz_gated", (("x", x, 2 * n * k, xt), ("wg", wg, 2 * f * k, xt), ("wu", wu, 2 * f * k, xt), ("y", y, 2 * n * f, xt),
                         ("pre", pre, 8 * n * f, _FLOAT)))
-    _check(lib.swz_gated(_ptr(x), _ptr(wg), _ptr(wu), x_type, act, _ptr(y), _ptr(pre), n, f, k, _stream(stream, x, wg)),
+    _check(lib.swz_gated(_ptr(x), _ptr(wg), _ptr(wu), x_type, act, _ptr(y), _ptr(pre), n, f, k, _stream(stream, x, wg, wu, y, pre)),
            "swz_gated")
 
 
@@ -541,7 +545,8 @@ def swz_gated_grad(x, wg, wu, dy, dx, dwg, dwu, n: int, f: int, k: int, ws, x_ty
                              ("pre", pre, 8 * n * f, _FLOAT), ("dx", dx, 2 * n * k, xt), ("dwg", dwg, 2 * f * k, xt),
                              ("dwu", dwu, 2 * f * k, xt), ("ws", ws, need, None)))
     _check(lib.swz_gated_grad(_ptr(x), _ptr(wg), _ptr(wu), x_type, act, _ptr(dy), _ptr(pre), _ptr(dx), _ptr(dwg), _ptr(dwu), n,
-                              f, k, _ptr(ws), _ws_bytes(ws, need), _stream(stream, x, wg)), "swz_gated_grad")
+                              f, k, _ptr(ws), _ws_bytes(ws, need),
+                              _stream(stream, x, wg, wu, dy, pre, dx, dwg, dwu, ws)), "swz_gated_grad")
 
 
 _CODES = _Type(1, "uint8")
@@ -557,7 +562,8 @@ def swz_quant_w4(w, q, scale, n: int, k: int, group: int = 128, w_type: int = X_
     groups = _w4_groups(n, k, group)
     _bufs("swz_quant_w4", (("w", w, n * k * (4 if w_type == X_F32 else 2), _X.get(w_type)), ("q", q, n * (k // 2), _CODES),
                            ("scale", scale, 2 * groups, _X.get(x_type)), ("zero", zero, groups, _CODES)))
-    _check(lib.swz_quant_w4(_ptr(w), w_type, n, k, group, x_type, _ptr(q), _ptr(scale), _ptr(zero), _stream(stream, w, q)),
+    _check(lib.swz_quant_w4(_ptr(w), w_type, n, k, group, x_type, _ptr(q), _ptr(scale), _ptr(zero),
+                            _stream(stream, w, q, scale, zero)),
            "swz_quant_w4")
 
 
@@ -566,7 +572,7 @@ def swz_dequant_w4(q, scale, w, n: int, k: int, group: int = 128, x_type: int = 
     xt, groups = _X.get(x_type), _w4_groups(n, k, group)
     _bufs("swz_dequant_w4", (("w", w, 2 * n * k, xt), ("q", q, n * (k // 2), _CODES), ("scale", scale, 2 * groups, xt),
                              ("zero", zero, groups, _CODES)))
-    _check(lib.swz_dequant_w4(_ptr(q), _ptr(scale), _ptr(zero), n, k, group, x_type, _ptr(w), _stream(stream, q, w)),
+    _check(lib.swz_dequant_w4(_ptr(q), _ptr(scale), _ptr(zero), n, k, group, x_type, _ptr(w), _stream(stream, q, w, scale, zero)),
            "swz_dequant_w4")
 
 
@@ -575,7 +581,8 @@ def swz_gemm_w4(x, q, scale, c, m: int, n: int, k: int, group: int = 128, x_type
     xt, groups = _X.get(x_type), _w4_groups(n, k, group)
     _bufs("swz_gemm_w4", (("x", x, 2 * m * k, xt), ("c", c, 2 * m * n, xt), ("q", q, n * (k // 2), _CODES),
                           ("scale", scale, 2 * groups, xt), ("zero", zero, groups, _CODES)))
-    _check(lib.swz_gemm_w4(_ptr(x), x_type, _ptr(q), _ptr(scale), _ptr(zero), group, _ptr(c), m, n, k, _stream(stream, x, q)),
+    _check(lib.swz_gemm_w4(_ptr(x), x_type, _ptr(q), _ptr(scale), _ptr(zero), group, _ptr(c), m, n, k,
+                           _stream(stream, x, q, scale, c, zero)),
            "swz_gemm_w4")
 
 
@@ -587,7 +594,8 @@ def swz_gated_w4(x, qg, scale_g, qu, scale_u, c, m: int, n: int, k: int, group: 
                            ("scale_g", scale_g, 2 * groups, xt), ("zero_g", zero_g, groups, _CODES), ("q_u", qu, codes, _CODES),
                            ("scale_u", scale_u, 2 * groups, xt), ("zero_u", zero_u, groups, _CODES)))
     _check(lib.swz_gated_w4(_ptr(x), x_type, act, _ptr(qg), _ptr(scale_g), _ptr(zero_g), _ptr(qu), _ptr(scale_u), _ptr(zero_u),
-                            group, _ptr(c), m, n, k, _stream(stream, x, qg)), "swz_gated_w4")
+                            group, _ptr(c), m, n, k,
+                            _stream(stream, x, qg, scale_g, qu, scale_u, c, zero_g, zero_u)), "swz_gated_w4")
 
 
 _X_OF = {}  # torch element types of the norm calls, filled by their first call
@@ -613,7 +621,6 @@ def _tensors(call: str, tensors):
 
     if not _X_OF:
         _X_OF.update({torch.bfloat16: X_BF16, torch.float16: X_F16, torch.float32: X_F32})
-    tensors = list(tensors)
     device = torch.cuda.current_device() if tensors else None
     alike = {type(t) for t in tensors} <= {torch.Tensor, torch.nn.Parameter}
     if not (alike and set(map(torch.Tensor.get_device, tensors)) <= {device} and all(map(torch.Tensor.is_contiguous, tensors))
@@ -652,20 +659,22 @@ def _norm_buffers(call: str, device, norm, floats: int, ws, need: int) -> None:
 
 def swz_grad_norm(tensors, norm, ws, stream=None) -> None:
     """norm[0] (fp32) = sqrt of the sum of all the tensors' squares."""
+    tensors = list(tensors)
     at, numel, types, _, device = _tensors("swz_grad_norm", tensors)
     need = _norm_workspace("swz_grad_norm", len(at))
     _norm_buffers("swz_grad_norm", device, norm, 1, ws, need)
     _check(lib.swz_grad_norm(_at(at), _at(numel), _at(types), len(at), _ptr(norm), _ptr(ws), _ws_bytes(ws, need),
-                             _stream(stream, norm, ws)), "swz_grad_norm")
+                             _stream(stream, norm, ws, *tensors[:1])), "swz_grad_norm")
 
 
 def swz_clip_grads(tensors, max_norm: float, norm, ws, out=None, stream=None) -> None:
     """The tensors scaled so that their norm together is at most max_norm, in place or into the tensors of `out`;
     norm (fp32 [2]): the norm before, and the factor."""
+    tensors = list(tensors)
     at, numel, types, kinds, device = _tensors("swz_clip_grads", tensors)
     to = None
     if out is not None:
-        to, to_numel, _, to_kinds, _ = _tensors("swz_clip_grads", out)
+        to, to_numel, _, to_kinds, _ = _tensors("swz_clip_grads", list(out))
         if len(to) != len(at):
             raise ValueError(f"swz_clip_grads: {len(to)} tensors to write, {len(at)} to read")
         if to_numel != numel or to_kinds != kinds:
@@ -674,7 +683,7 @@ def swz_clip_grads(tensors, max_norm: float, norm, ws, out=None, stream=None) ->
     need = _norm_workspace("swz_clip_grads", len(at))
     _norm_buffers("swz_clip_grads", device, norm, 2, ws, need)
     _check(lib.swz_clip_grads(_at(at), None if to is None else _at(to), _at(numel), _at(types), len(at), max_norm, _ptr(norm),
-                              _ptr(ws), _ws_bytes(ws, need), _stream(stream, norm, ws)), "swz_clip_grads")
+                              _ptr(ws), _ws_bytes(ws, need), _stream(stream, norm, ws, *tensors[:1])), "swz_clip_grads")
 
 
 def swz_fold(params, base: int, active: int):
