@@ -106,3 +106,44 @@ def test_gelu_of_4_bit_weights_keeps_its_digits(dt, low, top, m):
     zd = z.double().numpy()
     want = gelu64(zd)[0] * by
     assert np.all(np.abs(c.double().cpu().numpy() - want) <= (step + own(zd)) * np.abs(want))
+
+
+def test_dx_of_weights_behind_2_to_32_bytes():
+    """dx of weights of 4.6 GB each, with dy in a few columns only, on both sides of 2^32 bytes: sums short enough that one
+    column left out, or taken from another row of a weight, shows."""
+    announce("gated dx 2^32")
+    n, f, k = 24, 140001, 16392
+    u32 = 2.0 ** -23
+    g = torch.Generator(device=DEV)
+    g.manual_seed(13)
+    wg, wu = (torch.empty(f, k, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    for w in (wg, wu):
+        for i in range(0, f, 20000):
+            w[i:i + 20000] = torch.randn(min(20000, f - i), k, generator=g, device=DEV) / 128
+    border = (1 << 32) // (2 * k)
+    cols = torch.tensor([0, 65537, border - 1, border, border + 1, 131072, f - 1], device=DEV)
+    x = torch.randn(n, k, generator=g, device=DEV).bfloat16()
+    dy = torch.zeros(n, f, dtype=torch.bfloat16, device=DEV)
+    dy[:, cols] = (torch.rand(n, cols.numel(), generator=g, device=DEV) + 0.5).bfloat16()
+    y, pre = torch.empty_like(dy), torch.empty(2, n, f, device=DEV)
+    ws = torch.empty(T.swz_gated_workspace(n, f, k), dtype=torch.uint8, device=DEV)
+    T.swz_gated(x, wg, wu, y, n, f, k, pre=pre)
+    dx = [torch.full_like(x, float("nan")) for _ in range(2)]
+    T.swz_gated_grad(x, wg, wu, dy, dx[0], None, None, n, f, k, ws, pre=pre)
+    T.swz_gated_grad(x, wg, wu, dy, dx[1], None, None, n, f, k, ws)
+    torch.cuda.synchronize()
+    zg, zu, d = pre[0][:, cols].double(), pre[1][:, cols].double(), dy[:, cols].double()
+    s = torch.sigmoid(zg)
+    dg, du = d * zu * s * (1 + zg * (1 - s)), d * zg * s
+    terms = torch.stack([dg[:, i, None] * wg[c].double() + du[:, i, None] * wu[c].double() for i, c in enumerate(cols)])
+    ref = terms.sum(0)
+    size = sum(dg[:, i, None].abs() * wg[c].double().abs() + du[:, i, None].abs() * wu[c].double().abs() for i, c in enumerate(cols))
+    # dg and du off by a rounding and 64 u (1 + |z|) of the activation, |z| below 8; some 14 terms in fp32; one rounding
+    assert float(zg.abs().max()) < 8 and float(zu.abs().max()) < 8
+    tol = (2.0 ** -8 + 64 * 9 * u32 + 64 * u32) * size
+    tol += 2.0 ** -8 * (ref.abs() + tol)
+    assert bool(((dx[0].double() - ref).abs() <= tol).all())
+    for wrong in [torch.zeros_like(ref), -ref] + [ref - t for t in terms] + [ref - t + t.roll(1, 1) for t in terms]:
+        assert float(((wrong - ref).abs() > tol).double().mean()) > 0.5
+    # g and u made again differ in their sums' order: a step of dg and du each where that tips a rounding
+    assert bool(((dx[1].double() - dx[0].double()).abs() <= 2.0 ** -7 * size + 2.0 ** -7 * ref.abs()).all())

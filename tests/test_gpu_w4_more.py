@@ -36,3 +36,35 @@ def test_few_rows_have_the_bits_of_a_full_block(n, k, dt, group, zero):
         want = run(16, two)
         for m in range(1, 10):
             assert torch.equal(run(m, two), want[:m]), (m, two)
+
+
+def test_products_of_codes_behind_2_to_32_bytes():
+    """Codes of 4.9 GB: rows from all over, those around 2^32 bytes among them, have the bits that a call on a copy of them
+    gives (a row of W has its sums in the same order whatever stands beside it); one and 20 rows of X, and the gated block."""
+    announce("w4 products 2^32")
+    n, k, group = 600001, 16416, 128
+    g = torch.Generator(device=DEV)
+    g.manual_seed(15)
+    groups = -(-k // group)
+    q = torch.randint(0, 1 << 62, (n * k // 16,), generator=g, device=DEV).view(torch.uint8).view(n, k // 2)
+    s = torch.empty(n, groups, device=DEV).uniform_(0.5, 2, generator=g).div_(128).bfloat16()
+    z = torch.randint(0, 16, (n, groups), generator=g, device=DEV, dtype=torch.uint8)
+    border = (1 << 32) // (k // 2)
+    rows = torch.cat([torch.arange(border - 300, border + 300, device=DEV), torch.arange(0, n, 149, device=DEV),
+                      torch.arange(n - 40, n, device=DEV)])
+    few = [t[rows].contiguous() for t in (q, s, z)]
+    assert int(rows.numel()) > 4096  # the same rule for the rows of a workgroup
+    x = torch.randn(20, k, generator=g, device=DEV).bfloat16()
+    for m in (1, 20):
+        for zero, zero_few in ((None, None), (z, few[2])):
+            c, want = torch.full((m, n), float("nan"), dtype=x.dtype, device=DEV), torch.empty(m, rows.numel(), dtype=x.dtype, device=DEV)
+            T.swz_gemm_w4(x[:m], q, s, c, m, n, k, group=group, zero=zero)
+            T.swz_gemm_w4(x[:m], *few[:2], want, m, rows.numel(), k, group=group, zero=zero_few)
+            torch.cuda.synchronize()
+            assert torch.equal(c[:, rows], want) and bool(c.isfinite().all())
+            assert want.double().std(dim=1).min() > 0.1  # nothing that zeros or one row in all places would give
+    c, want = torch.full((2, n), float("nan"), dtype=x.dtype, device=DEV), torch.empty(2, rows.numel(), dtype=x.dtype, device=DEV)
+    T.swz_gated_w4(x[:2], q, s, q, s, c, 2, n, k, group=group)
+    T.swz_gated_w4(x[:2], *few[:2], *few[:2], want, 2, rows.numel(), k, group=group)
+    torch.cuda.synchronize()
+    assert torch.equal(c[:, rows], want) and bool(c.isfinite().all()) and want.double().std(dim=1).min() > 0.1
