@@ -8,7 +8,8 @@ import math
 import numpy as np
 import pytest
 
-from test_gpu_gated import DEV, DT, announce
+from oracle import feed_forward as F
+from test_gpu_gated import DEV, DT, Case, announce
 
 import torch
 
@@ -147,3 +148,167 @@ def test_dx_of_weights_behind_2_to_32_bytes():
         assert float(((wrong - ref).abs() > tol).double().mean()) > 0.5
     # g and u made again differ in their sums' order: a step of dg and du each where that tips a rounding
     assert bool(((dx[1].double() - dx[0].double()).abs() <= 2.0 ** -7 * size + 2.0 ** -7 * ref.abs()).all())
+
+
+# ------------------------------------------------- fp16 gradients at the ends of the type's range
+class Ranged(Case):
+    """fp16 inputs whose dg and du are far from 1, x and the weights being `out` and 1 / out of their usual size, so that
+    dx (out > 1) or dwg and dwu (out < 1) are ordinary fp16 numbers."""
+
+    def __init__(self, n, k, f, act, dy, out, seed):
+        super().__init__(n, k, f, "fp16", act, seed=seed)
+        rng = np.random.default_rng(seed + 1)
+        half = DT["fp16"][0]
+        self.x = (torch.from_numpy(rng.standard_normal((n, k))) * out).to(half)
+        self.wg, self.wu = ((torch.from_numpy(rng.standard_normal((f, k))) * (s / out / np.sqrt(k))).to(half) for s in (1.5, 4.0))
+        self.dy = (torch.from_numpy(rng.uniform(-1, 1, (n, f))) * dy).to(half)
+
+    def near(self, d, which):
+        """Relative to its norm, a result is off by its rounding and by that of dg and du: each at most a half step, 2^-11,
+        and 0.4 of it in the mean, of terms of either sign."""
+        x, wg, wu, dy = (getattr(self, a).double().numpy() for a in ("x", "wg", "wu", "dy"))
+        want = dict(zip(("dx", "dwg", "dwu"), F.gated_grad(x, wg, wu, self.act, dy)))
+        for w in which:
+            assert np.abs(want[w]).max() < 65504 and np.linalg.norm(want[w]) > 0
+            rms = np.sqrt(np.mean(want[w] ** 2))
+            assert rms > 2.0 ** -11  # a normal number, so that steps are relative
+            got = d[w].double().cpu().numpy()
+            assert np.isfinite(got).all() and np.linalg.norm(got - want[w]) <= 2.0 ** -10 * np.linalg.norm(want[w]), w
+        return F.gated_grad(x, wg, wu, self.act, dy)[3:]
+
+
+SIZES = [(1, 8, 5), (3, 72, 130), (40, 264, 200), (300, 264, 333), (200, 1032, 2000)]
+
+
+@pytest.mark.parametrize("pre", [True, False])
+@pytest.mark.parametrize("act", F.ACTS)
+@pytest.mark.parametrize("n,k,f", SIZES)
+@pytest.mark.parametrize("which,dy,out", [(("dx",), 60000.0, 2.0 ** 9), (("dwg", "dwu"), 60000.0, 2.0 ** -9)])
+def test_gradients_of_products_beyond_fp16(which, dy, out, n, k, f, act, pre):
+    """dg of up to 10^6: no fp16 numbers, but the gradients are."""
+    announce("gated range", n, k, f, act, pre, which)
+    c = Ranged(n, k, f, act, dy, out, seed=n + f)
+    d = c.device()
+    c.forward(d, pre)
+    c.backward(d, pre, which)
+    torch.cuda.synchronize()
+    dg, du = c.near(d, which)
+    assert n * f < 100 or np.abs(dg).max() > 65520
+
+
+@pytest.mark.parametrize("pre", [True, False])
+@pytest.mark.parametrize("n,k,f", SIZES)
+@pytest.mark.parametrize("which,dy,out", [(("dx",), 2.0 ** -14, 2.0 ** -10), (("dwg", "dwu"), 2.0 ** -14, 2.0 ** 10)])
+def test_gradients_of_products_below_fp16(which, dy, out, n, k, f, pre):
+    """dg and du of 2^-16 and less keep their digits."""
+    announce("gated range", n, k, f, pre, which)
+    c = Ranged(n, k, f, "silu", dy, out, seed=n + f)
+    c.dy = (c.dy.double() * 2.0 ** -5).half()  # of few digits themselves
+    d = c.device()
+    c.forward(d, pre)
+    c.backward(d, pre, which)
+    torch.cuda.synchronize()
+    c.near(d, which)
+
+
+@pytest.mark.parametrize("n,k,f", SIZES[1:])
+def test_range_of_one_product_leaves_the_other_alone(n, k, f):
+    """dg beyond fp16 and du below its normal numbers in one call: u is large and the activation small."""
+    announce("gated two ranges", n, k, f)
+    rng = np.random.default_rng(n)
+    c = Ranged(n, k, f, "silu", 64.0, 1.0, seed=n + k)
+    c.x[:, 0] = 1.0
+    c.wg = (torch.from_numpy(rng.standard_normal((f, k))) * 2.0 ** -22).half()
+    c.wg[:, 0] = 0.0
+    c.wu[:, 0] = 12000.0
+    c.wu[:, 1:] = 0.0
+    for pre in (True, False):
+        d = c.device()
+        c.forward(d, pre)
+        c.backward(d, pre)
+        torch.cuda.synchronize()
+        x, wg, wu, dy = (getattr(c, a).double().numpy() for a in ("x", "wg", "wu", "dy"))
+        _, _, dwu, dg, du = F.gated_grad(x, wg, wu, "silu", dy)
+        assert np.abs(dg).max() > 65520 and np.abs(du).max() < 2.0 ** -8
+        got = d["dwu"].double().cpu().numpy()
+        # a half step of dwu and of du (held at 2^-10 of the largest at least), fp16's smallest step for what is below it
+        assert np.linalg.norm(got - dwu) <= 2.0 ** -10 * np.linalg.norm(dwu) + 2.0 ** -25 * np.sqrt(dwu.size)
+
+
+def test_infinities_stay_in_their_rows_beyond_the_range():
+    """Values that are not finite do not count for the range of the others."""
+    announce("gated range, infinities")
+    c = Ranged(90, 72, 130, "silu", 60000.0, 2.0 ** 9, seed=4)
+    c.dy[4] = 0.0
+    d = c.device()
+    c.forward(d)
+    c.backward(d, which=("dx",))
+    torch.cuda.synchronize()
+    want = d["dx"].clone()
+    assert bool(want.isfinite().all())
+    d["dy"][4, 3], d["dy"][5, 7] = float("inf"), float("nan")
+    for pre in (True, False):
+        c.forward(d, pre)
+        c.backward(d, pre, which=("dx",))
+        torch.cuda.synchronize()
+        keep = [i for i in range(90) if i not in (4, 5)]
+        assert bool((d["dx"][keep].float() - want[keep].float()).abs().max() <= 2.0 ** -10 * want.float().abs().max())
+        assert not bool(d["dx"][4].isfinite().any()) and bool(d["dx"][5].isnan().all())
+
+
+def test_range_is_each_calls_own():
+    """One workspace, calls of large, ordinary and small gradients in turn, and replays of one graph over all of them."""
+    announce("gated range in turn")
+    n, k, f = 40, 264, 200
+    cases = [Ranged(n, k, f, "silu", dy, out, seed=7) for dy, out in ((60000.0, 2.0 ** 9), (1.0, 1.0), (2.0 ** -16, 2.0 ** -9))]
+    d = cases[0].device()
+    order = [0, 1, 2, 1, 0, 2, 0]
+    want = {}
+    for pre in (True, False):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            cases[0].forward(d, pre)
+            cases[0].backward(d, pre, ("dx",))
+        for i in order:
+            for a in ("x", "wg", "wu", "dy"):
+                d[a].copy_(getattr(cases[i], a))
+            cases[i].forward(d, pre)
+            cases[i].backward(d, pre, ("dx",))
+            torch.cuda.synchronize()
+            cases[i].near(d, ("dx",))
+            assert torch.equal(want.setdefault((i, pre), d["dx"].clone()), d["dx"])
+            d["dx"].fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(d["dx"], want[i, pre])
+
+
+def test_range_where_workgroups_share_slots():
+    """More tiles of dg than the call tells apart (2048): gradients of made-again products, large at one place of the last
+    tile, against the same sums in 64 bits on the GPU."""
+    announce("gated range, many tiles")
+    n, k, f = 4100, 16, 16900
+    g = torch.Generator(device=DEV)
+    g.manual_seed(21)
+    rand = lambda *s: torch.rand(*s, generator=g, device=DEV) - 0.5  # noqa: E731
+    x, wg, wu = (rand(n, k) * 2.0 ** -7).half(), (rand(f, k) * 2.0 ** 8).half(), (rand(f, k) * 2.0 ** 8).half()
+    dy = (rand(n, f) * 0.01).half()
+    ws = torch.full((T.swz_gated_workspace(n, f, k),), 0xFF, dtype=torch.uint8, device=DEV)
+    zg, zu = x.double() @ wg.double().t(), x.double() @ wu.double().t()
+    for last in (0.0, 60000.0):
+        dy[n - 1, f - 1] = last
+        x[n - 1] = 2.0 ** -6
+        wg[f - 1], wu[f - 1] = 2.0 ** 8, 2.0 ** 8
+        zg[n - 1], zu[n - 1] = (w.double() @ x[n - 1].double() for w in (wg, wu))
+        zg[:, f - 1], zu[:, f - 1] = (x.double() @ w[f - 1].double() for w in (wg, wu))
+        dwg, dwu = torch.full_like(wg, float("nan")), torch.full_like(wu, float("nan"))
+        T.swz_gated_grad(x, wg, wu, dy, None, dwg, dwu, n, f, k, ws, x_type=T.X_F16)
+        torch.cuda.synchronize()
+        s = torch.sigmoid(zg)
+        for got, d in ((dwg, dy.double() * zu * s * (1 + zg * (1 - s))), (dwu, dy.double() * zg * s)):
+            assert (float(d.abs().max()) > 65520) == (last > 0)
+            want = d.t().contiguous() @ x.double()
+            err = (got.double() - want).norm(dim=1)
+            # rounding of d and of the result; what the largest leaves of the others: 2^-25 of fp16 at its scale
+            size = (d.abs().t().contiguous() @ x.double().abs()).norm(dim=1)
+            assert bool((err <= 2.0 ** -10 * want.norm(dim=1) + 2.0 ** -12 * size).all())

@@ -209,7 +209,8 @@ swz::GatedPlan plan_gated(int64_t n, int64_t f, int64_t k) {
     p.dg = 0;
     p.du = up(2 * n * p.ldz, 256);
     p.rest = two ? 2 * p.du : 0;
-    p.sums = 2 * p.du + p.rest;
+    p.slots = 2 * p.du + p.rest;
+    p.sums = p.slots + (n > 0 ? 256 + 2 * 4 * swz::kGatedSlots : 0);
     p.bytes = p.sums + up(dx > dw ? dx : dw, 256);
     return p;
 }

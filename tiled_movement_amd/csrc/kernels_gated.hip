@@ -9,7 +9,8 @@
 // place against 4 k operations to make them again).
 //
 // Backward: dg and du are made once, in x's type (as two terms for small
-// products: gated_two_terms()), by elements from the kept g
+// products: gated_two_terms(); in fp16 times a power of two where they leave its
+// range: held_times()), by elements from the kept g
 // and u or by the forward products over again.  The products that follow sum over
 // f (dx) and over the rows of x (dW), where the weights, dg, du and x
 // lie across the sum; they are read as they lie, by transposing reads out of
@@ -237,6 +238,86 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(const uint8_t* __r
     }
 }
 
+// What a call holds dg (du) times, from the bits of its largest finite magnitude m.
+// 1 in bf16, whose range is fp32's.  In fp16 1 where m is 2^-4 to below 65520:
+// it rounds to a number, and what is 2^-10 of it still has all its digits; else
+// the power of two that brings m to 2^14 .. 2^15, but 2^40 at most.
+template <int ELEM>
+__device__ __forceinline__ float held_times(uint32_t bits) {
+    if constexpr (ELEM != kF16) return 1.f;
+    if (bits == 0 || (bits >= 0x3d800000u && bits < 0x477ff000u)) return 1.f;
+    const int e = 141 - static_cast<int>(bits >> 23);
+    return __uint_as_float(static_cast<uint32_t>(127 + (e < 40 ? e : 40)) << 23);
+}
+// 1 / v of a power of two.
+__device__ __forceinline__ float inverse(float v) { return __uint_as_float((254u << 23) - __float_as_uint(v)); }
+// The larger of a and |v|'s bits, if v is finite.
+__device__ __forceinline__ uint32_t larger(uint32_t a, float v) {
+    const uint32_t b = magnitude_bits(v);
+    return b < 0x7f800000u && b > a ? b : a;
+}
+__device__ __forceinline__ uint32_t wave_most(uint32_t m) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t o = __shfl_xor(m, d);
+        m = o > m ? o : m;
+    }
+    return m;
+}
+// m is known when all of dg is made, so a call makes dg and du at 1 and leaves
+// their workgroups' magnitudes in slots, up to kGatedSlots of dg, then of du.  A
+// second launch joins them, leaves the result (`most`) for the products, and makes
+// both again where 1 is not what they are to be held times.
+// Gradients of 333 x 1000 to 2777 41.5 us without this, 46 with it; one slot for all
+// workgroups, raised by atomics, 51.  tmp: 2 NT / 64 words of LDS.
+template <int NT>
+__device__ __forceinline__ uint2 join_slots(const uint32_t* __restrict__ slots, int count, lds_u32* tmp) {
+    uint32_t m[2] = {0, 0};
+    for (int i = threadIdx.x; i < count; i += NT) {
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            const uint32_t v = slots[o * kGatedSlots + i];
+            m[o] = v > m[o] ? v : m[o];
+        }
+    }
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+        m[o] = wave_most(m[o]);
+        if (threadIdx.x % 64 == 0) tmp[o * (NT / 64) + threadIdx.x / 64] = m[o];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int w = 0; w < NT / 64; ++w) {
+            const uint32_t v = tmp[o * (NT / 64) + w];
+            m[o] = v > m[o] ? v : m[o];
+        }
+    __syncthreads();
+    return make_uint2(m[0], m[1]);
+}
+// A workgroup's magnitudes into its slots.  Workgroups beyond kGatedSlots share
+// them, zeroed before.
+template <int NT>
+__device__ __forceinline__ void leave_slots(uint32_t mg, uint32_t mu, uint32_t* slots, uint32_t id, bool shared, lds_u32* tmp) {
+    mg = wave_most(mg), mu = wave_most(mu);
+    if (threadIdx.x % 64 == 0) tmp[threadIdx.x / 64] = mg, tmp[NT / 64 + threadIdx.x / 64] = mu;
+    __syncthreads();
+    if (threadIdx.x >= 2) return;
+    uint32_t m = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) {
+        const uint32_t v = tmp[threadIdx.x * (NT / 64) + w];
+        m = v > m ? v : m;
+    }
+    uint32_t* slot = slots + threadIdx.x * kGatedSlots + id % kGatedSlots;
+    if (shared)
+        raise_slot(slot, m);
+    else
+        *slot = m;
+}
+__global__ __launch_bounds__(256) void k_clear_slots(uint32_t* slots) { slots[blockIdx.x * 256 + threadIdx.x] = 0; }
+
 // What is left of v when it is rounded to CT; nothing where that has no end.
 template <class CT>
 __device__ __forceinline__ float rest_of(float v) {
@@ -247,17 +328,28 @@ __device__ __forceinline__ float rest_of(float v) {
 // dg and du ([n][ldz], x's type) from the kept g and u, eight places a thread;
 // rows by blockIdx.y.  Bound by the bytes.  Rows of an f that is no multiple of 8
 // begin at any element: their pieces are loaded as they lie, and the last one by
-// elements.
-template <class CT, int ACT>
-__global__ __launch_bounds__(256) void k_gated_dz(const float* __restrict__ pre, const CT* __restrict__ dy, int64_t n, int64_t f,
-                                                  int64_t ldz, CT* __restrict__ dg, CT* __restrict__ du, int64_t rest) {
+// elements.  joined: 0 in the first launch, else its workgroups.
+template <int ELEM, int ACT>
+__global__ __launch_bounds__(256) void k_gated_dz(const float* __restrict__ pre, const Value<ELEM>* __restrict__ dy, int64_t n,
+                                                  int64_t f, int64_t ldz, Value<ELEM>* __restrict__ dg,
+                                                  Value<ELEM>* __restrict__ du, int64_t rest, uint32_t* __restrict__ slots,
+                                                  int joined, uint32_t* __restrict__ most) {
+    using CT = Value<ELEM>;
+    __shared__ uint32_t tmp[8];
     typedef float f32x8 __attribute__((ext_vector_type(8), aligned(4)));
     typedef CT ct8 __attribute__((ext_vector_type(8)));
     typedef CT ct8_any __attribute__((ext_vector_type(8), aligned(2)));
     const int64_t j = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-    if (j >= f) return;
     const int here = f - j < 8 ? static_cast<int>(f - j) : 8;
-    for (int64_t i = blockIdx.y; i < n; i += gridDim.y) {
+    float tg = 1.f, tu = 1.f;
+    if (ELEM == kF16 && joined) {
+        const uint2 m = join_slots<256>(slots, joined, (lds_u32*)tmp);
+        if (blockIdx.x + blockIdx.y + threadIdx.x == 0) most[0] = m.x, most[1] = m.y;
+        tg = held_times<ELEM>(m.x), tu = held_times<ELEM>(m.y);
+        if (tg == 1.f && tu == 1.f) return;
+    }
+    uint32_t mg = 0, mu = 0;
+    for (int64_t i = j < f ? blockIdx.y : n; i < n; i += gridDim.y) {
         f32x8 g = 0.f, u = 0.f;
         ct8_any d = 0;
         if (here == 8) {
@@ -273,7 +365,12 @@ __global__ __launch_bounds__(256) void k_gated_dz(const float* __restrict__ pre,
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float2 a = act::both<ACT, true>(g[e]);
-            const float de = static_cast<float>(d[e]), vg = de * u[e] * a.y, vu = de * a.x;
+            const float de = static_cast<float>(d[e]);
+            float vg = de * u[e] * a.y, vu = de * a.x;
+            if constexpr (ELEM == kF16) {
+                mg = larger(mg, vg), mu = larger(mu, vu);
+                vg *= tg, vu *= tu;
+            }
             zg[e] = static_cast<CT>(vg), zu[e] = static_cast<CT>(vu);
             rg[e] = static_cast<CT>(rest_of<CT>(vg)), ru[e] = static_cast<CT>(rest_of<CT>(vu));
         }
@@ -285,6 +382,10 @@ __global__ __launch_bounds__(256) void k_gated_dz(const float* __restrict__ pre,
             *reinterpret_cast<ct8*>(du + rest + i * ldz + j) = ru;
         }
     }
+    if constexpr (ELEM == kF16) {
+        if (joined) return;
+        leave_slots<256>(mg, mu, slots, blockIdx.y * gridDim.x + blockIdx.x, false, (lds_u32*)tmp);
+    }
 }
 
 // The same with g and u made again.
@@ -292,11 +393,22 @@ template <class C, int ACT>
 __global__ __launch_bounds__(C::NT) void k_gated_again_dz(Operand X, PairOperand W, int64_t kbytes,
                                                           const Value<C::ELEM>* __restrict__ dy, int64_t ldz,
                                                           Value<C::ELEM>* __restrict__ dg, Value<C::ELEM>* __restrict__ du,
-                                                          int64_t rest, Order order) {
+                                                          int64_t rest, uint32_t* __restrict__ slots, int joined,
+                                                          uint32_t* __restrict__ most, Order order) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
     int64_t tm, tn;
-    if (!order.at(blockIdx.x, &tm, &tn)) return;
+    if (!order.at(blockIdx.x, &tm, &tn)) {
+        if (C::ELEM == kF16 && !joined && gridDim.x <= kGatedSlots && threadIdx.x < 2) slots[threadIdx.x * kGatedSlots + blockIdx.x] = 0;
+        return;
+    }
+    float tg = 1.f, tu = 1.f;
+    if (C::ELEM == kF16 && joined) {
+        const uint2 m = join_slots<C::NT>(slots, joined, (lds_u32*)lds);
+        if (tm + tn + threadIdx.x == 0) most[0] = m.x, most[1] = m.y;
+        tg = held_times<C::ELEM>(m.x), tu = held_times<C::ELEM>(m.y);
+        if (tg == 1.f && tu == 1.f) return;
+    }
     f32x4 acc[C::BL][C::BR];
     tile_product<C>(acc, X, W, tm * C::TL, tn * (C::TR / 2), kbytes, lds);
     const Place<C> at(tm, tn);
@@ -304,6 +416,7 @@ __global__ __launch_bounds__(C::NT) void k_gated_again_dz(Operand X, PairOperand
     lds_f32* slice = (lds_f32*)(lds + at.wave * C::kSlice);
     const int64_t n = X.rows, f = W.rows;
     f32x4 z[H::BL][H::BR];
+    uint32_t mg = 0, mu = 0;
 #pragma unroll
     for (int x = 0; x < H::BL; ++x)
 #pragma unroll
@@ -314,10 +427,20 @@ __global__ __launch_bounds__(C::NT) void k_gated_again_dz(Operand X, PairOperand
                 const int64_t r = at.i0 + 16 * x + at.l16, j = at.f0 + 16 * b + 4 * at.g + i;
                 const float d = r < n && j < f ? static_cast<float>(dy[r * f + j]) : 0.f;
                 const float2 a = act::both<ACT, true>(acc[x][b][i]);
-                z[x][b][i] = d * acc[x][H::BR + b][i] * a.y;
-                acc[x][b][i] = d * a.x;
+                float vg = d * acc[x][H::BR + b][i] * a.y, vu = d * a.x;
+                if constexpr (C::ELEM == kF16) {
+                    if (r < n && j < f) mg = larger(mg, vg), mu = larger(mu, vu);
+                    vg *= tg, vu *= tu;
+                }
+                z[x][b][i] = vg;
+                acc[x][b][i] = vu;
             }
         }
+    if constexpr (C::ELEM == kF16) {
+        constexpr int kSlices = C::WL * C::WR * C::kSlice;  // the words are behind what the waves store from
+        static_assert(kSlices + 8 * C::NT / 64 <= C::kLds, "fits");
+        if (!joined) leave_slots<C::NT>(mg, mu, slots, blockIdx.x, gridDim.x > kGatedSlots, (lds_u32*)(lds + kSlices));
+    }
     // whole pieces: ldz is a multiple of 8, and what lies behind f is not used
     const auto same = [](float v) { return v; };
     const auto left = [](float v) { return rest_of<Value<C::ELEM>>(v); };
@@ -331,18 +454,18 @@ __global__ __launch_bounds__(C::NT) void k_gated_again_dz(Operand X, PairOperand
     if (rest) store_tile<H>(z, slice, du + rest, ldz, at.i0, at.f0, n, ldz, true, at.lane, left);
 }
 
-// Sums of part `part` of a product in fp32, or its result.
+// Sums of part `part` of a product in fp32, or its result; in fp16 times `by`.
 template <class C, class CT>
 __device__ __forceinline__ void store_result(const f32x4 (&acc)[C::BL][C::BR], lds_u8* lds, CT* c, float* sums, int64_t part,
-                                             int64_t rows, int64_t cols, int64_t tm, int64_t tn) {
+                                             int64_t rows, int64_t cols, int64_t tm, int64_t tn, float by) {
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int64_t i0 = tm * C::TL + wave / C::WR * C::BL * 16, j0 = tn * C::TR + wave % C::WR * C::BR * 16;
     lds_f32* slice = (lds_f32*)(lds + wave * C::kSlice);
-    const auto same = [](float v) { return v; };
+    const auto out = [&](float v) { return C::ELEM == kF16 ? v * by : v; };
     if (sums)
-        store_tile<C>(acc, slice, sums + part * rows * cols, cols, i0, j0, rows, cols, true, lane, same);
+        store_tile<C>(acc, slice, sums + part * rows * cols, cols, i0, j0, rows, cols, true, lane, out);
     else
-        store_tile<C>(acc, slice, c, cols, i0, j0, rows, cols, true, lane, same);
+        store_tile<C>(acc, slice, c, cols, i0, j0, rows, cols, true, lane, out);
 }
 
 // The columns [k0, k0 + kb) of bytes of the summed axis that part `part` has.
@@ -355,12 +478,12 @@ __device__ __forceinline__ int64_t part_of(int64_t kbytes, int64_t part_bytes, i
 
 // dx = dg Wg + du Wu, or the part blockIdx.y of its sum over f; TWO: over the
 // rests of dg and du too, `rest` bytes on.  (As a loop in the large tiles it
-// costs registers: dx of 4096 x 4096 from 8192 484 us, 563.)
+// costs registers: dx of 4096 x 4096 from 8192 484 us, 563.)  In fp16 the sum is
+// held times what du is; dg's part is brought there where dg is held otherwise.
 template <class C, bool TWO>
 __global__ __launch_bounds__(C::NT) void k_gated_dx(Operand Zg, Operand Zu, Operand Wg, Operand Wu, int64_t kbytes,
                                                     int64_t part_bytes, int64_t rest, Value<C::ELEM>* __restrict__ dx,
-                                                    float* __restrict__ sums,
-                                                    Order order) {
+                                                    float* __restrict__ sums, const uint32_t* __restrict__ most, Order order) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
     int64_t tm, tn, k0;
@@ -368,14 +491,27 @@ __global__ __launch_bounds__(C::NT) void k_gated_dx(Operand Zg, Operand Zu, Oper
     const int64_t kb = part_of(kbytes, part_bytes, blockIdx.y, &k0);
     Zg.data += k0, Zu.data += k0, Wg.data += k0 / 2 * Wg.ld, Wu.data += k0 / 2 * Wu.ld;
     f32x4 acc[C::BL][C::BR];
+    const auto bring = [&](int from, int to) {
+        if constexpr (C::ELEM == kF16) {
+            const float tf = held_times<C::ELEM>(most[from]), tt = held_times<C::ELEM>(most[to]);
+            if (tf == tt) return;
+#pragma unroll
+            for (int x = 0; x < C::BL; ++x)
+#pragma unroll
+                for (int y = 0; y < C::BR; ++y) acc[x][y] *= tt * inverse(tf);
+        }
+    };
     tile_product<C>(acc, Zg, Wg, tm * C::TL, tn * C::TR, kb, lds);
+    bring(0, 1);
     tile_product<C>(acc, Zu, Wu, tm * C::TL, tn * C::TR, kb, lds, true);
     if (TWO) {
         Zg.data += rest, Zu.data += rest;
+        bring(1, 0);
         tile_product<C>(acc, Zg, Wg, tm * C::TL, tn * C::TR, kb, lds, true);
+        bring(0, 1);
         tile_product<C>(acc, Zu, Wu, tm * C::TL, tn * C::TR, kb, lds, true);
     }
-    store_result<C>(acc, lds, dx, sums, blockIdx.y, Zg.rows, Wg.rows, tm, tn);
+    store_result<C>(acc, lds, dx, sums, blockIdx.y, Zg.rows, Wg.rows, tm, tn, inverse(C::ELEM == kF16 ? held_times<C::ELEM>(most[1]) : 1.f));
 }
 
 // dWg = dg^T x (blockIdx.z 0) and dWu = du^T x (1), or the part blockIdx.y of
@@ -383,7 +519,8 @@ __global__ __launch_bounds__(C::NT) void k_gated_dx(Operand Zg, Operand Zu, Oper
 template <class C, bool TWO>
 __global__ __launch_bounds__(C::NT) void k_gated_dw(Operand Zg, Operand Zu, Operand X, int64_t kbytes, int64_t part_bytes,
                                                     int64_t rest, Value<C::ELEM>* __restrict__ dwg,
-                                                    Value<C::ELEM>* __restrict__ dwu, float* __restrict__ sums, Order order) {
+                                                    Value<C::ELEM>* __restrict__ dwu, float* __restrict__ sums,
+                                                    const uint32_t* __restrict__ most, Order order) {
     __shared__ i32x4 lds_v[C::kLds / 16];
     lds_u8* lds = (lds_u8*)(reinterpret_cast<uint8_t*>(lds_v));
     int64_t tm, tn, k0;
@@ -398,7 +535,8 @@ __global__ __launch_bounds__(C::NT) void k_gated_dw(Operand Zg, Operand Zu, Oper
         Z.data += rest;
         tile_product<C>(acc, Z, X, tm * C::TL, tn * C::TR, kb, lds, true);
     }
-    store_result<C>(acc, lds, up ? dwu : dwg, sums, blockIdx.z * gridDim.y + blockIdx.y, Z.rows, X.rows, tm, tn);
+    store_result<C>(acc, lds, up ? dwu : dwg, sums, blockIdx.z * gridDim.y + blockIdx.y, Z.rows, X.rows, tm, tn,
+                    inverse(C::ELEM == kF16 ? held_times<C::ELEM>(most[up ? 1 : 0]) : 1.f));
 }
 
 // A result from the fp32 sums of its parts, eight values a thread, the loads of
@@ -519,24 +657,38 @@ hipError_t backward(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
     auto* dg = reinterpret_cast<CT*>(ws + p.dg);
     auto* du = reinterpret_cast<CT*>(ws + p.du);
     auto* sums = reinterpret_cast<float*>(ws + p.sums);
+    auto* most = reinterpret_cast<uint32_t*>(ws + p.slots);
+    auto* slots = most + 64;
     const int64_t ldz = p.ldz;
-    hipError_t e = by_act(j.act, [&](auto a) {
-        constexpr int ACT = decltype(a)::value;
-        if (j.pre) {
-            const dim3 grid(blocks_of(j.f, 2048), static_cast<unsigned>(j.n < 16384 ? j.n : 16384));
-            hipLaunchKernelGGL((k_gated_dz<CT, ACT>), grid, dim3(256), 0, stream, j.pre, static_cast<const CT*>(j.dy), j.n, j.f,
-                               ldz, dg, du, p.rest / 2);
-            return hipGetLastError();
-        }
-        return by_gated_tile<ELEM>(gated_tile(j.n, j.f), [&](auto cfg) {
-            using C = decltype(cfg);
-            const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.f + C::TR / 2 - 1) / (C::TR / 2);
-            const Order order = Order::make(tm, tn, 1);
-            hipLaunchKernelGGL((k_gated_again_dz<C, ACT>), dim3(order.grid()), dim3(C::NT), 0, stream, operand(j.x, j.k, j.n),
-                               pair_operand(j), 2 * j.k, static_cast<const CT*>(j.dy), ldz, dg, du, p.rest / 2, order);
-            return hipGetLastError();
+    // joined: the first launch's slots, which it leaves here
+    const auto make_dz = [&](int* joined) {
+        return by_act(j.act, [&](auto a) {
+            constexpr int ACT = decltype(a)::value;
+            if (j.pre) {
+                const int64_t across = blocks_of(j.f, 2048), down = ELEM == kF16 ? kGatedSlots / across : 16384;
+                const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>(j.n < down ? j.n : down));
+                hipLaunchKernelGGL((k_gated_dz<ELEM, ACT>), grid, dim3(256), 0, stream, j.pre, static_cast<const CT*>(j.dy), j.n, j.f,
+                                   ldz, dg, du, p.rest / 2, slots, *joined, most);
+                *joined = static_cast<int>(grid.x * grid.y);
+                return hipGetLastError();
+            }
+            return by_gated_tile<ELEM>(gated_tile(j.n, j.f), [&](auto cfg) {
+                using C = decltype(cfg);
+                const int64_t tm = (j.n + C::TL - 1) / C::TL, tn = (j.f + C::TR / 2 - 1) / (C::TR / 2);
+                const Order order = Order::make(tm, tn, 1);
+                if (ELEM == kF16 && !*joined && order.grid() > kGatedSlots)
+                    hipLaunchKernelGGL(k_clear_slots, dim3(2 * kGatedSlots / 256), dim3(256), 0, stream, slots);
+                hipLaunchKernelGGL((k_gated_again_dz<C, ACT>), dim3(order.grid()), dim3(C::NT), 0, stream, operand(j.x, j.k, j.n),
+                                   pair_operand(j), 2 * j.k, static_cast<const CT*>(j.dy), ldz, dg, du, p.rest / 2, slots, *joined,
+                                   most, order);
+                *joined = order.grid() < kGatedSlots ? static_cast<int>(order.grid()) : kGatedSlots;
+                return hipGetLastError();
+            });
         });
-    });
+    };
+    int joined = 0;
+    hipError_t e = make_dz(&joined);
+    if (e == hipSuccess && ELEM == kF16) e = make_dz(&joined);
     const auto join = [&](const float* from, int64_t parts, int64_t values, void* out) {
         hipLaunchKernelGGL(k_join_parts<CT>, dim3(blocks_of(values / 8, 256)), dim3(256), 0, stream, from, static_cast<int>(parts),
                            values / 8, static_cast<CT*>(out));
@@ -550,7 +702,8 @@ hipError_t backward(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
             const int64_t part_bytes = ((2 * j.f + 127) / 128 + p.dx_parts - 1) / p.dx_parts * 128;
             hipLaunchKernelGGL((k_gated_dx<C, decltype(two)::value>), dim3(order.grid(), static_cast<unsigned>(p.dx_parts)), dim3(C::NT), 0, stream,
                                operand(dg, ldz, j.n), operand(du, ldz, j.n), operand(j.wg, j.k, j.k), operand(j.wu, j.k, j.k),
-                               2 * j.f, part_bytes, p.rest, static_cast<CT*>(j.dx), p.dx_parts > 1 ? sums : nullptr, order);
+                               2 * j.f, part_bytes, p.rest, static_cast<CT*>(j.dx), p.dx_parts > 1 ? sums : nullptr, most,
+                               order);
             return hipGetLastError();
         });
         if (e == hipSuccess && p.dx_parts > 1) e = join(sums, p.dx_parts, j.n * j.k, j.dx);
@@ -564,7 +717,8 @@ hipError_t backward(const GatedJob& j, const GatedPlan& p, hipStream_t stream) {
             const int64_t part_bytes = ((2 * j.n + 127) / 128 + p.dw_parts - 1) / p.dw_parts * 128;
             hipLaunchKernelGGL((k_gated_dw<C, decltype(two)::value>), dim3(order.grid(), static_cast<unsigned>(p.dw_parts), both), dim3(C::NT), 0, stream,
                                operand(dg, ldz, j.f), operand(du, ldz, j.f), operand(j.x, j.k, j.k), 2 * j.n, part_bytes,
-                               p.rest, static_cast<CT*>(j.dwg), static_cast<CT*>(j.dwu), p.dw_parts > 1 ? sums : nullptr, order);
+                               p.rest, static_cast<CT*>(j.dwg), static_cast<CT*>(j.dwu), p.dw_parts > 1 ? sums : nullptr, most,
+                               order);
             return hipGetLastError();
         });
         if (p.dw_parts > 1) {

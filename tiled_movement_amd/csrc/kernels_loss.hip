@@ -288,12 +288,6 @@ __global__ void k_clear_slots(uint32_t* slots) {
     if (threadIdx.x < kSlots) slots[threadIdx.x] = 0;
 }
 
-// Raises a slot to a magnitude's bits if that is finite and more than it holds.
-__device__ __forceinline__ void raise_slot(uint32_t* slot, uint32_t bits) {
-    if (bits < 0x7f800000u && bits > __hip_atomic_load(slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(slot, bits);
-}
-__device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
 // g_i tau as f 2^s times the largest of them (its bits), 1/2 < |f| <= 1 and
 // s <= 0.  0, and what is not finite, is its own f.
 struct RowScale {

@@ -55,9 +55,11 @@ enum class ProductTile { k64x64, k64x256, k128x128, k128x256, k256x256 };
 inline bool gated_two_terms(int64_t n, int64_t f, int64_t k) { return n * f <= (int64_t(1) << 23) / k; }
 // Workspace of the gradient: byte offsets, the pitch of dg and du in elements,
 // and for the products their tiles and the parts that their sums are split into.
-// `rest` is from dg to its rest, and from du to its; 0: none are held.
+// `rest` is from dg to its rest, and from du to its; 0: none are held.  slots: an
+// fp16 call's magnitudes of dg and du, joined (256 bytes), then by workgroups.
+constexpr int kGatedSlots = 2048;
 struct GatedPlan {
-    int64_t dg, du, rest, sums, bytes;
+    int64_t dg, du, rest, slots, sums, bytes;
     int64_t ldz, dx_parts, dw_parts;
     ProductTile dx_tile, dw_tile;
 };

@@ -122,6 +122,12 @@ __device__ __forceinline__ void wg_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// Raises a slot to a magnitude's bits if that is finite and more than it holds.
+__device__ __forceinline__ void raise_slot(uint32_t* slot, uint32_t bits) {
+    if (bits < 0x7f800000u && bits > __hip_atomic_load(slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(slot, bits);
+}
+__device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
 // Which tile a workgroup takes, in a grid of f x s tiles (f: the direction
 // that neighbours step along).  Workgroups go to the eight XCDs in turn, and
 // the 32 of an XCD that run at once share its L2: the fewer rows and columns of
