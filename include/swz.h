@@ -614,8 +614,8 @@ int swz_gated(const void* d_x, const void* d_wg, const void* d_wu, int32_t x_typ
 /* Host only.  Bytes of workspace of the gradient call: 256-byte aligned device
  * memory that carries nothing from one call to the next; calls that may run at
  * the same time (on two streams, in two graphs) need one each.  It holds dg and
- * du (2 bytes each a place of y; 4 where n f k is up to 2^23) and, where a gradient has few tiles, fp32 sums
- * of its parts.
+ * du (2 bytes each a place of y; 4 where n f k is up to 2^23), 16 KiB, and, where
+ * a gradient has few tiles, fp32 sums of its parts.
  * Errors: as swz_gated. */
 int swz_gated_workspace(int64_t n, int64_t f, int64_t k, int64_t* bytes);
 
@@ -625,12 +625,15 @@ int swz_gated_workspace(int64_t n, int64_t f, int64_t k, int64_t* bytes);
  * all x_type, overwritten, 16-byte aligned; each may be NULL (not all).
  *   d_pre    : what swz_gated wrote there, or NULL: g and u are made again, for
  *              4 n f k operations more.
- * dg and du are rounded to x_type once (as they are where a program holds them;
- * with fp16, values beyond its range are infinite or lose digits, as gradients
- * of that type do), and for n f k up to 2^23, where few values would leave the
+ * dg and du are rounded to x_type once (as they are where a program holds
+ * them), and for n f k up to 2^23, where few values would leave the
  * results up to 1.8 times the error of their own rounding, what that rounding
- * left is held too; sums are fp32 and rounded to x_type at the end.  n = 0
- * writes zero dwg and dwu.  Results do not depend on the order of anything:
+ * left is held too.  With fp16 both are held times a power of two of their own
+ * where the call's largest finite value of one is beyond the type's range or
+ * below 2^-4: a value of 2^-10 of the largest and more keeps all its digits, and a
+ * smaller one is off by at most 2^-21 of the largest.
+ * Sums are fp32 and rounded to x_type at the end.  n = 0 writes zero dwg and
+ * dwu.  Results do not depend on the order of anything:
  * the same call gives the same bits.
  * Errors: as swz_gated, and SWZ_EINVAL for a workspace below
  * swz_gated_workspace. */
