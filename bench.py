@@ -7,7 +7,10 @@ before timing; the calls rotate over enough source/destination pairs
 (>= 512 MiB) that the 256 MB Infinity Cache cannot hold the working set, so
 traffic reaches HBM.
 
-Prints ONE JSON line.  Extra fields: the other workloads and layouts
+Prints ONE JSON line of a few kilobytes; its `extra` holds one rate per
+workload and layout (GB/s, TFLOP/s of products, us a call of map), and the
+whole records (shapes, parameters, counters) go to the file of --record.
+Extra fields: the other workloads and layouts
 (swizzle / pad / plain / direct), the library's reference copy of the same
 bytes (the practical read-once / write-once ceiling; it copies the
 workloads' own random bytes, since an all-zero buffer copies about 4%
@@ -17,7 +20,7 @@ sources), and the CPU oracle timed on every workload as a reported
 baseline, each checked bit for bit against the GPU result.
 
 Usage:
-  python bench.py [--gpus 1] [--steps K] [--warmup W] [--quick]
+  python bench.py [--gpus 1] [--steps K] [--warmup W] [--quick] [--record FILE]
   python bench.py --workload NAME --layout swizzle|pad|plain|direct [--steps K] [--pairs P]
       time one workload only (used for profiler runs), optionally rotating over
       exactly P buffer pairs; NAME is one of
@@ -102,6 +105,20 @@ def code_text(src):
     src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
     src = re.sub(r"//[^\n]*", "", src)
     return "\n".join(ln.rstrip() for ln in src.splitlines() if ln.strip())
+
+
+RATES = ("GBps", "TFLOPs", "us_per_call", "GBps_tuned_order", "value")
+
+
+def short(line):
+    """The JSON line with each of `extra`'s records cut to its rate (the first of RATES that it has): whole, the line is
+    longer than what is kept of a program's output in some places, and so lost altogether."""
+
+    def rate(rec):
+        found = [rec[k] for k in RATES if k in rec]
+        return found[0] if found else {k: rate(v) for k, v in rec.items()}
+
+    return {**line, "extra": {k: rate(v) for k, v in line["extra"].items()}}
 
 
 def kernel_sources_digest():
@@ -741,6 +758,7 @@ def main(argv=None):
                     help="every tile order and the default order on many shapes, as shares of a copy")
     ap.add_argument("--random-shapes", type=int, default=0,
                     help="AUTO transposes of this many seeded random shapes, as shares of a copy")
+    ap.add_argument("--record", default=None, help="write the whole records of everything measured to this file (JSON)")
     args = ap.parse_args(argv)
     global PAIRS_OVERRIDE
     PAIRS_OVERRIDE = args.pairs
@@ -897,7 +915,10 @@ def main(argv=None):
         line["roofline"] = {"bound": "mfma", "achieved": round(tflops, 1), "peak": MFMA_BF16_PEAK_TFLOPS,
                             "unit": "TFLOP/s", "frac": round(tflops / MFMA_BF16_PEAK_TFLOPS, 4), "traffic": None,
                             "algorithmic_flops_per_launch": nbytes}
-    print(json.dumps(line), flush=True)
+    if args.record:
+        with open(args.record, "w") as f:
+            json.dump(line, f)
+    print(json.dumps(short(line)), flush=True)
     return 0
 
 

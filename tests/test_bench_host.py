@@ -89,3 +89,24 @@ def test_source_digest_follows_code_not_comments():
     assert bench.code_text(src) == bench.code_text(src.replace("// one", "// changed").replace("two", "other"))
     assert bench.code_text(src) == "int f(int x) {\n   return x ^ 3;\n}"
     assert bench.code_text(src) != bench.code_text(src.replace("x ^ 3", "x ^ 5"))
+
+
+def test_the_line_stays_short_whatever_is_measured():
+    """One rate a workload and layout on stdout; shapes, parameters and counters only in --record's file."""
+    rec = {"layout": "swizzle", "shape": [1, 8192, 8192], "elem_bytes": 4, "params": [5, 0, 5], "pad_elems": 0, "lds_bytes": 4096,
+           "threads": 256, "buffer_pairs": 4, "predicted_conflict_cycles_per_tile": {"write": 96, "read": 992}, "GBps": 3977.1,
+           "frac": 0.4971, "us_per_step": 33.75, "frac_of_copy": 0.6548, "measured_conflict_cycles_per_tile": 1088.0}
+    cpu = {"value": 13.8, "unit": "GB/s", "cores": 16, "sample": "x" * 120, "matches_gpu": True}
+    extra = {f"{w}/{lay}": dict(rec) for w in bench.WORKLOADS for lay in ("swizzle", "pad", "plain", "direct")}
+    extra.update({"map/swizzle": {"us_per_call": 1.9, "batch_us_per_125_triples": 6.5}, "torch_mm_bf16": {"TFLOPs": 1311.7, "m": 8192},
+                  "fp32_transpose_long/swizzle": {"shape": [1, 8192, 2048], "GBps_default_order": 4700.0, "GBps_tuned_order": 5790.0},
+                  "cpu_baseline": {w: dict(cpu) for w in bench.ORACLE_TIMED}})
+    line = {"metric": bench.METRIC, "value": 5669.2, "config": {"workload": bench.WORKLOADS["fp32_transpose"]}, "cpu_baseline": cpu,
+            "extra": extra}
+    out = bench.short(line)
+    assert len(json.dumps(line)) > 16000 > 4 * len(json.dumps(out))
+    assert {k: v for k, v in out.items() if k != "extra"} == {k: v for k, v in line.items() if k != "extra"}
+    assert out["extra"]["fp32_transpose/plain"] == 3977.1 and out["extra"]["torch_mm_bf16"] == 1311.7
+    assert out["extra"]["map/swizzle"] == 1.9 and out["extra"]["fp32_transpose_long/swizzle"] == 5790.0
+    assert set(out["extra"]["cpu_baseline"].values()) == {13.8} and line["extra"]["fp32_transpose/plain"] == rec
+    assert bench.short({"extra": {}}) == {"extra": {}}
