@@ -241,13 +241,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(const uint8_t* __r
 // What a call holds dg (du) times, from the bits of its largest finite magnitude m.
 // 1 in bf16, whose range is fp32's.  In fp16 1 where m is 2^-4 to below 65520:
 // it rounds to a number, and what is 2^-10 of it still has all its digits; else
-// the power of two that brings m to 2^14 .. 2^15, but 2^40 at most.
+// the power of two that brings m to 2^14 .. 2^15, but 2^64 at most (a sum of 2^22
+// products of 2^16 by what lies below 2^-64 rounds to zero in fp16).
 template <int ELEM>
 __device__ __forceinline__ float held_times(uint32_t bits) {
     if constexpr (ELEM != kF16) return 1.f;
     if (bits == 0 || (bits >= 0x3d800000u && bits < 0x477ff000u)) return 1.f;
     const int e = 141 - static_cast<int>(bits >> 23);
-    return __uint_as_float(static_cast<uint32_t>(127 + (e < 40 ? e : 40)) << 23);
+    return __uint_as_float(static_cast<uint32_t>(127 + (e < 64 ? e : 64)) << 23);
 }
 // 1 / v of a power of two.
 __device__ __forceinline__ float inverse(float v) { return __uint_as_float((254u << 23) - __float_as_uint(v)); }
